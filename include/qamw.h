@@ -398,6 +398,92 @@ int32_t qamw_decode_matmul(const uint16_t* Xr_bf16, int64_t T, int64_t d, int64_
                            const float* sigma, const float* codebook, int32_t K,
                            void* Y, int32_t ydtype, int64_t ldy, void* stream);
 
+/*
+ * Microscaled 4-bit floating point, the 4-bit weight format that the matrix
+ * cores multiply directly: to compare the codec with, and to run layers in.
+ * A row is cut into blocks of 32 consecutive elements; the last block of a
+ * row may be short.  With m the block's largest |v|,
+ *     e     = max(floor(log2 m) - 2, -127)   (m = 0: e = -127)
+ *     scale = the byte e + 127; 255 if the block holds an infinity or a NaN
+ *     code  = sign and v 2^-e rounded to nearest, ties to even, among
+ *             {0, 1/2, 1, 3/2, 2, 3, 4, 6}, beyond 6 to 6: 4 bits, the sign
+ *             in bit 3 and the magnitude's place in this list in bits 0 to 2
+ *     value = +-magnitude 2^e; NaN throughout a block of scale 255 (the
+ *             codes of such a block are written as 0)
+ *
+ *   codes   [N][qamw_mxfp4_row_bytes(d)] uint8: element j in byte j / 2, the
+ *           even one in the low half; 16 bytes per block, the elements past
+ *           d as 0
+ *   scales  [N][qamw_mxfp4_scale_bytes(d)] uint8: one per block, padded with
+ *           0 to a multiple of 16
+ * Any d in [1, 2^20] and any leading dimension >= d; matrices and their rows
+ * need only their elements' alignment here (16-byte aligned rows are faster).
+ * codes and scales are 16-byte aligned.  N = 0 and T = 0 are valid and do
+ * nothing.  dtypes: QAMW_F32, QAMW_BF16 or QAMW_F16 unless said otherwise.
+ *
+ * qamw_mxfp4_quantize: W [N][ldw] -> codes, scales and, if values is not
+ *   NULL, the values they stand for, [N][ldv] of vdtype (the W_hat that
+ *   qamw_output_error takes), rounded to nearest even where vdtype cannot
+ *   hold them.
+ * qamw_mxfp4_dequantize: codes, scales -> W_out [N][ldo] of out_dtype, the
+ *   same values.
+ * qamw_mxfp4_matmul: Y[t][n] = sum_j X^[t][j] W^[n][j], W^ the values of
+ *   codes and scales and X^ those of X [T][ldx], which the call quantises by
+ *   the rule above.  Y [T][ldy] of ydtype (QAMW_F32 or QAMW_BF16).  Products
+ *   are exact and summed in fp32, in a fixed order.  A row of W or X with a
+ *   NaN block gives NaN.  To multiply with rotated operands, rotate X with
+ *   qamw_rotate_activations and the weight's rows with the same call before
+ *   quantising them.
+ *   workspace >= qamw_mxfp4_matmul_workspace_bytes(T, N, d), 256-byte aligned
+ */
+int64_t qamw_mxfp4_row_bytes(int64_t d);     /* -1 for d outside [1, 2^20] */
+int64_t qamw_mxfp4_scale_bytes(int64_t d);
+int32_t qamw_mxfp4_quantize(const void* W, int32_t wdtype, int64_t N, int64_t d, int64_t ldw, uint8_t* codes,
+                            uint8_t* scales, void* values, int32_t vdtype, int64_t ldv, void* stream);
+int32_t qamw_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t d, void* W_out,
+                              int32_t out_dtype, int64_t ldo, void* stream);
+size_t qamw_mxfp4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
+int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, int64_t ldx, const uint8_t* codes,
+                          const uint8_t* scales, int64_t N, void* Y, int32_t ydtype, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Softmax cross entropy of a language model's last hidden states against its
+ * vocabulary head, and the gradient (QAM-W, Experiments: the codec is judged
+ * by what it does to the model's loss).  The T x V logits are never stored.
+ *     z_tv   = sum_j H[t][j] W[v][j]
+ *     lse_t  = log sum_v exp z_tv,   loss_t = lse_t - z_{t, targets[t]}
+ *     G_tv   = dloss_t (exp(z_tv - lse_t) - [v = targets[t]])
+ *     dH     = G W,   dW = G^T H
+ * A token whose target is outside [0, V) (-100, say) is not counted: loss 0,
+ * a zero row of dH, and nothing of its hidden state (which may be NaN) or of
+ * its dloss in dW; its lse is still written.
+ *   H        [T][ldh], W [V][ldw], both of dtype QAMW_F32 or QAMW_BF16, with
+ *            16-byte aligned rows; d a multiple of 8
+ *   targets  [T] int64
+ *   loss, lse, dloss  [T] float32
+ *   dH       [T][lddh] and dW [V][lddw] of the same dtype, 16-byte aligned
+ *            rows; either may be NULL and is then not computed
+ *   lse      (gradient) as qamw_cross_entropy wrote it for these inputs
+ * Arithmetic: products of the inputs as they are, summed in fp32 on matrix
+ * cores; statistics in fp32.  For bf16 inputs G is rounded to bf16 before it
+ * is multiplied; dH and dW are summed in fp32 and rounded once.  All sums have
+ * a fixed order.  T = 0 is valid (dW is then written as 0).  Rows of H, W and
+ * of a T-element row of dtype must be under 4 MiB (T <= 2^20 for fp32).
+ *   workspace >= qamw_cross_entropy_workspace_bytes(T, V, d, dtype) or
+ *             qamw_cross_entropy_grad_workspace_bytes(T, V, d, dtype) bytes,
+ *             256-byte aligned
+ */
+size_t qamw_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype);
+int32_t qamw_cross_entropy(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W, int64_t V,
+                           int64_t ldw, const int64_t* targets, float* loss, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t qamw_cross_entropy_grad_workspace_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype);
+int32_t qamw_cross_entropy_grad(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W,
+                                int64_t V, int64_t ldw, const int64_t* targets, const float* lse, const float* dloss,
+                                void* dH, int64_t lddh, void* dW, int64_t lddw, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

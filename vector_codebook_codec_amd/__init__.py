@@ -3,7 +3,8 @@
 The codec's work runs in hand-written HIP kernels behind the C ABI of
 include/qamw.h (libqamw.so, built in-tree by ``_build.build()``).  This
 package binds that ABI for torch device tensors; see ``codec`` for the entry
-points ``qamw_calibrate``, ``qamw_encode`` and ``qamw_decode``.
+points ``qamw_calibrate``, ``qamw_encode`` and ``qamw_decode``, ``mxfp4`` for
+the microscaled 4-bit format, and ``cross_entropy`` for the model's loss.
 """
 from .codec import (  # noqa: F401
     load_codebook,
@@ -33,6 +34,20 @@ from .codec import (  # noqa: F401
     qamw_packed_row_words,
     qamw_plan_bytes,
     qamw_rotate_activations,
+)
+from .cross_entropy import (  # noqa: F401
+    qamw_cross_entropy,
+    qamw_cross_entropy_grad,
+    qamw_cross_entropy_grad_workspace_bytes,
+    qamw_cross_entropy_workspace_bytes,
+)
+from .mxfp4 import (  # noqa: F401
+    qamw_mxfp4_dequantize,
+    qamw_mxfp4_matmul,
+    qamw_mxfp4_matmul_workspace_bytes,
+    qamw_mxfp4_quantize,
+    qamw_mxfp4_row_bytes,
+    qamw_mxfp4_scale_bytes,
 )
 
 __version__ = "0.1.0"

@@ -51,6 +51,17 @@ SIGNATURES = {
                                  _p]),
     "qamw_rotate_activations": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i32, _u64, _p, _i64, _p]),
     "qamw_decode_matmul": (_i32, [_p, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _i32, _p, _i32, _i64, _p]),
+    "qamw_mxfp4_row_bytes": (_i64, [_i64]),
+    "qamw_mxfp4_scale_bytes": (_i64, [_i64]),
+    "qamw_mxfp4_quantize": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _i32, _i64, _p]),
+    "qamw_mxfp4_dequantize": (_i32, [_p, _p, _i64, _i64, _p, _i32, _i64, _p]),
+    "qamw_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "qamw_mxfp4_matmul": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _i64, _p, _i32, _i64, _p, _sz, _p]),
+    "qamw_cross_entropy_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "qamw_cross_entropy": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _sz, _p]),
+    "qamw_cross_entropy_grad_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "qamw_cross_entropy_grad": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p,
+                                       _sz, _p]),
     "qamw_decode": (_i32, [_p, _p, _i64, _i64, _p, _p, _i32, _u64, _p, _i32, _p, _i32, _i64, _p]),
 }
 

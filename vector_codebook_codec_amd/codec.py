@@ -82,6 +82,16 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _temporary(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace that the caller does not see: kept from reuse until `stream`, where that is not the current one,
+    has passed the call."""
+    t = _workspace(nbytes, device)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                        else torch.cuda.ExternalStream(_stream(stream), device=device))
+    return t
+
+
 def load_codebook(K: int) -> np.ndarray:
     """The stored K x 2 float32 codebook (2D Lloyd-Max, unit circular Gaussian)."""
     path = os.path.join(CODEBOOK_DIR, f"qamw_K{K}.f32")

@@ -600,4 +600,137 @@ int32_t qamw_decode_matmul(const uint16_t* Xr_bf16, int64_t T, int64_t d, int64_
                               K, B, Y, ydtype, ldy, (hipStream_t)stream);
 }
 
+// ---------------- microscaled 4-bit floating point ----------------
+constexpr int64_t kMx4MaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+
+int64_t qamw_mxfp4_row_bytes(int64_t d) { return d >= 1 && d <= kMx4MaxDim ? mx4_blocks(d) * 16 : -1; }
+int64_t qamw_mxfp4_scale_bytes(int64_t d) { return d >= 1 && d <= kMx4MaxDim ? mx4_scale_bytes(d) : -1; }
+
+static int check_mx4(int64_t N, int64_t d, const void* codes, const void* scales) {
+  if (N < 0 || d <= 0) return fail(QAMW_EINVAL, "sizes must not be negative and d positive (rows %lld, d=%lld)", (long long)N, (long long)d);
+  if (N > kMaxRows || d > kMx4MaxDim) return fail(QAMW_EUNSUPPORTED, "matrix too large (rows %lld, d=%lld)", (long long)N, (long long)d);
+  if (N && (!codes || !scales || !aligned16(codes) || !aligned16(scales)))
+    return fail(QAMW_EINVAL, "codes and scales must be non-NULL and 16-byte aligned");
+  return QAMW_OK;
+}
+// a matrix of any leading dimension, aligned to its elements
+static int check_plain_rows(const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld, const char* name, bool f16) {
+  if (dt != QAMW_F32 && dt != QAMW_BF16 && !(f16 && dt == QAMW_F16))
+    return fail(QAMW_EUNSUPPORTED, "%s dtype %d not supported", name, dt);
+  if (ld < cols) return fail(QAMW_EINVAL, "%s: leading dimension %lld < %lld", name, (long long)ld, (long long)cols);
+  if (rows && (!p || (uintptr_t)p % (uintptr_t)elem_size(dt)))
+    return fail(QAMW_EINVAL, "%s must be non-NULL and aligned to its elements", name);
+  return QAMW_OK;
+}
+
+int32_t qamw_mxfp4_quantize(const void* W, int32_t wdtype, int64_t N, int64_t d, int64_t ldw, uint8_t* codes,
+                            uint8_t* scales, void* values, int32_t vdtype, int64_t ldv, void* stream) {
+  int rc = check_mx4(N, d, codes, scales);
+  if (rc) return rc;
+  if ((rc = check_plain_rows(W, wdtype, N, d, ldw, "W", true))) return rc;
+  if (values && (rc = check_plain_rows(values, vdtype, N, d, ldv, "values", true))) return rc;
+  if (N == 0) return QAMW_OK;
+  return launch_mx4_quantize(W, wdtype, N, (int)d, ldw, codes, scales, values, values ? vdtype : QAMW_BF16, ldv,
+                             (hipStream_t)stream);
+}
+
+int32_t qamw_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N, int64_t d, void* W_out,
+                              int32_t out_dtype, int64_t ldo, void* stream) {
+  int rc = check_mx4(N, d, codes, scales);
+  if (rc) return rc;
+  if ((rc = check_plain_rows(W_out, out_dtype, N, d, ldo, "W_out", true))) return rc;
+  if (N == 0) return QAMW_OK;
+  return launch_mx4_dequantize(codes, scales, N, (int)d, W_out, out_dtype, ldo, (hipStream_t)stream);
+}
+
+size_t qamw_mxfp4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) {
+  if (T <= 0 || T > kMaxRows || N <= 0 || N > kMaxRows || d <= 0 || d > kMx4MaxDim) return 0;
+  return round_up((size_t)T * (size_t)mx4_blocks(d) * 16, 256) + round_up((size_t)T * (size_t)mx4_scale_bytes(d), 256);
+}
+
+int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, int64_t ldx, const uint8_t* codes,
+                          const uint8_t* scales, int64_t N, void* Y, int32_t ydtype, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  int rc = check_mx4(N, d, codes, scales);
+  if (rc) return rc;
+  if (T < 0) return fail(QAMW_EINVAL, "T must not be negative (T=%lld)", (long long)T);
+  if (T > kMaxRows || ((T + 15) / 16) * ((N + 15) / 16) >= kMaxRows) return fail(QAMW_EUNSUPPORTED, "product too large");
+  if ((rc = check_plain_rows(X, xdtype, T, d, ldx, "X", true))) return rc;
+  if ((rc = check_plain_rows(Y, ydtype, N ? T : 0, N, ldy, "Y", false))) return rc;
+  if (T == 0 || N == 0) return QAMW_OK;
+  const size_t need = qamw_mxfp4_matmul_workspace_bytes(T, N, d);
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))
+    return fail(QAMW_EWORKSPACE, "the 4-bit product needs %zu bytes of 256-byte aligned workspace (got %zu)", need,
+                workspace_bytes);
+  return launch_mx4_matmul(X, xdtype, T, (int)d, ldx, codes, scales, N, Y, ydtype, ldy, workspace, (hipStream_t)stream);
+}
+
+// ---------------- vocabulary cross entropy ----------------
+// sizes that the kernels' 32-bit offsets inside a tile and their grids can hold
+static bool ce_sizes_fit(int64_t T, int64_t V, int64_t d, int32_t dtype) {
+  const int es = elem_size(dtype);
+  return T <= kMaxDim && V <= kMaxDim && d * es < kMaxRowBytes && T * es < kMaxRowBytes &&
+         ((T + 127) / 128) * ((V + 127) / 128) < kMaxRows;
+}
+static int check_ce(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
+                    const int64_t* targets) {
+  if (T < 0 || V <= 0 || d <= 0)
+    return fail(QAMW_EINVAL, "V and d must be positive and T not negative (T=%lld V=%lld d=%lld)", (long long)T,
+                (long long)V, (long long)d);
+  if (dtype != QAMW_F32 && dtype != QAMW_BF16) return fail(QAMW_EUNSUPPORTED, "dtype %d not supported", dtype);
+  if (d % 8) return fail(QAMW_EINVAL, "d=%lld is not a multiple of 8", (long long)d);
+  if (!ce_sizes_fit(T, V, d, dtype)) return fail(QAMW_EUNSUPPORTED, "operands too large");
+  int rc;
+  if (T && (rc = check_rows16(H, dtype, d, ldh, "H", false))) return rc;
+  if ((rc = check_rows16(W, dtype, d, ldw, "W", false))) return rc;
+  if (ldh * elem_size(dtype) > kMaxRowBytes || ldw * elem_size(dtype) > kMaxRowBytes)
+    return fail(QAMW_EUNSUPPORTED, "leading dimension too large");
+  if (T && (!targets || ((uintptr_t)targets & 7u))) return fail(QAMW_EINVAL, "targets must be non-NULL and 8-byte aligned");
+  return QAMW_OK;
+}
+static bool aligned4(const void* p) { return p && ((uintptr_t)p & 3u) == 0; }
+
+size_t qamw_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype) {
+  if (T <= 0 || V <= 0 || d <= 0 || (dtype != QAMW_F32 && dtype != QAMW_BF16) || !ce_sizes_fit(T, V, d, dtype)) return 0;
+  return ce_workspace_bytes(T, V);
+}
+size_t qamw_cross_entropy_grad_workspace_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype) {
+  if (T <= 0 || V <= 0 || d <= 0 || (dtype != QAMW_F32 && dtype != QAMW_BF16) || !ce_sizes_fit(T, V, d, dtype)) return 0;
+  return ce_grad_workspace_bytes(T, V, (int)d, dtype);
+}
+
+int32_t qamw_cross_entropy(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W, int64_t V,
+                           int64_t ldw, const int64_t* targets, float* loss, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int rc = check_ce(H, dtype, T, d, ldh, W, V, ldw, targets);
+  if (rc) return rc;
+  if (T == 0) return QAMW_OK;
+  if (!aligned4(loss) || !aligned4(lse)) return fail(QAMW_EINVAL, "loss and lse must be non-NULL and 4-byte aligned");
+  const size_t need = qamw_cross_entropy_workspace_bytes(T, V, d, dtype);
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))
+    return fail(QAMW_EWORKSPACE, "the cross entropy needs %zu bytes of 256-byte aligned workspace (got %zu)", need,
+                workspace_bytes);
+  return launch_cross_entropy(H, dtype, T, (int)d, ldh, W, V, ldw, targets, loss, lse, workspace, (hipStream_t)stream);
+}
+
+int32_t qamw_cross_entropy_grad(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W,
+                                int64_t V, int64_t ldw, const int64_t* targets, const float* lse, const float* dloss,
+                                void* dH, int64_t lddh, void* dW, int64_t lddw, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  int rc = check_ce(H, dtype, T, d, ldh, W, V, ldw, targets);
+  if (rc) return rc;
+  if (T && dH && (rc = check_rows16(dH, dtype, d, lddh, "dH", false))) return rc;
+  if (dW && (rc = check_rows16(dW, dtype, d, lddw, "dW", false))) return rc;
+  if (T == 0) return dW ? launch_zero_rows(dW, dtype, V, (int)d, lddw, (hipStream_t)stream) : QAMW_OK;
+  if (!aligned4(lse) || !aligned4(dloss)) return fail(QAMW_EINVAL, "lse and dloss must be non-NULL and 4-byte aligned");
+  if (!dH && !dW) return QAMW_OK;
+  const size_t need = qamw_cross_entropy_grad_workspace_bytes(T, V, d, dtype);
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))
+    return fail(QAMW_EWORKSPACE, "the cross entropy's gradient needs %zu bytes of 256-byte aligned workspace (got %zu)",
+                need, workspace_bytes);
+  return launch_cross_entropy_grad(H, dtype, T, (int)d, ldh, W, V, ldw, targets, lse, dloss, dH, lddh, dW, lddw,
+                                   workspace, (hipStream_t)stream);
+}
+
 }  // extern "C"

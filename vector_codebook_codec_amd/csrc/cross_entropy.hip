@@ -1,0 +1,410 @@
+// Softmax cross entropy of hidden states H [T][d] against a vocabulary head
+// W [V][d], and its gradient, without keeping the T x V logits.
+//
+//     z_tv = <H_t, W_v>,   lse_t = log sum_v exp z_tv,   loss_t = lse_t - z_{t, y_t}
+//     G_tv = dloss_t (exp(z_tv - lse_t) - [v = y_t]),   dH = G W,   dW = G^T H
+//
+// A token whose target lies outside [0, V) is not counted: its loss and its
+// gradient are 0, and its hidden state, NaN or not, reaches nothing else.
+//
+// Forward: a workgroup forms one tile of logits in registers (vocabulary
+// entries are the A operand, so a lane holds several logits of one token) and
+// leaves per token the tile's largest logit m and sum of exp(z - m); a second
+// kernel joins the tiles in a fixed order.
+//
+// Gradient: the vocabulary is walked in pieces.  Of a piece the logits are
+// formed again and turned into G at once, stored in H's type once as G [T][v]
+// and once transposed; dW = G^T H is final for the piece, dH = G W is summed
+// over the pieces in fp32.  Every product contracts along the operands' rows,
+// which is why H and each piece of W are also laid out transposed.  G is
+// rounded to bf16 for bf16 inputs, like H and W themselves: its relative
+// error 2^-9 is below that of the rounded gradients it is summed into.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "qamw.h"
+#include "qamw_device.h"
+#include "qamw_internal.h"
+#include "tile_product.h"
+
+namespace qamw {
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+template <class Op> struct Elem;
+template <> struct Elem<OpBf16> {
+  typedef uint16_t T;
+  static __device__ __forceinline__ uint16_t put(float v) { return (uint16_t)f32_to_bf16_bits(v); }
+};
+template <> struct Elem<OpF32> {
+  typedef float T;
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+// four consecutive elements, 4-element aligned
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+
+// ---------------------------------------------------------------------------
+// Tile statistics of the logits: part[tile][t] = (max, sum of exp(z - max)),
+// and the target's logit from the one tile that holds it.
+// ---------------------------------------------------------------------------
+template <class Tl, class Op>
+__global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Operand H, int kchunks, int tiles_m,
+                                                                int tiles_n, const int64_t* __restrict__ targets,
+                                                                float2* __restrict__ part, float* __restrict__ zt) {
+  extern __shared__ __align__(1024) char tile_lds[];
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * Tl::BM, n0 = (int64_t)tn * Tl::BN;
+  f32x4 acc[Tl::TM][Tl::TN] = {};
+  Tl::run(acc, W, m0, H, n0, kchunks, 0, (kchunks + kStepChunks - 1) / kStepChunks, tile_lds);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int wm = wave / Tl::WN, wn = wave % Tl::WN;
+  const int64_t v0 = m0 + wm * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
+  const int tl = wn * (Tl::BN / Tl::WN) + (lane & 15);              // token inside the tile
+  float2* red = reinterpret_cast<float2*>(tile_lds);                // [WM][BN]
+  __syncthreads();                                                  // the tile's operands are no longer read
+#pragma unroll
+  for (int j = 0; j < Tl::TN; ++j) {
+    const int64_t t = n0 + tl + 16 * j;
+    const int64_t y = t < H.rows ? targets[t] : -1;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < Tl::TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t v = v0 + 16 * i + r;
+        if (v >= W.rows) acc[i][j][r] = -INFINITY;
+        m = fmaxf(m, acc[i][j][r]);
+        if (v == y && v < W.rows) zt[t] = acc[i][j][r];
+      }
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float base = m == -INFINITY ? 0.0f : m;                   // a tile of -inf alone sums to 0
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Tl::TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s += exp_of(acc[i][j][r] - base);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) red[wm * Tl::BN + tl + 16 * j] = make_float2(m, s);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < Tl::BN; k += Tl::kThreads) {
+    float2 a = red[k];
+#pragma unroll
+    for (int w = 1; w < Tl::WM; ++w) {
+      const float2 b = red[w * Tl::BN + k];
+      const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.0f : m;
+      a = make_float2(m, a.y * exp_of(a.x - base) + b.y * exp_of(b.x - base));
+    }
+    if (n0 + k < H.rows) part[(int64_t)tm * H.rows + n0 + k] = a;
+  }
+}
+
+// Joins the tiles' statistics: 16 tokens a workgroup, 16 threads a token,
+// thread k takes tiles k, k + 16, ...; then the 16 in order.
+__global__ __launch_bounds__(256) void ce_finish_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
+                                                        const int64_t* __restrict__ targets, int64_t T, int64_t V,
+                                                        int tiles, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 red[16][16];
+  const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
+  const int64_t t = (int64_t)blockIdx.x * 16 + i;
+  float m = -INFINITY;
+  double s = 0.0;
+  if (t < T) {
+    for (int q = k; q < tiles; q += 16) m = fmaxf(m, part[(int64_t)q * T + t].x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    for (int q = k; q < tiles; q += 16) {
+      const float2 p = part[(int64_t)q * T + t];
+      s += (double)p.y * (double)exp_of(p.x - base);
+    }
+  }
+  red[k][i] = make_float2(m, (float)s);
+  __syncthreads();
+  if (k == 0 && t < T) {
+    m = red[0][i].x;
+    for (int q = 1; q < 16; ++q) m = fmaxf(m, red[q][i].x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    s = 0.0;
+    for (int q = 0; q < 16; ++q) s += (double)red[q][i].y * (double)exp_of(red[q][i].x - base);
+    const float l = base + logf((float)s);
+    const int64_t y = targets[t];
+    lse[t] = l;
+    loss[t] = (y >= 0 && y < V) ? l - zt[t] : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// G of one piece: vocabulary entries v_first + [0, W.rows).  G [T][vp] and
+// Gt [W.rows][tp]; the columns past W.rows (to vp) and past T (to tp) are 0.
+// ---------------------------------------------------------------------------
+template <class Tl, class Op>
+__global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
+    Operand W, Operand H, int kchunks, int tiles_m, int tiles_n, const int64_t* __restrict__ targets, int64_t v_first,
+    int64_t V, const float* __restrict__ lse, const float* __restrict__ dloss, typename Elem<Op>::T* __restrict__ G,
+    int64_t vp, typename Elem<Op>::T* __restrict__ Gt, int64_t tp) {
+  extern __shared__ __align__(1024) char tile_lds[];
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * Tl::BM, n0 = (int64_t)tn * Tl::BN;
+  f32x4 acc[Tl::TM][Tl::TN] = {};
+  Tl::run(acc, W, m0, H, n0, kchunks, 0, (kchunks + kStepChunks - 1) / kStepChunks, tile_lds);
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int64_t v0 = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
+  const int64_t t0 = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+#pragma unroll
+  for (int j = 0; j < Tl::TN; ++j) {
+    const int64_t t = t0 + 16 * j;
+    int64_t y = -1;
+    float l = 0.0f, g = 0.0f;
+    if (t < H.rows) {
+      y = targets[t];
+      l = lse[t];
+      g = dloss[t];
+    }
+    const bool counted = y >= 0 && y < V;
+    y = counted ? y - v_first : -1;
+#pragma unroll
+    for (int i = 0; i < Tl::TM; ++i) {
+      const int64_t v = v0 + 16 * i;
+      f32x4 q;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p = exp_of(acc[i][j][r] - l) - (v + r == y ? 1.0f : 0.0f);
+        q[r] = counted && v + r < W.rows ? p * g : 0.0f;
+      }
+      if (t < H.rows && v < vp) store4(G + t * vp + v, q);
+      if (t < tp)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (v + r < W.rows) Gt[(v + r) * tp + t] = Elem<Op>::put(q[r]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// out[c][r] = in[r][c] for r < R and 0 for R <= r < rp; rows whose target is
+// not counted read as 0 (targets NULL: all rows count).  64 x 64 tiles
+// through LDS.
+// ---------------------------------------------------------------------------
+template <class E>
+__global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__ in, int64_t pitch, int64_t R, int64_t C,
+                                                           E* __restrict__ out, int64_t rp,
+                                                           const int64_t* __restrict__ targets, int64_t V) {
+  __shared__ E tile[64][64 + 4 / sizeof(E) * 1 + 1];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  for (int64_t c0 = (int64_t)blockIdx.y * 64; c0 < C; c0 += (int64_t)gridDim.y * 64) {
+    const int x = threadIdx.x & 63;
+    __syncthreads();
+    for (int y = threadIdx.x >> 6; y < 64; y += 4) {
+      const int64_t r = r0 + y, c = c0 + x;
+      E v = 0;
+      if (r < R && c < C && (!targets || (targets[r] >= 0 && targets[r] < V))) v = in[r * pitch + c];
+      tile[y][x] = v;
+    }
+    __syncthreads();
+    for (int y = threadIdx.x >> 6; y < 64; y += 4)
+      if (c0 + y < C && r0 + x < rp) out[(c0 + y) * rp + r0 + x] = tile[x][y];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// C[n][m] = sum_k A[m][k] B[n][k] over K steps split among gridDim.y
+// workgroups: split s writes (or adds to) C + s * split_stride.
+// ---------------------------------------------------------------------------
+template <class Tl, class Out>
+__global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Operand B, int kchunks, int tiles_m,
+                                                                  int tiles_n, int steps_per_split,
+                                                                  Out* __restrict__ C, int64_t ldc,
+                                                                  int64_t split_stride, bool add) {
+  extern __shared__ __align__(1024) char tile_lds[];
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * Tl::BM, n0 = (int64_t)tn * Tl::BN;
+  const int steps = (kchunks + kStepChunks - 1) / kStepChunks;
+  const int s0 = min((int)blockIdx.y * steps_per_split, steps), s1 = min(s0 + steps_per_split, steps);
+  f32x4 acc[Tl::TM][Tl::TN] = {};
+  if (s0 < s1) Tl::run(acc, A, m0, B, n0, kchunks, s0, s1, tile_lds);
+  Out* out = C + blockIdx.y * split_stride;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int64_t m = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
+  const int64_t n = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+#pragma unroll
+  for (int j = 0; j < Tl::TN; ++j)
+    if (n + 16 * j < B.rows)
+#pragma unroll
+      for (int i = 0; i < Tl::TM; ++i)
+        if (m + 16 * i < A.rows) {                                  // A.rows is a multiple of 4
+          Out* p = out + (n + 16 * j) * ldc + m + 16 * i;
+          if constexpr (sizeof(Out) == 4) {
+            if (add) acc[i][j] += *reinterpret_cast<const f32x4*>(p);
+          }
+          store4(p, acc[i][j]);
+        }
+}
+
+// dH = the fp32 sums of the splits, in order, rounded once
+template <class E>
+__global__ __launch_bounds__(256) void ce_sum_splits_kernel(const float* __restrict__ part, int splits, int64_t stride,
+                                                            int64_t T, int d, E* __restrict__ out, int64_t ldo) {
+  const int64_t per = d / 4, n = T * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    f32x4 s = reinterpret_cast<const f32x4*>(part)[i];
+    for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(part + k * stride + 4 * i);
+    store4(out + i / per * ldo + i % per * 4, s);
+  }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void ce_zero_kernel(E* __restrict__ out, int64_t rows, int d, int64_t ldo) {
+  const int64_t per = d / 4, n = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    store4(out + i / per * ldo + i % per * 4, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+}
+
+// ===========================================================================
+// launchers
+// ===========================================================================
+template <class Op> using CeTile = Tile<Op, 128, 128, 2, 2>;
+constexpr int kCeTile = 128;
+
+static unsigned blocks_for(int64_t n, int per) { return (unsigned)std::min<int64_t>((n + per - 1) / per, 65536); }
+static int tiles(int64_t n) { return (int)((n + kCeTile - 1) / kCeTile); }
+
+size_t ce_workspace_bytes(int64_t T, int64_t V) {
+  return round_up((size_t)tiles(V) * T * sizeof(float2), 256) + round_up((size_t)T * sizeof(float), 256);
+}
+
+template <class Op>
+static int ce_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
+                 const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
+  typedef CeTile<Op> Tl;
+  const int es = sizeof(typename Elem<Op>::T), kchunks = d / Op::kElems;
+  const Operand a = {(const char*)W, ldw * es, V, nullptr, 0}, b = {(const char*)H, ldh * es, T, nullptr, 0};
+  const int tm = tiles(V), tn = tiles(T);
+  float2* part = (float2*)ws;
+  float* zt = (float*)((char*)ws + round_up((size_t)tm * T * sizeof(float2), 256));
+  auto kernel = ce_stats_kernel<Tl, Op>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, a, b, kchunks, tm, tn,
+                     targets, part, zt);
+  int rc = check_launch("ce_stats_kernel");
+  if (rc) return rc;
+  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, st, part, zt, targets, T, V, tm, loss,
+                     lse);
+  return check_launch("ce_finish_kernel");
+}
+int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
+                         const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
+  return dt == QAMW_F32 ? ce_as<OpF32>(H, T, d, ldh, W, V, ldw, targets, loss, lse, ws, st)
+                        : ce_as<OpBf16>(H, T, d, ldh, W, V, ldw, targets, loss, lse, ws, st);
+}
+
+// Sizes and places of the gradient's workspace.
+struct CeGradPlan {
+  int64_t piece;            // vocabulary entries per piece
+  int64_t vp, tp;           // row pitches of G and Wt, of Gt and Ht (elements)
+  int splits;               // fp32 sums of dH, each over its share of every piece's K steps
+  size_t g, gt, wt, ht, sum, bytes;
+};
+static CeGradPlan ce_grad_plan(int64_t T, int64_t V, int d, int es) {
+  CeGradPlan p;
+  const int64_t budget = (int64_t)256 << 20;
+  const int64_t fit = budget / ((2 * T + d) * es) / 256 * 256;
+  p.piece = std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(fit, kMaxRowBytes / es), 256), (V + 7) / 8 * 8);
+  p.vp = p.piece;
+  p.tp = (T + 7) / 8 * 8;
+  const int64_t work = (int64_t)tiles(T) * tiles(d), steps = p.vp * es / kStepBytes + 1;
+  p.splits = (int)std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(512 / work, 1), 16), (steps + 7) / 8);
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t o = at; at += round_up(bytes, 256); return o; };
+  p.g = take((size_t)T * p.vp * es);
+  p.gt = take((size_t)p.piece * p.tp * es);
+  p.wt = take((size_t)d * p.vp * es);
+  p.ht = take((size_t)d * p.tp * es);
+  p.sum = take((size_t)p.splits * T * d * sizeof(float));
+  p.bytes = at;
+  return p;
+}
+size_t ce_grad_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt) { return ce_grad_plan(T, V, d, elem_size(dt)).bytes; }
+
+template <class Op>
+static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
+                      const int64_t* targets, const float* lse, const float* dloss, void* dH, int64_t lddh, void* dW,
+                      int64_t lddw, void* ws, hipStream_t st) {
+  typedef CeTile<Op> Tl;
+  typedef typename Elem<Op>::T E;
+  const int es = sizeof(E);
+  const CeGradPlan p = ce_grad_plan(T, V, d, es);
+  char* w = (char*)ws;
+  E *G = (E*)(w + p.g), *Gt = (E*)(w + p.gt), *Wt = (E*)(w + p.wt), *Ht = (E*)(w + p.ht);
+  float* sum = (float*)(w + p.sum);
+  const int64_t split_stride = T * (int64_t)d;
+  const unsigned dtiles = (unsigned)std::min<int64_t>((d + 63) / 64, 65535);
+  int rc;
+  if (dW) {
+    hipLaunchKernelGGL((ce_transpose_kernel<E>), dim3((unsigned)((p.tp + 63) / 64), dtiles), dim3(256), 0, st,
+                       (const E*)H, ldh, T, (int64_t)d, Ht, p.tp, targets, V);
+    if ((rc = check_launch("ce_transpose_kernel"))) return rc;
+  }
+  auto grad = ce_softmax_grad_kernel<Tl, Op>;
+  auto to_sum = ce_product_kernel<Tl, float>;
+  auto to_dw = ce_product_kernel<Tl, E>;
+  for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+    const int64_t n = std::min<int64_t>(p.piece, V - v0);
+    const Operand Wp = {(const char*)W + v0 * ldw * es, ldw * es, n, nullptr, 0};
+    const Operand Hp = {(const char*)H, ldh * es, T, nullptr, 0};
+    const int tm = tiles(n), tn = tiles(T), td = tiles(d);
+    hipLaunchKernelGGL(grad, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, Wp, Hp, d / Op::kElems, tm,
+                       tn, targets, v0, V, lse, dloss, G, p.vp, Gt, p.tp);
+    if ((rc = check_launch("ce_softmax_grad_kernel"))) return rc;
+    if (dW) {
+      const Operand a = {(const char*)Ht, p.tp * es, d, nullptr, 0}, b = {(const char*)Gt, p.tp * es, n, nullptr, 0};
+      const int kc = (int)(p.tp / Op::kElems);
+      hipLaunchKernelGGL(to_dw, dim3((unsigned)(td * tm), 1), dim3(Tl::kThreads), Tl::kLdsBytes, st, a, b, kc, td, tm,
+                         (kc + kStepChunks - 1) / kStepChunks, (E*)dW + v0 * lddw, lddw, (int64_t)0, false);
+      if ((rc = check_launch("ce_product_kernel"))) return rc;
+    }
+    if (dH) {
+      const int64_t np = (n + 7) / 8 * 8;                           // whole chunks; G and Wt hold 0 past n
+      hipLaunchKernelGGL((ce_transpose_kernel<E>), dim3((unsigned)((np + 63) / 64), dtiles), dim3(256), 0, st,
+                         (const E*)W + v0 * ldw, ldw, n, (int64_t)d, Wt, p.vp, (const int64_t*)nullptr, V);
+      if ((rc = check_launch("ce_transpose_kernel"))) return rc;
+      const Operand a = {(const char*)Wt, p.vp * es, d, nullptr, 0}, b = {(const char*)G, p.vp * es, T, nullptr, 0};
+      const int kc = (int)(np / Op::kElems), steps = (kc + kStepChunks - 1) / kStepChunks;
+      hipLaunchKernelGGL(to_sum, dim3((unsigned)(td * tn), (unsigned)p.splits), dim3(Tl::kThreads), Tl::kLdsBytes, st, a, b,
+                         kc, td, tn, (steps + p.splits - 1) / p.splits, sum, (int64_t)d, split_stride, v0 > 0);
+      if ((rc = check_launch("ce_product_kernel"))) return rc;
+    }
+  }
+  if (dH) {
+    hipLaunchKernelGGL((ce_sum_splits_kernel<E>), dim3(blocks_for(T * (d / 4), 256)), dim3(256), 0, st, sum, p.splits,
+                       split_stride, T, d, (E*)dH, lddh);
+    if ((rc = check_launch("ce_sum_splits_kernel"))) return rc;
+  }
+  return QAMW_OK;
+}
+int launch_cross_entropy_grad(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V,
+                              int64_t ldw, const int64_t* targets, const float* lse, const float* dloss, void* dH,
+                              int64_t lddh, void* dW, int64_t lddw, void* ws, hipStream_t st) {
+  return dt == QAMW_F32
+             ? ce_grad_as<OpF32>(H, T, d, ldh, W, V, ldw, targets, lse, dloss, dH, lddh, dW, lddw, ws, st)
+             : ce_grad_as<OpBf16>(H, T, d, ldh, W, V, ldw, targets, lse, dloss, dH, lddh, dW, lddw, ws, st);
+}
+// the gradient of no tokens
+int launch_zero_rows(void* out, int32_t dt, int64_t rows, int d, int64_t ldo, hipStream_t st) {
+  const dim3 grid(blocks_for(rows * (d / 4), 256)), block(256);
+  if (dt == QAMW_F32) hipLaunchKernelGGL((ce_zero_kernel<float>), grid, block, 0, st, (float*)out, rows, d, ldo);
+  else hipLaunchKernelGGL((ce_zero_kernel<uint16_t>), grid, block, 0, st, (uint16_t*)out, rows, d, ldo);
+  return check_launch("ce_zero_kernel");
+}
+
+}  // namespace qamw

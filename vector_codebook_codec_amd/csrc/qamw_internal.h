@@ -150,4 +150,29 @@ int launch_decode(int L, const uint32_t* packed, const uint16_t* rho_f16, int N,
                   const float* sigma, uint64_t seed, const float* cb, int K, int B, int row_words, void* out,
                   int32_t odt, int64_t ldo, hipStream_t st);
 
+// ---- microscaled 4-bit operands (mxfp4.hip): blocks of 32, 16 bytes of codes and one scale code each;
+// scale rows are padded to whole 16-byte groups
+constexpr int kMx4Block = 32;
+inline int64_t mx4_blocks(int64_t d) { return (d + kMx4Block - 1) / kMx4Block; }
+inline int64_t mx4_scale_bytes(int64_t d) { return (mx4_blocks(d) + 15) / 16 * 16; }
+int launch_mx4_quantize(const void* W, int32_t wdt, int64_t N, int d, int64_t ldw, uint8_t* codes, uint8_t* scales,
+                        void* values, int32_t vdt, int64_t ldv, hipStream_t st);
+int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N, int d, void* W, int32_t odt,
+                          int64_t ldo, hipStream_t st);
+int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
+                      const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st);
+
+// row pitch that a 256-row tile's 32-bit byte offsets can hold
+constexpr int64_t kMaxRowBytes = int64_t(1) << 22;
+
+// ---- vocabulary cross entropy (cross_entropy.hip)
+size_t ce_workspace_bytes(int64_t T, int64_t V);
+size_t ce_grad_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt);
+int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
+                         const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st);
+int launch_cross_entropy_grad(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V,
+                              int64_t ldw, const int64_t* targets, const float* lse, const float* dloss, void* dH,
+                              int64_t lddh, void* dW, int64_t lddw, void* ws, hipStream_t st);
+int launch_zero_rows(void* out, int32_t dt, int64_t rows, int d, int64_t ldo, hipStream_t st);
+
 }  // namespace qamw
