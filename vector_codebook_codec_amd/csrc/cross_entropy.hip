@@ -143,15 +143,39 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(const float2* __restrict
   }
 }
 
+// The largest |dloss| of the counted tokens, or 1 where that is 0 or not
+// finite.  G is kept relative to it: under a mean loss, whose upstream
+// gradients are all the same number, -1 + p is then what is rounded to bf16,
+// and not a multiple of an arbitrary factor.
+__global__ __launch_bounds__(1024) void ce_upstream_kernel(const float* __restrict__ dloss,
+                                                           const int64_t* __restrict__ targets, int64_t T, int64_t V,
+                                                           float* __restrict__ unit) {
+  __shared__ float red[16];
+  float m = 0.0f;
+  for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    const int64_t y = targets[t];
+    if (y >= 0 && y < V) m = fmaxf(m, fabsf(dloss[t]));
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, red[i]);
+    *unit = m > 0.0f && m < INFINITY ? m : 1.0f;
+  }
+}
+
 // ---------------------------------------------------------------------------
-// G of one piece: vocabulary entries v_first + [0, W.rows).  G [T][vp] and
+// G / unit of one piece: vocabulary entries v_first + [0, W.rows).  G [T][vp] and
 // Gt [W.rows][tp]; the columns past W.rows (to vp) and past T (to tp) are 0.
 // ---------------------------------------------------------------------------
 template <class Tl, class Op>
 __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
     Operand W, Operand H, int kchunks, int tiles_m, int tiles_n, const int64_t* __restrict__ targets, int64_t v_first,
-    int64_t V, const float* __restrict__ lse, const float* __restrict__ dloss, typename Elem<Op>::T* __restrict__ G,
-    int64_t vp, typename Elem<Op>::T* __restrict__ Gt, int64_t tp) {
+    int64_t V, const float* __restrict__ lse, const float* __restrict__ dloss, const float* __restrict__ unit,
+    typename Elem<Op>::T* __restrict__ G, int64_t vp, typename Elem<Op>::T* __restrict__ Gt, int64_t tp) {
+  typedef typename Elem<Op>::T E;
   extern __shared__ __align__(1024) char tile_lds[];
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
@@ -161,6 +185,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
   const int64_t v0 = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
   const int64_t t0 = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+  __syncthreads();                                                  // the tile's operands are no longer read
 #pragma unroll
   for (int j = 0; j < Tl::TN; ++j) {
     const int64_t t = t0 + 16 * j;
@@ -169,7 +194,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
     if (t < H.rows) {
       y = targets[t];
       l = lse[t];
-      g = dloss[t];
+      g = dloss[t] / *unit;
     }
     const bool counted = y >= 0 && y < V;
     y = counted ? y - v_first : -1;
@@ -182,11 +207,36 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
         const float p = exp_of(acc[i][j][r] - l) - (v + r == y ? 1.0f : 0.0f);
         q[r] = counted && v + r < W.rows ? p * g : 0.0f;
       }
-      if (t < H.rows && v < vp) store4(G + t * vp + v, q);
-      if (t < tp)
+      if constexpr (sizeof(E) == 2) {
+        *reinterpret_cast<uint2*>(Tile16<Tl::BM>::at(tile_lds, (int)(t - n0), (int)(v - m0))) =
+            make_uint2(pack_bf16x2(q[0], q[1]), pack_bf16x2(q[2], q[3]));
+      } else {
+        if (t < H.rows && v < vp) store4(G + t * vp + v, q);
+        if (t < tp)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (v + r < W.rows) Gt[(v + r) * tp + t] = Elem<Op>::put(q[r]);
+          for (int r = 0; r < 4; ++r)
+            if (v + r < W.rows) Gt[(v + r) * tp + t] = q[r];
+      }
+    }
+  }
+  if constexpr (sizeof(E) == 2) {
+    // 16-bit results go through LDS: rows of G and of Gt in runs of 16 bytes a lane
+    __syncthreads();
+    for (int k = threadIdx.x; k < Tl::BN * (Tl::BM / 8); k += Tl::kThreads) {
+      const int t = k / (Tl::BM / 8), v = k % (Tl::BM / 8) * 8;
+      if (n0 + t < H.rows && m0 + v < vp)
+        *reinterpret_cast<u32x4*>(G + (n0 + t) * vp + m0 + v) =
+            *reinterpret_cast<const u32x4*>(Tile16<Tl::BM>::at(tile_lds, t, v));
+    }
+    for (int k = threadIdx.x; k < Tl::BM / 2 * (Tl::BN / 8); k += Tl::kThreads) {
+      // 8 lanes along the tokens, 8 along the vocabulary
+      const int cell = k / 64, o = cell % (Tl::BN / 64) * 8 + (k & 7), v = (cell / (Tl::BN / 64) * 8 + (k >> 3 & 7)) * 2;
+      if (n0 + 8 * o >= tp || m0 + v >= W.rows) continue;
+      u32x4 c0, c1;
+      Tile16<Tl::BM>::columns(tile_lds, 8 * o, v, c0, c1);
+      E* p = Gt + (m0 + v) * tp + n0 + 8 * o;
+      *reinterpret_cast<u32x4*>(p) = c0;
+      if (m0 + v + 1 < W.rows) *reinterpret_cast<u32x4*>(p + tp) = c1;
     }
   }
 }
@@ -200,30 +250,56 @@ template <class E>
 __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__ in, int64_t pitch, int64_t R, int64_t C,
                                                            E* __restrict__ out, int64_t rp,
                                                            const int64_t* __restrict__ targets, int64_t V) {
-  __shared__ E tile[64][64 + 4 / sizeof(E) * 1 + 1];
+  constexpr int kUnit = 16 / sizeof(E);                              // elements per 16 bytes; divides C and rp
+  __shared__ __align__(16) char tile[64 * 64 * sizeof(E) + (sizeof(E) == 4 ? 64 * 16 : 0)];
   const int64_t r0 = (int64_t)blockIdx.x * 64;
+  auto place = [&](int r, int c) __attribute__((always_inline)) {
+    if constexpr (sizeof(E) == 2) return Tile16<64>::at(tile, r, c);
+    else return tile + r * (64 * 4 + 16) + c * 4;
+  };
   for (int64_t c0 = (int64_t)blockIdx.y * 64; c0 < C; c0 += (int64_t)gridDim.y * 64) {
-    const int x = threadIdx.x & 63;
     __syncthreads();
-    for (int y = threadIdx.x >> 6; y < 64; y += 4) {
-      const int64_t r = r0 + y, c = c0 + x;
-      E v = 0;
-      if (r < R && c < C && (!targets || (targets[r] >= 0 && targets[r] < V))) v = in[r * pitch + c];
-      tile[y][x] = v;
+#pragma unroll
+    for (int k = threadIdx.x; k < 64 * 64 / kUnit; k += 256) {
+      const int y = k / (64 / kUnit), x = k % (64 / kUnit) * kUnit;
+      const int64_t r = r0 + y;
+      u32x4 v = {0, 0, 0, 0};
+      if (r < R && c0 + x < C && (!targets || (targets[r] >= 0 && targets[r] < V)))
+        v = *reinterpret_cast<const u32x4*>(in + r * pitch + c0 + x);
+      *reinterpret_cast<u32x4*>(place(y, x)) = v;
     }
     __syncthreads();
-    for (int y = threadIdx.x >> 6; y < 64; y += 4)
-      if (c0 + y < C && r0 + x < rp) out[(c0 + y) * rp + r0 + x] = tile[x][y];
+    if constexpr (sizeof(E) == 2) {
+      const int o = threadIdx.x & 7, c = (threadIdx.x >> 3) * 2;
+      if (r0 + 8 * o < rp && c0 + c < C) {
+        u32x4 a, b;
+        Tile16<64>::columns(tile, 8 * o, c, a, b);
+        E* p = out + (c0 + c) * rp + r0 + 8 * o;
+        *reinterpret_cast<u32x4*>(p) = a;
+        *reinterpret_cast<u32x4*>(p + rp) = b;
+      }
+    } else {
+#pragma unroll
+      for (int k = threadIdx.x; k < 64 * 16; k += 256) {
+        const int x = k % 16 * 4, c = k / 16;
+        if (r0 + x >= rp || c0 + c >= C) continue;
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float*>(place(x + i, c));
+        *reinterpret_cast<f32x4*>(out + (c0 + c) * rp + r0 + x) = v;
+      }
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// C[n][m] = sum_k A[m][k] B[n][k] over K steps split among gridDim.y
-// workgroups: split s writes (or adds to) C + s * split_stride.
+// C[n][m] = unit sum_k A[m][k] B[n][k] (unit NULL: 1) over K steps split among
+// gridDim.y workgroups: split s writes (or adds to) C + s * split_stride.
 // ---------------------------------------------------------------------------
 template <class Tl, class Out>
 __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Operand B, int kchunks, int tiles_m,
                                                                   int tiles_n, int steps_per_split,
+                                                                  const float* __restrict__ unit,
                                                                   Out* __restrict__ C, int64_t ldc,
                                                                   int64_t split_stride, bool add) {
   extern __shared__ __align__(1024) char tile_lds[];
@@ -238,6 +314,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
   const int64_t m = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
   const int64_t n = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+  const float u = unit ? *unit : 1.0f;
 #pragma unroll
   for (int j = 0; j < Tl::TN; ++j)
     if (n + 16 * j < B.rows)
@@ -245,6 +322,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
       for (int i = 0; i < Tl::TM; ++i)
         if (m + 16 * i < A.rows) {                                  // A.rows is a multiple of 4
           Out* p = out + (n + 16 * j) * ldc + m + 16 * i;
+          acc[i][j] *= u;
           if constexpr (sizeof(Out) == 4) {
             if (add) acc[i][j] += *reinterpret_cast<const f32x4*>(p);
           }
@@ -252,15 +330,17 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
         }
 }
 
-// dH = the fp32 sums of the splits, in order, rounded once
+// dH = unit times the fp32 sums of the splits, in order, rounded once
 template <class E>
 __global__ __launch_bounds__(256) void ce_sum_splits_kernel(const float* __restrict__ part, int splits, int64_t stride,
-                                                            int64_t T, int d, E* __restrict__ out, int64_t ldo) {
+                                                            int64_t T, int d, const float* __restrict__ unit,
+                                                            E* __restrict__ out, int64_t ldo) {
+  const float u = *unit;
   const int64_t per = d / 4, n = T * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     f32x4 s = reinterpret_cast<const f32x4*>(part)[i];
     for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(part + k * stride + 4 * i);
-    store4(out + i / per * ldo + i % per * 4, s);
+    store4(out + i / per * ldo + i % per * 4, s * u);
   }
 }
 
@@ -274,33 +354,35 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(E* __restrict__ out, int64
 // ===========================================================================
 // launchers
 // ===========================================================================
-template <class Op> using CeTile = Tile<Op, 128, 128, 2, 2>;
-constexpr int kCeTile = 128;
-
 static unsigned blocks_for(int64_t n, int per) { return (unsigned)std::min<int64_t>((n + per - 1) / per, 65536); }
-static int tiles(int64_t n) { return (int)((n + kCeTile - 1) / kCeTile); }
 
 size_t ce_workspace_bytes(int64_t T, int64_t V) {
-  return round_up((size_t)tiles(V) * T * sizeof(float2), 256) + round_up((size_t)T * sizeof(float), 256);
+  return round_up((size_t)tiles_of(V, kSmallTile) * T * sizeof(float2), 256) + round_up((size_t)T * sizeof(float), 256);
 }
 
-template <class Op>
-static int ce_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
-                 const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
-  typedef CeTile<Op> Tl;
-  const int es = sizeof(typename Elem<Op>::T), kchunks = d / Op::kElems;
-  const Operand a = {(const char*)W, ldw * es, V, nullptr, 0}, b = {(const char*)H, ldh * es, T, nullptr, 0};
-  const int tm = tiles(V), tn = tiles(T);
+template <class Op, class Tl>
+static int ce_tiled(const Operand& W, const Operand& H, int kchunks, const int64_t* targets, float* loss, float* lse,
+                    void* ws, hipStream_t st) {
+  const int tm = (int)tiles_of(W.rows, Tl::BM), tn = (int)tiles_of(H.rows, Tl::BN);
+  const int64_t T = H.rows;
   float2* part = (float2*)ws;
   float* zt = (float*)((char*)ws + round_up((size_t)tm * T * sizeof(float2), 256));
   auto kernel = ce_stats_kernel<Tl, Op>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, a, b, kchunks, tm, tn,
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, H, kchunks, tm, tn,
                      targets, part, zt);
   int rc = check_launch("ce_stats_kernel");
   if (rc) return rc;
-  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, st, part, zt, targets, T, V, tm, loss,
-                     lse);
+  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, st, part, zt, targets, T, W.rows, tm,
+                     loss, lse);
   return check_launch("ce_finish_kernel");
+}
+template <class Op>
+static int ce_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
+                 const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
+  const int es = sizeof(typename Elem<Op>::T), kchunks = d / Op::kElems;
+  const Operand a = {(const char*)W, ldw * es, V, nullptr, 0}, b = {(const char*)H, ldh * es, T, nullptr, 0};
+  return large_tiles_pay(V, T) ? ce_tiled<Op, LargeTile<Op>>(a, b, kchunks, targets, loss, lse, ws, st)
+                               : ce_tiled<Op, SmallTile<Op>>(a, b, kchunks, targets, loss, lse, ws, st);
 }
 int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                          const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
@@ -308,70 +390,108 @@ int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ld
                         : ce_as<OpBf16>(H, T, d, ldh, W, V, ldw, targets, loss, lse, ws, st);
 }
 
+// G, Gt and Wt of one piece.  More of it means fewer launches, each with a
+// last round of workgroups that fills the CUs badly: T = 4096, V = 131072,
+// d = 4096 takes 15.1 ms at 128 MiB, 14.7 ms at 420 MiB and 14.5 ms at
+// 820 MiB.
+constexpr int64_t kCeBudget = (int64_t)512 << 20;
 // Sizes and places of the gradient's workspace.
 struct CeGradPlan {
   int64_t piece;            // vocabulary entries per piece
   int64_t vp, tp;           // row pitches of G and Wt, of Gt and Ht (elements)
-  int splits;               // fp32 sums of dH, each over its share of every piece's K steps
-  size_t g, gt, wt, ht, sum, bytes;
+  ProductPlan dh;           // dH's product over one piece: splits hold fp32 sums of their own over all pieces
+  size_t unit, g, gt, wt, ht, sum, bytes;
 };
 static CeGradPlan ce_grad_plan(int64_t T, int64_t V, int d, int es) {
   CeGradPlan p;
-  const int64_t budget = (int64_t)256 << 20;
-  const int64_t fit = budget / ((2 * T + d) * es) / 256 * 256;
-  p.piece = std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(fit, kMaxRowBytes / es), 256), (V + 7) / 8 * 8);
+  // Entries whose G, Gt and Wt fit the budget, as whole rounds of large tiles
+  // over the CUs where a round is no more than that (T = 4096: 16 tiles of
+  // tokens by 16 of vocabulary), then evened out over the pieces.
+  const int64_t budget = kCeBudget;
+  int64_t fit = std::min<int64_t>(budget / ((2 * T + d) * es), kMaxRowBytes / es) / kLargeTile;   // tiles
+  fit = std::max<int64_t>(fit, 1);
+  int64_t round = kCus;
+  for (int64_t tn = tiles_of(T, kLargeTile); round > 1 && tn % 2 == 0; tn /= 2) round /= 2;
+  if (round <= fit) fit = fit / round * round;
+  else round = 1;
+  const int64_t all = tiles_of(V, kLargeTile), pieces = tiles_of(all, fit);
+  p.piece = std::min<int64_t>(tiles_of(tiles_of(all, pieces), round) * round * kLargeTile, (V + 7) / 8 * 8);
   p.vp = p.piece;
   p.tp = (T + 7) / 8 * 8;
-  const int64_t work = (int64_t)tiles(T) * tiles(d), steps = p.vp * es / kStepBytes + 1;
-  p.splits = (int)std::min<int64_t>(std::min<int64_t>(std::max<int64_t>(512 / work, 1), 16), (steps + 7) / 8);
+  p.dh = product_plan(d, T, (p.vp * es + kStepBytes - 1) / kStepBytes, es == 4 ? kStepUsF32 : kStepUsBf16);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += round_up(bytes, 256); return o; };
+  p.unit = take(sizeof(float));
   p.g = take((size_t)T * p.vp * es);
   p.gt = take((size_t)p.piece * p.tp * es);
   p.wt = take((size_t)d * p.vp * es);
   p.ht = take((size_t)d * p.tp * es);
-  p.sum = take((size_t)p.splits * T * d * sizeof(float));
+  p.sum = take((size_t)p.dh.splits * T * d * sizeof(float));
   p.bytes = at;
   return p;
 }
 size_t ce_grad_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt) { return ce_grad_plan(T, V, d, elem_size(dt)).bytes; }
 
+template <class Op, class Tl>
+static int softmax_grad_tiled(const Operand& W, const Operand& H, int kchunks, const int64_t* targets, int64_t v0, int64_t V,
+                              const float* lse, const float* dloss, const float* unit, typename Elem<Op>::T* G, int64_t vp,
+                              typename Elem<Op>::T* Gt, int64_t tp, hipStream_t st) {
+  const int tm = (int)tiles_of(W.rows, Tl::BM), tn = (int)tiles_of(H.rows, Tl::BN);
+  auto kernel = ce_softmax_grad_kernel<Tl, Op>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, H, kchunks, tm, tn,
+                     targets, v0, V, lse, dloss, unit, G, vp, Gt, tp);
+  return check_launch("ce_softmax_grad_kernel");
+}
+template <class Tl, class Out>
+static int product_tiled(const Operand& A, const Operand& B, int kchunks, int splits, const float* unit, Out* C, int64_t ldc,
+                         int64_t split_stride, bool add, hipStream_t st) {
+  const int tm = (int)tiles_of(A.rows, Tl::BM), tn = (int)tiles_of(B.rows, Tl::BN);
+  const int steps = (kchunks + kStepChunks - 1) / kStepChunks, per = (steps + splits - 1) / splits;
+  auto kernel = ce_product_kernel<Tl, Out>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn), (unsigned)splits), dim3(Tl::kThreads), Tl::kLdsBytes, st, A, B,
+                     kchunks, tm, tn, per, unit, C, ldc, split_stride, add);
+  return check_launch("ce_product_kernel");
+}
+template <class Op, class Out>
+static int product(const Operand& A, const Operand& B, int kchunks, const ProductPlan& p, const float* unit, Out* C,
+                   int64_t ldc, int64_t split_stride, bool add, hipStream_t st) {
+  return p.large ? product_tiled<LargeTile<Op>, Out>(A, B, kchunks, p.splits, unit, C, ldc, split_stride, add, st)
+                 : product_tiled<SmallTile<Op>, Out>(A, B, kchunks, p.splits, unit, C, ldc, split_stride, add, st);
+}
+
 template <class Op>
 static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                       const int64_t* targets, const float* lse, const float* dloss, void* dH, int64_t lddh, void* dW,
                       int64_t lddw, void* ws, hipStream_t st) {
-  typedef CeTile<Op> Tl;
   typedef typename Elem<Op>::T E;
   const int es = sizeof(E);
   const CeGradPlan p = ce_grad_plan(T, V, d, es);
   char* w = (char*)ws;
   E *G = (E*)(w + p.g), *Gt = (E*)(w + p.gt), *Wt = (E*)(w + p.wt), *Ht = (E*)(w + p.ht);
-  float* sum = (float*)(w + p.sum);
+  float *unit = (float*)(w + p.unit), *sum = (float*)(w + p.sum);
   const int64_t split_stride = T * (int64_t)d;
   const unsigned dtiles = (unsigned)std::min<int64_t>((d + 63) / 64, 65535);
-  int rc;
+  hipLaunchKernelGGL(ce_upstream_kernel, dim3(1), dim3(1024), 0, st, dloss, targets, T, V, unit);
+  int rc = check_launch("ce_upstream_kernel");
+  if (rc) return rc;
   if (dW) {
     hipLaunchKernelGGL((ce_transpose_kernel<E>), dim3((unsigned)((p.tp + 63) / 64), dtiles), dim3(256), 0, st,
                        (const E*)H, ldh, T, (int64_t)d, Ht, p.tp, targets, V);
     if ((rc = check_launch("ce_transpose_kernel"))) return rc;
   }
-  auto grad = ce_softmax_grad_kernel<Tl, Op>;
-  auto to_sum = ce_product_kernel<Tl, float>;
-  auto to_dw = ce_product_kernel<Tl, E>;
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
     const int64_t n = std::min<int64_t>(p.piece, V - v0);
     const Operand Wp = {(const char*)W + v0 * ldw * es, ldw * es, n, nullptr, 0};
     const Operand Hp = {(const char*)H, ldh * es, T, nullptr, 0};
-    const int tm = tiles(n), tn = tiles(T), td = tiles(d);
-    hipLaunchKernelGGL(grad, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, Wp, Hp, d / Op::kElems, tm,
-                       tn, targets, v0, V, lse, dloss, G, p.vp, Gt, p.tp);
-    if ((rc = check_launch("ce_softmax_grad_kernel"))) return rc;
+    const int kd = d / Op::kElems;
+    rc = large_tiles_pay(n, T)
+             ? softmax_grad_tiled<Op, LargeTile<Op>>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt, p.tp, st)
+             : softmax_grad_tiled<Op, SmallTile<Op>>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt, p.tp, st);
+    if (rc) return rc;
     if (dW) {
       const Operand a = {(const char*)Ht, p.tp * es, d, nullptr, 0}, b = {(const char*)Gt, p.tp * es, n, nullptr, 0};
-      const int kc = (int)(p.tp / Op::kElems);
-      hipLaunchKernelGGL(to_dw, dim3((unsigned)(td * tm), 1), dim3(Tl::kThreads), Tl::kLdsBytes, st, a, b, kc, td, tm,
-                         (kc + kStepChunks - 1) / kStepChunks, (E*)dW + v0 * lddw, lddw, (int64_t)0, false);
-      if ((rc = check_launch("ce_product_kernel"))) return rc;
+      const ProductPlan whole = {large_tiles_pay(d, n), 1};
+      if ((rc = product<Op, E>(a, b, (int)(p.tp / Op::kElems), whole, unit, (E*)dW + v0 * lddw, lddw, 0, false, st))) return rc;
     }
     if (dH) {
       const int64_t np = (n + 7) / 8 * 8;                           // whole chunks; G and Wt hold 0 past n
@@ -379,15 +499,12 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
                          (const E*)W + v0 * ldw, ldw, n, (int64_t)d, Wt, p.vp, (const int64_t*)nullptr, V);
       if ((rc = check_launch("ce_transpose_kernel"))) return rc;
       const Operand a = {(const char*)Wt, p.vp * es, d, nullptr, 0}, b = {(const char*)G, p.vp * es, T, nullptr, 0};
-      const int kc = (int)(np / Op::kElems), steps = (kc + kStepChunks - 1) / kStepChunks;
-      hipLaunchKernelGGL(to_sum, dim3((unsigned)(td * tn), (unsigned)p.splits), dim3(Tl::kThreads), Tl::kLdsBytes, st, a, b,
-                         kc, td, tn, (steps + p.splits - 1) / p.splits, sum, (int64_t)d, split_stride, v0 > 0);
-      if ((rc = check_launch("ce_product_kernel"))) return rc;
+      if ((rc = product<Op, float>(a, b, (int)(np / Op::kElems), p.dh, nullptr, sum, d, split_stride, v0 > 0, st))) return rc;
     }
   }
   if (dH) {
-    hipLaunchKernelGGL((ce_sum_splits_kernel<E>), dim3(blocks_for(T * (d / 4), 256)), dim3(256), 0, st, sum, p.splits,
-                       split_stride, T, d, (E*)dH, lddh);
+    hipLaunchKernelGGL((ce_sum_splits_kernel<E>), dim3(blocks_for(T * (d / 4), 256)), dim3(256), 0, st, sum, p.dh.splits,
+                       split_stride, T, d, unit, (E*)dH, lddh);
     if ((rc = check_launch("ce_sum_splits_kernel"))) return rc;
   }
   return QAMW_OK;

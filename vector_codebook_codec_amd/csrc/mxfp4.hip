@@ -262,15 +262,19 @@ int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N
   return dequantize_to<MemBf16>(codes, scales, N, d, W, ldo, st);
 }
 
-template <class Out>
-static int matmul_to(const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, hipStream_t st) {
-  typedef Tile<OpMx4, 128, 128, 2, 2> Tl;
-  const int tiles_m = (int)((W.rows + Tl::BM - 1) / Tl::BM), tiles_n = (int)((X.rows + Tl::BN - 1) / Tl::BN);
+template <class Tl, class Out>
+static int matmul_tiled(const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, hipStream_t st) {
+  const int tiles_m = (int)tiles_of(W.rows, Tl::BM), tiles_n = (int)tiles_of(X.rows, Tl::BN);
   const bool wide = ldy % 4 == 0 && (uintptr_t)Y % (4 * sizeof(typename Out::T)) == 0;
   auto kernel = mx4_matmul_kernel<Tl, Out>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, X, kchunks,
                      tiles_m, tiles_n, (typename Out::T*)Y, ldy, wide);
   return check_launch("mx4_matmul_kernel");
+}
+template <class Out>
+static int matmul_to(const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, hipStream_t st) {
+  return large_tiles_pay(W.rows, X.rows) ? matmul_tiled<LargeTile<OpMx4>, Out>(W, X, kchunks, Y, ldy, st)
+                                         : matmul_tiled<SmallTile<OpMx4>, Out>(W, X, kchunks, Y, ldy, st);
 }
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st) {

@@ -162,6 +162,43 @@ int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st);
 
+// Tiles of a product (tile_product.h).  256 CUs run one large tile or two
+// small ones each; a pair of small tiles takes 0.64 of a large one's time per
+// K step (measured at 8192 x 8192 x 4096: 498 us for 8 rounds of pairs,
+// 392 us for 4 rounds of large tiles).
+constexpr int kLargeTile = 256, kSmallTile = 128, kCus = 256;
+inline int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
+inline bool large_tiles_pay(int64_t M, int64_t N) {
+  const int64_t large = tiles_of(tiles_of(M, kLargeTile) * tiles_of(N, kLargeTile), kCus);
+  const int64_t pairs = tiles_of(tiles_of(M, kSmallTile) * tiles_of(N, kSmallTile), 2 * kCus);
+  return 100 * large <= 64 * pairs;
+}
+// How a product [M][N] of `steps` K steps is cut: tile shape, and into how
+// many fp32 partial results along K (1, 2, 4, 8 or 16), by the estimated time:
+// rounds of workgroups times K steps, plus writing and reading the partial
+// results at 4 TB/s.  step_us: a large tile's K step with all CUs busy
+// (measured, microseconds).
+constexpr float kStepUsBf16 = 1.5f, kStepUsF32 = 7.4f, kStepUsMx4 = 2.0f;
+struct ProductPlan {
+  bool large;
+  int splits;
+};
+inline ProductPlan product_plan(int64_t M, int64_t N, int64_t steps, float step_us) {
+  ProductPlan best = {large_tiles_pay(M, N), 1};
+  double best_us = 1e30;
+  for (int s = 1; s <= 16; s *= 2) {
+    if (s > 1 && steps < 8 * s) break;                 // at least 8 steps a workgroup
+    for (int large = 0; large < 2; ++large) {
+      const int tile = large ? kLargeTile : kSmallTile;
+      const int64_t wgs = tiles_of(M, tile) * tiles_of(N, tile) * s;
+      const double rounds = large ? (double)tiles_of(wgs, kCus) : 0.64 * (double)tiles_of(wgs, 2 * kCus);
+      const double us = rounds * step_us * (double)tiles_of(steps, s) + (s > 1 ? (double)s * M * N * 8e-6 / 4.0 : 0.0);
+      if (us < 0.98 * best_us) best_us = us, best = {large != 0, s};
+    }
+  }
+  return best;
+}
+
 // row pitch that a 256-row tile's 32-bit byte offsets can hold
 constexpr int64_t kMaxRowBytes = int64_t(1) << 22;
 

@@ -7,13 +7,17 @@
 // elements.  A K step is 8 chunks (128 bytes) of every row of both operands,
 // copied from global memory straight into LDS (buffer loads with an LDS
 // destination).  Chunk c of row r lies at position c ^ ((r >> 1) & 7) of its
-// 128-byte LDS row: the 16 rows that a matrix instruction reads at one chunk
-// index then fall in 16 different 16-byte bank groups.  The copy writes LDS
-// in lane order, so the permutation is applied to the global address.
+// 128-byte LDS row.  The copy writes LDS in lane order, so the permutation is
+// applied to the global address.
 //
 // Matrix-instruction operands: lane l holds row l % 16 of a 16-row fragment
-// and, in instruction s (0 or 1) of a K step, chunk 2 (l / 16) + s.  Which k
-// a chunk stands for does not matter as long as A and B agree.  Results:
+// and, in instruction s (0 or 1) of a K step, chunk 2 q + s with q = 0, 3, 2,
+// 1 for l / 16 = 0, 1, 2, 3.  Which k a chunk stands for does not matter as
+// long as A and B agree; this order and the permutation above together let
+// every group of 16 lanes that a 16-byte LDS read serves at once (rows 0-3
+// and 12-15 of one lane group with rows 4-11 of its neighbour, and the other
+// way round) fall in 16 different bank groups: with q = l / 16 each read took
+// 4 extra cycles.  Results:
 // register r of lane l is C[m = 4 (l / 16) + r][n = l % 16] of a 16 x 16 tile,
 // so consecutive registers are consecutive rows of A.
 //
@@ -61,6 +65,7 @@ __device__ __forceinline__ void copy4_to_lds(__amdgpu_buffer_rsrc_t r, char* lds
 // ---- element types: products of one fragment pair over one chunk per lane
 struct OpBf16 {
   static constexpr int kElems = 8;                 // elements per chunk
+  static constexpr int kMmas = 1;                  // matrix instructions per chunk
   static constexpr bool kScaled = false;
   static __device__ __forceinline__ f32x4 mma(i32x4 a, i32x4 b, f32x4 c, int, int, int) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
@@ -69,6 +74,7 @@ struct OpBf16 {
 };
 struct OpF32 {
   static constexpr int kElems = 4;
+  static constexpr int kMmas = 4;
   static constexpr bool kScaled = false;
   static __device__ __forceinline__ f32x4 mma(i32x4 a, i32x4 b, f32x4 c, int, int, int) {
     const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
@@ -79,6 +85,7 @@ struct OpF32 {
 };
 struct OpMx4 {
   static constexpr int kElems = 32;
+  static constexpr int kMmas = 1;
   static constexpr bool kScaled = true;
   // s selects the byte of the lane's two scale codes
   static __device__ __forceinline__ f32x4 mma(i32x4 a, i32x4 b, f32x4 c, int s, int sa, int sb) {
@@ -95,13 +102,23 @@ struct Tile {
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;     // 16 x 16 results per wavefront
   static constexpr int kRows = BM + BN;
   static constexpr int kDataBytes = kRows * kStepBytes;
-  static constexpr int kStageBytes = kDataBytes + (Op::kScaled ? kRows * kStepChunks : 0);
-  static constexpr int kLdsBytes = 2 * kStageBytes;
+  static constexpr int kScaleBytes = Op::kScaled ? kRows * 16 : 0;         // codes of two K steps
+  static constexpr int kLdsBytes = 2 * (kDataBytes + kScaleBytes);
   static constexpr int kCopiesA = BM / 8 / kWaves, kCopiesB = BN / 8 / kWaves;   // 8 rows per wavefront copy
   static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && (8 * kWaves) % 16 == 0, "whole copies");
+  static_assert(!Op::kScaled || (BM % kWave == 0 && BN % kWave == 0), "whole scale copies");
 
-  // acc += the tile (m0, n0) over K steps [step0, step1); kchunks = chunks of
-  // a row.  Every thread of the workgroup calls it; lds holds kLdsBytes.
+  // acc += the tile (m0, n0) over K steps [step0, step1), step0 even and below
+  // step1; kchunks = chunks of a row.  Every thread of the workgroup calls it;
+  // lds holds kLdsBytes.
+  //
+  // Two LDS buffers take the K steps in turn.  Fragments are read from LDS
+  // half a step before the matrix instructions that use them, so that one
+  // barrier a step is enough and stands between two runs of matrix
+  // instructions whose operands are already in registers:
+  //   read (k, half 1)       | multiply (k, half 0)
+  //   wait for the copies of step k + 1, barrier: nobody reads buffer k again
+  //   copy step k + 2 into it; read (k + 1, half 0) | multiply (k, half 1)
   static __device__ __forceinline__ void run(f32x4 (&acc)[TM][TN], const Operand& A, int64_t m0, const Operand& B,
                                              int64_t n0, int kchunks, int step0, int step1, char* lds) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -120,14 +137,14 @@ struct Tile {
     for (int i = 0; i < kCopiesB; ++i) vb[i] = (uint32_t)((crow + 8 * kWaves * i) * B.pitch) + 16u * chunk;
 
     __amdgpu_buffer_rsrc_t bsa, bsb;
-    constexpr int kSaCopies = Op::kScaled ? (BM * 2 + kThreads - 1) / kThreads : 0;
-    constexpr int kSbCopies = Op::kScaled ? (BN * 2 + kThreads - 1) / kThreads : 0;
     if constexpr (Op::kScaled) {
       bsa = buffer_of(A.scale + m0 * A.scale_pitch, (uint32_t)(ra * A.scale_pitch));
       bsb = buffer_of(B.scale + n0 * B.scale_pitch, (uint32_t)(rb * B.scale_pitch));
     }
+    char* const scales = lds + 2 * kDataBytes;
 
-    auto copy = [&](int step, char* st) __attribute__((always_inline)) {
+    auto copy = [&](int step) __attribute__((always_inline)) {
+      char* st = lds + ((step - step0) & 1) * kDataBytes;
       const bool in = step * kStepChunks + chunk < kchunks;
       const uint32_t soff = (uint32_t)step * kStepBytes;
 #pragma unroll
@@ -137,61 +154,99 @@ struct Tile {
       for (int i = 0; i < kCopiesB; ++i)
         copy16_to_lds(bufb, st + BM * kStepBytes + (wave + kWaves * i) * 1024, in ? vb[i] : kPastEnd, soff);
       if constexpr (Op::kScaled) {
-        // two dwords (8 codes) per row; a scale row is whole 16-byte groups
-        char* sc = st + kDataBytes;
-        const uint32_t ks = (uint32_t)step * kStepChunks + 4u * (threadIdx.x & 1);
+        // 16 codes of a row, those of this step and the next; a scale row is
+        // whole 16-byte groups
+        if (((step - step0) & 1) == 0) {
+          char* sc = scales + (((step - step0) >> 1) & 1) * kScaleBytes;
+          const uint32_t ks = (uint32_t)step * kStepChunks;
 #pragma unroll
-        for (int i = 0; i < kSaCopies; ++i) {
-          const int base = i * kThreads + wave * kWave;
-          if (base < BM * 2)
-            copy4_to_lds(bsa, sc + base * 4, (uint32_t)(((base + lane) >> 1) * A.scale_pitch) + ks, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kSbCopies; ++i) {
-          const int base = i * kThreads + wave * kWave;
-          if (base < BN * 2)
-            copy4_to_lds(bsb, sc + BM * 8 + base * 4, (uint32_t)(((base + lane) >> 1) * B.scale_pitch) + ks, 0);
+          for (int r0 = 0; r0 < kRows; r0 += kThreads) {
+            const int base = r0 + wave * kWave;              // 64 rows, all of one operand
+            if (base < BM) copy16_to_lds(bsa, sc + base * 16, (uint32_t)((base + lane) * A.scale_pitch) + ks, 0);
+            else if (base < kRows)
+              copy16_to_lds(bsb, sc + base * 16, (uint32_t)((base - BM + lane) * B.scale_pitch) + ks, 0);
+          }
         }
       }
     };
 
-    const int l16 = lane & 15, g = lane >> 4;
-    // byte offset in a 128-byte row of this lane's chunk of instruction s; fragments start at multiples of 16 rows
-    const int pos[2] = {((2 * g) ^ ((l16 >> 1) & 7)) * 16, ((2 * g + 1) ^ ((l16 >> 1) & 7)) * 16};
-    const int arow = wm * (BM / WM) + l16, brow = wn * (BN / WN) + l16;
-
-    copy(step0, lds);
-    for (int step = step0; step < step1; ++step) {
-      char* st = lds + ((step - step0) & 1) * kStageBytes;
-      __builtin_amdgcn_s_waitcnt(0x0f70);                    // vmcnt(0): this wavefront's part of the step is in LDS
-      __syncthreads();
-      if (step + 1 < step1) copy(step + 1, lds + ((step + 1 - step0) & 1) * kStageBytes);
-      int sa[TM], sb[TN];
+    const int l16 = lane & 15, pair = -(lane >> 4) & 3;
+    // byte offset in a 128-byte row of this lane's chunk of half s; fragments start at multiples of 16 rows
+    const int pos[2] = {((2 * pair) ^ ((l16 >> 1) & 7)) * 16, ((2 * pair + 1) ^ ((l16 >> 1) & 7)) * 16};
+    const int arow = wm * (BM / WM) + l16, brow = BM + wn * (BN / WN) + l16;
+    i32x4 a[2][TM], b[2][TN];
+    int sa[TM] = {}, sb[TN] = {}, na[TM] = {}, nb[TN] = {};
+    auto fetch = [&](int step, int s) __attribute__((always_inline)) {
+      const char* st = lds + ((step - step0) & 1) * kDataBytes + pos[s];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) a[s][i] = *reinterpret_cast<const i32x4*>(st + (arow + 16 * i) * kStepBytes);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) b[s][j] = *reinterpret_cast<const i32x4*>(st + (brow + 16 * j) * kStepBytes);
+    };
+    auto fetch_scales = [&](int step) __attribute__((always_inline)) {
       if constexpr (Op::kScaled) {
-        const char* sc = st + kDataBytes;
+        const int k = step - step0;
+        const char* sc = scales + ((k >> 1) & 1) * kScaleBytes + (k & 1) * 8 + 2 * pair;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = *reinterpret_cast<const uint16_t*>(sc + (arow + 16 * i) * 8 + 2 * g);
+        for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint16_t*>(sc + (arow + 16 * i) * 16);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) sb[j] = *reinterpret_cast<const uint16_t*>(sc + (BM + brow + 16 * j) * 8 + 2 * g);
+        for (int j = 0; j < TN; ++j) nb[j] = *reinterpret_cast<const uint16_t*>(sc + (brow + 16 * j) * 16);
       }
+    };
+    auto take_scales = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        i32x4 a[TM], b[TN];
+      for (int i = 0; i < TM; ++i) sa[i] = na[i];
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-          a[i] = *reinterpret_cast<const i32x4*>(st + (arow + 16 * i) * kStepBytes + pos[s]);
+      for (int j = 0; j < TN; ++j) sb[j] = nb[j];
+    };
+    auto multiply = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          b[j] = *reinterpret_cast<const i32x4*>(st + (BM + brow + 16 * j) * kStepBytes + pos[s]);
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int j = 0; j < TN; ++j) acc[i][j] = Op::mma(a[s][i], b[s][j], acc[i][j], s, sa[i], sb[j]);
+    };
+    // One LDS read between every few matrix instructions (bf16 at 8192 x 8192 x
+    // 4096: 392 us against 406 us as the compiler orders them).  The scaled
+    // instructions run faster as the compiler orders them (11008 x 8192 x 4096:
+    // 228 us against 235 us).
+    auto interleave = [&]() __attribute__((always_inline)) {
+      if constexpr (Op::kScaled) return;
+      constexpr int kMma = TM * TN * Op::kMmas, kReads = TM + TN;
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = Op::mma(a[i], b[j], acc[i][j], s, Op::kScaled ? sa[i] : 0, Op::kScaled ? sb[j] : 0);
+      for (int i = 0; i < kReads; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);               // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, kMma / kReads, 0);   // matrix instructions
       }
+    };
+
+    copy(step0);
+    if (step0 + 1 < step1) copy(step0 + 1);
+    __builtin_amdgcn_s_waitcnt(0x0f70);                      // vmcnt(0): this wavefront's copies are in LDS
+    __syncthreads();
+    fetch(step0, 0);
+    fetch_scales(step0);
+    for (int step = step0; step < step1; ++step) {
+      take_scales();
+      fetch(step, 1);
+      multiply(0);
+      interleave();
+      __builtin_amdgcn_s_waitcnt(0x0f70);
+      __syncthreads();
+      if (step + 2 < step1) copy(step + 2);
+      fetch(step + 1, 0);                                    // past the last step: stale, not used
+      fetch_scales(step + 1);
+      multiply(1);
+      interleave();
     }
   }
 };
+
+// The two tile shapes.  256 x 256 moves half as many operand bytes through
+// LDS per product; one workgroup fills a CU.  128 x 128 serves products with
+// too few large tiles; two workgroups share a CU.  8192 x 8192 x 4096 bf16:
+// 392 us (1.40 PFLOP/s) and 498 us.
+template <class Op> using LargeTile = Tile<Op, 256, 256, 4, 2>;
+template <class Op> using SmallTile = Tile<Op, 128, 128, 4, 2>;
 
 // Workgroup -> tile.  Consecutive workgroups go to the 8 XCDs in turn, each
 // with an L2 of its own: XCD x takes one contiguous run of tiles, and runs go
@@ -208,5 +263,33 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& t
   tn = first + in % width;
   tm = in / width;
 }
+
+// A tile of 16-bit results [BN rows n][BM columns m] in LDS, to be written out
+// in long runs along either axis.  Row n's 16-byte units are permuted by
+// f(n), so that all three accesses spread over the banks: 8-byte writes of 16
+// consecutive rows, 16-byte reads along a row, and 4-byte reads down 8 rows
+// by lanes 8 rows apart.
+template <int BM>
+struct Tile16 {
+  static_assert(BM == 64 || BM >= 128, "f stays below the units of a row");
+  static __device__ __forceinline__ int f(int n) {
+    if (BM == 64) return (n >> 3) & 7;
+    return (n & 1) | ((n >> 3) & 1) << 1 | ((n >> 1 ^ n >> 4) & 1) << 2 | ((n >> 2 ^ n >> 5) & 1) << 3;
+  }
+  static __device__ __forceinline__ char* at(char* lds, int n, int m) {
+    return lds + n * (BM * 2) + (((m >> 3) ^ f(n)) << 4) + (m & 7) * 2;
+  }
+  // columns m, m + 1 (m even) of rows n .. n + 7 (n a multiple of 8): 8 results of each column
+  static __device__ __forceinline__ void columns(char* lds, int n, int m, u32x4& c0, u32x4& c1) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const uint32_t*>(at(lds, n + k, m));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      c0[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x05040100);
+      c1[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], 0x07060302);
+    }
+  }
+};
 
 }  // namespace qamw
