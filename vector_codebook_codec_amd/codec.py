@@ -82,6 +82,30 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _matrix(t: torch.Tensor, name: str):
+    """Rows, columns and leading dimension of a matrix with unit column stride; an empty or one-row matrix has its
+    columns, or more, as leading dimension.  (Calls of a few microseconds: attributes are read once, in C.)"""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    n, d = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and d > 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return n, d, ld if n > 1 else d
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream) -> int:
+    """_stream, without building a Stream object for the current one."""
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(torch.cuda.current_device())
+    return _stream(stream)
+
+
 def _temporary(nbytes: int, device, stream) -> torch.Tensor:
     """A workspace that the caller does not see: kept from reuse until `stream`, where that is not the current one,
     has passed the call."""

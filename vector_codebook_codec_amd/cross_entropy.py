@@ -7,8 +7,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _WDT, _dev, _stream, _temporary, _vec
-from .mxfp4 import _pitch
+from .codec import _WDT, _dev, _matrix, _raw_stream, _temporary, _vec
 
 __all__ = [
     "qamw_cross_entropy",
@@ -27,8 +26,8 @@ def qamw_cross_entropy_grad_workspace_bytes(T: int, V: int, d: int, dtype=torch.
 
 
 def _head(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor):
-    T, d, ldh = _pitch(H, "H")
-    V, d2, ldw = _pitch(W, "W")
+    T, d, ldh = _matrix(H, "H")
+    V, d2, ldw = _matrix(W, "W")
     if d2 != d:
         raise ValueError("H [T][d] and W [V][d] must agree")
     if H.dtype not in _WDT or W.dtype != H.dtype:
@@ -51,11 +50,12 @@ def qamw_cross_entropy(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
     lib = _lib.load()
     dt = _WDT[H.dtype]
     if workspace is None:
-        workspace = _temporary(int(lib.qamw_cross_entropy_workspace_bytes(T, V, d, dt)), H.device, stream)
-    _dev(workspace, "workspace")
+        workspace = _temporary(lib.qamw_cross_entropy_workspace_bytes(T, V, d, dt), H.device, stream)
+    else:
+        _dev(workspace, "workspace")
     _lib.check("qamw_cross_entropy", lib.qamw_cross_entropy(
         H.data_ptr(), dt, T, d, ldh, W.data_ptr(), V, ldw, targets.data_ptr(), loss.data_ptr(), lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)))
     return loss, lse
 
 
@@ -74,20 +74,20 @@ def qamw_cross_entropy_grad(H: torch.Tensor, W: torch.Tensor, targets: torch.Ten
         dW = torch.empty((V, d), dtype=H.dtype, device=H.device)
     lddh = lddw = d
     if dH is not None:
-        n2, d2, lddh = _pitch(dH, "dH")
+        n2, d2, lddh = _matrix(dH, "dH")
         if (n2, d2) != (T, d) or dH.dtype != H.dtype:
             raise ValueError("dH must be T x d of H's dtype")
     if dW is not None:
-        n2, d2, lddw = _pitch(dW, "dW")
+        n2, d2, lddw = _matrix(dW, "dW")
         if (n2, d2) != (V, d) or dW.dtype != H.dtype:
             raise ValueError("dW must be V x d of H's dtype")
     lib = _lib.load()
     dt = _WDT[H.dtype]
     if workspace is None:
-        workspace = _temporary(int(lib.qamw_cross_entropy_grad_workspace_bytes(T, V, d, dt)), H.device, stream)
+        workspace = _temporary(lib.qamw_cross_entropy_grad_workspace_bytes(T, V, d, dt), H.device, stream)
     _dev(workspace, "workspace")
     _lib.check("qamw_cross_entropy_grad", lib.qamw_cross_entropy_grad(
         H.data_ptr(), dt, T, d, ldh, W.data_ptr(), V, ldw, targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
         None if dH is None else dH.data_ptr(), lddh, None if dW is None else dW.data_ptr(), lddw,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)))
     return dH, dW

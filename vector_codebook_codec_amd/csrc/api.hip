@@ -646,7 +646,7 @@ int32_t qamw_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64
 
 size_t qamw_mxfp4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) {
   if (T <= 0 || T > kMaxRows || N <= 0 || N > kMaxRows || d <= 0 || d > kMx4MaxDim) return 0;
-  return round_up((size_t)T * (size_t)mx4_blocks(d) * 16, 256) + round_up((size_t)T * (size_t)mx4_scale_bytes(d), 256);
+  return mx4_matmul_workspace_bytes(T, N, d);
 }
 
 int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, int64_t ldx, const uint8_t* codes,
@@ -693,7 +693,7 @@ static bool aligned4(const void* p) { return p && ((uintptr_t)p & 3u) == 0; }
 
 size_t qamw_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype) {
   if (T <= 0 || V <= 0 || d <= 0 || (dtype != QAMW_F32 && dtype != QAMW_BF16) || !ce_sizes_fit(T, V, d, dtype)) return 0;
-  return ce_workspace_bytes(T, V);
+  return ce_workspace_bytes(T, V, (int)d, dtype);
 }
 size_t qamw_cross_entropy_grad_workspace_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype) {
   if (T <= 0 || V <= 0 || d <= 0 || (dtype != QAMW_F32 && dtype != QAMW_BF16) || !ce_sizes_fit(T, V, d, dtype)) return 0;

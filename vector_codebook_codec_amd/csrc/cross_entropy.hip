@@ -55,6 +55,35 @@ __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f3
 // Tile statistics of the logits: part[tile][t] = (max, sum of exp(z - max)),
 // and the target's logit from the one tile that holds it.
 // ---------------------------------------------------------------------------
+// Of one 16-token column of fragments: token t (target y, -1 for none), lane
+// group l / 16 holding entries v + 16 i + r.  The result is the same in all
+// four lanes of a token.
+template <int TM, int TN>
+__device__ __forceinline__ float2 column_stats(f32x4 (&acc)[TM][TN], int j, int64_t v, int64_t V, int64_t t, int64_t y,
+                                               float* __restrict__ zt) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t e = v + 16 * i + r;
+      if (e >= V) acc[i][j][r] = -INFINITY;
+      m = fmaxf(m, acc[i][j][r]);
+      if (e == y && e < V) zt[t] = acc[i][j][r];
+    }
+  m = fmaxf(m, __shfl_xor(m, 16));
+  m = fmaxf(m, __shfl_xor(m, 32));
+  const float base = m == -INFINITY ? 0.0f : m;                     // a tile of -inf alone sums to 0
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s += exp_of(acc[i][j][r] - base);
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  return make_float2(m, s);
+}
+
 template <class Tl, class Op>
 __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Operand H, int kchunks, int tiles_m,
                                                                 int tiles_n, const int64_t* __restrict__ targets,
@@ -74,28 +103,8 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Opera
 #pragma unroll
   for (int j = 0; j < Tl::TN; ++j) {
     const int64_t t = n0 + tl + 16 * j;
-    const int64_t y = t < H.rows ? targets[t] : -1;
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t v = v0 + 16 * i + r;
-        if (v >= W.rows) acc[i][j][r] = -INFINITY;
-        m = fmaxf(m, acc[i][j][r]);
-        if (v == y && v < W.rows) zt[t] = acc[i][j][r];
-      }
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    const float base = m == -INFINITY ? 0.0f : m;                   // a tile of -inf alone sums to 0
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < Tl::TM; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s += exp_of(acc[i][j][r] - base);
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lane < 16) red[wm * Tl::BN + tl + 16 * j] = make_float2(m, s);
+    const float2 s = column_stats(acc, j, v0, W.rows, t, t < H.rows ? targets[t] : -1, zt);
+    if (lane < 16) red[wm * Tl::BN + tl + 16 * j] = s;
   }
   __syncthreads();
   for (int k = threadIdx.x; k < Tl::BN; k += Tl::kThreads) {
@@ -110,33 +119,60 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Opera
   }
 }
 
-// Joins the tiles' statistics: 16 tokens a workgroup, 16 threads a token,
-// thread k takes tiles k, k + 16, ...; then the 16 in order.
+// The same for up to 16 TF tokens, a tile of 16 RF vocabulary entries.
+template <class Op, int RF, int TF, int U>
+__global__ __launch_bounds__(kThinThreads) void ce_stats_thin_kernel(Operand W, Operand H, int kchunks,
+                                                                     const int64_t* __restrict__ targets,
+                                                                     float2* __restrict__ part, float* __restrict__ zt) {
+  __shared__ __align__(16) char red[thin_lds_bytes<RF, TF>()];
+  const int64_t m0 = (int64_t)blockIdx.x * (16 * RF);
+  f32x4 acc[RF][TF] = {};
+  thin_run<Op, RF, TF, U>(acc, W, m0, H, kchunks);
+  thin_sum(acc, red);
+  if (threadIdx.x >= kWave) return;
+  const int lane = threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < TF; ++j) {
+    const int64_t t = 16 * j + (lane & 15);
+    const float2 s = column_stats(acc, j, m0 + 4 * (lane >> 4), W.rows, t, t < H.rows ? targets[t] : -1, zt);
+    if (lane < 16 && t < H.rows) part[blockIdx.x * H.rows + t] = s;
+  }
+}
+
+// Joins the tiles' statistics: TB tokens a workgroup and 256 / TB threads a
+// token, thread k taking tiles k, k + 256 / TB, ...; then those in order.
+template <int TB>
 __global__ __launch_bounds__(256) void ce_finish_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
                                                         const int64_t* __restrict__ targets, int64_t T, int64_t V,
                                                         int tiles, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 red[16][16];
-  const int k = threadIdx.x >> 4, i = threadIdx.x & 15;
-  const int64_t t = (int64_t)blockIdx.x * 16 + i;
-  float m = -INFINITY;
-  double s = 0.0;
+  constexpr int kParts = 256 / TB;
+  __shared__ float2 red[kParts][TB];
+  const int k = threadIdx.x / TB, i = threadIdx.x % TB;
+  const int64_t t = (int64_t)blockIdx.x * TB + i;
+  float m = -INFINITY, s = 0.0f;
   if (t < T) {
-    for (int q = k; q < tiles; q += 16) m = fmaxf(m, part[(int64_t)q * T + t].x);
-    const float base = m == -INFINITY ? 0.0f : m;
-    for (int q = k; q < tiles; q += 16) {
+#pragma unroll 8
+    for (int q = k; q < tiles; q += kParts) {
       const float2 p = part[(int64_t)q * T + t];
-      s += (double)p.y * (double)exp_of(p.x - base);
+      const float top = fmaxf(m, p.x), base = top == -INFINITY ? 0.0f : top;
+      s = s * exp_of(m - base) + p.y * exp_of(p.x - base);
+      m = top;
     }
   }
-  red[k][i] = make_float2(m, (float)s);
-  __syncthreads();
+  red[k][i] = make_float2(m, s);
+  // pairs at distance kParts / 2, kParts / 4, ..., 1
+#pragma unroll
+  for (int h = kParts / 2; h; h >>= 1) {
+    __syncthreads();
+    if (k < h) {
+      const float2 a = red[k][i], b = red[k + h][i];
+      const float top = fmaxf(a.x, b.x), base = top == -INFINITY ? 0.0f : top;
+      red[k][i] = make_float2(top, a.y * exp_of(a.x - base) + b.y * exp_of(b.x - base));
+    }
+  }
   if (k == 0 && t < T) {
-    m = red[0][i].x;
-    for (int q = 1; q < 16; ++q) m = fmaxf(m, red[q][i].x);
-    const float base = m == -INFINITY ? 0.0f : m;
-    s = 0.0;
-    for (int q = 0; q < 16; ++q) s += (double)red[q][i].y * (double)exp_of(red[q][i].x - base);
-    const float l = base + logf((float)s);
+    const float2 a = red[0][i];
+    const float l = (a.x == -INFINITY ? 0.0f : a.x) + logf(a.y);
     const int64_t y = targets[t];
     lse[t] = l;
     loss[t] = (y >= 0 && y < V) ? l - zt[t] : 0.0f;
@@ -356,10 +392,36 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(E* __restrict__ out, int64
 // ===========================================================================
 static unsigned blocks_for(int64_t n, int per) { return (unsigned)std::min<int64_t>((n + per - 1) / per, 65536); }
 
-size_t ce_workspace_bytes(int64_t T, int64_t V) {
-  return round_up((size_t)tiles_of(V, kSmallTile) * T * sizeof(float2), 256) + round_up((size_t)T * sizeof(float), 256);
+// Up to this many tokens the loss reads the head in thin tiles.  V = 32000,
+// d = 4096, bf16: 69.6 us thin at 16 tokens; at 32, 77.2 us thin against 70.6
+// us in 64 x 64 tiles.
+constexpr int64_t kThinTokens = 16;
+// Vocabulary entries of a thin tile: 16 for a few tokens (T = 1: 56.9 us
+// against 62.7 us with 64), 64 where the hidden states that every tile reads
+// weigh more (T = 16: 69.6 us against 83.5 us with 16).
+constexpr int64_t kFewTokens = 4;
+
+static ProductType product_type(int es) { return es == 4 ? kProductF32 : kProductBf16; }
+static int64_t steps_of(int64_t elements, int es) { return tiles_of(elements * es, kStepBytes); }
+// tile shape of the logits, and its vocabulary entries
+static int logits_shape(int64_t T, int64_t V, int d, int es) { return product_plan(product_type(es), V, T, steps_of(d, es), 1).shape; }
+static int logits_tile(int64_t T, int64_t V, int d, int es) {
+  return T <= kFewTokens ? 16 : T <= kThinTokens ? 64 : kShapeTile[logits_shape(T, V, d, es)];
+}
+size_t ce_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt) {
+  return round_up((size_t)tiles_of(V, logits_tile(T, V, d, elem_size(dt))) * T * sizeof(float2), 256) +
+         round_up((size_t)T * sizeof(float), 256);
 }
 
+static int ce_finish(const float2* part, const float* zt, const int64_t* targets, int64_t T, int64_t V, int tiles, float* loss,
+                     float* lse, hipStream_t st) {
+  if (T <= 64)
+    hipLaunchKernelGGL(ce_finish_kernel<1>, dim3((unsigned)T), dim3(256), 0, st, part, zt, targets, T, V, tiles, loss, lse);
+  else
+    hipLaunchKernelGGL(ce_finish_kernel<16>, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, st, part, zt, targets, T, V,
+                       tiles, loss, lse);
+  return check_launch("ce_finish_kernel");
+}
 template <class Op, class Tl>
 static int ce_tiled(const Operand& W, const Operand& H, int kchunks, const int64_t* targets, float* loss, float* lse,
                     void* ws, hipStream_t st) {
@@ -370,19 +432,30 @@ static int ce_tiled(const Operand& W, const Operand& H, int kchunks, const int64
   auto kernel = ce_stats_kernel<Tl, Op>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, H, kchunks, tm, tn,
                      targets, part, zt);
-  int rc = check_launch("ce_stats_kernel");
-  if (rc) return rc;
-  hipLaunchKernelGGL(ce_finish_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), 0, st, part, zt, targets, T, W.rows, tm,
-                     loss, lse);
-  return check_launch("ce_finish_kernel");
+  const int rc = check_launch("ce_stats_kernel");
+  return rc ? rc : ce_finish(part, zt, targets, T, W.rows, tm, loss, lse, st);
+}
+template <class Op, int RF, int TF, int U>
+static int ce_thin(const Operand& W, const Operand& H, int kchunks, const int64_t* targets, float* loss, float* lse, void* ws,
+                   hipStream_t st) {
+  const int tm = (int)tiles_of(W.rows, 16 * RF);
+  const int64_t T = H.rows;
+  float2* part = (float2*)ws;
+  float* zt = (float*)((char*)ws + round_up((size_t)tm * T * sizeof(float2), 256));
+  hipLaunchKernelGGL((ce_stats_thin_kernel<Op, RF, TF, U>), dim3((unsigned)tm), dim3(kThinThreads), 0, st, W, H, kchunks, targets,
+                     part, zt);
+  const int rc = check_launch("ce_stats_thin_kernel");
+  return rc ? rc : ce_finish(part, zt, targets, T, W.rows, tm, loss, lse, st);
 }
 template <class Op>
 static int ce_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                  const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
   const int es = sizeof(typename Elem<Op>::T), kchunks = d / Op::kElems;
   const Operand a = {(const char*)W, ldw * es, V, nullptr, 0}, b = {(const char*)H, ldh * es, T, nullptr, 0};
-  return large_tiles_pay(V, T) ? ce_tiled<Op, LargeTile<Op>>(a, b, kchunks, targets, loss, lse, ws, st)
-                               : ce_tiled<Op, SmallTile<Op>>(a, b, kchunks, targets, loss, lse, ws, st);
+  if (T <= kFewTokens) return ce_thin<Op, 1, 1, 4>(a, b, kchunks, targets, loss, lse, ws, st);
+  if (T <= kThinTokens) return ce_thin<Op, 4, 1, 2>(a, b, kchunks, targets, loss, lse, ws, st);
+  return with_shape<Op>(logits_shape(T, V, d, es),
+                        [&](auto tile) { return ce_tiled<Op, decltype(tile)>(a, b, kchunks, targets, loss, lse, ws, st); });
 }
 int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                          const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
@@ -394,6 +467,7 @@ int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ld
 // last round of workgroups that fills the CUs badly: T = 4096, V = 131072,
 // d = 4096 takes 15.1 ms at 128 MiB, 14.7 ms at 420 MiB and 14.5 ms at
 // 820 MiB.
+constexpr int64_t kPieceTile = kShapeTile[kShapes - 1];
 constexpr int64_t kCeBudget = (int64_t)512 << 20;
 // Sizes and places of the gradient's workspace.
 struct CeGradPlan {
@@ -408,17 +482,17 @@ static CeGradPlan ce_grad_plan(int64_t T, int64_t V, int d, int es) {
   // over the CUs where a round is no more than that (T = 4096: 16 tiles of
   // tokens by 16 of vocabulary), then evened out over the pieces.
   const int64_t budget = kCeBudget;
-  int64_t fit = std::min<int64_t>(budget / ((2 * T + d) * es), kMaxRowBytes / es) / kLargeTile;   // tiles
+  int64_t fit = std::min<int64_t>(budget / ((2 * T + d) * es), kMaxRowBytes / es) / kPieceTile;   // tiles
   fit = std::max<int64_t>(fit, 1);
   int64_t round = kCus;
-  for (int64_t tn = tiles_of(T, kLargeTile); round > 1 && tn % 2 == 0; tn /= 2) round /= 2;
+  for (int64_t tn = tiles_of(T, kPieceTile); round > 1 && tn % 2 == 0; tn /= 2) round /= 2;
   if (round <= fit) fit = fit / round * round;
   else round = 1;
-  const int64_t all = tiles_of(V, kLargeTile), pieces = tiles_of(all, fit);
-  p.piece = std::min<int64_t>(tiles_of(tiles_of(all, pieces), round) * round * kLargeTile, (V + 7) / 8 * 8);
+  const int64_t all = tiles_of(V, kPieceTile), pieces = tiles_of(all, fit);
+  p.piece = std::min<int64_t>(tiles_of(tiles_of(all, pieces), round) * round * kPieceTile, (V + 7) / 8 * 8);
   p.vp = p.piece;
   p.tp = (T + 7) / 8 * 8;
-  p.dh = product_plan(d, T, (p.vp * es + kStepBytes - 1) / kStepBytes, es == 4 ? kStepUsF32 : kStepUsBf16);
+  p.dh = product_plan(product_type(es), d, T, steps_of(p.vp, es), 16);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += round_up(bytes, 256); return o; };
   p.unit = take(sizeof(float));
@@ -455,8 +529,9 @@ static int product_tiled(const Operand& A, const Operand& B, int kchunks, int sp
 template <class Op, class Out>
 static int product(const Operand& A, const Operand& B, int kchunks, const ProductPlan& p, const float* unit, Out* C,
                    int64_t ldc, int64_t split_stride, bool add, hipStream_t st) {
-  return p.large ? product_tiled<LargeTile<Op>, Out>(A, B, kchunks, p.splits, unit, C, ldc, split_stride, add, st)
-                 : product_tiled<SmallTile<Op>, Out>(A, B, kchunks, p.splits, unit, C, ldc, split_stride, add, st);
+  return with_shape<Op>(p.shape, [&](auto tile) {
+    return product_tiled<decltype(tile), Out>(A, B, kchunks, p.splits, unit, C, ldc, split_stride, add, st);
+  });
 }
 
 template <class Op>
@@ -484,13 +559,13 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
     const Operand Wp = {(const char*)W + v0 * ldw * es, ldw * es, n, nullptr, 0};
     const Operand Hp = {(const char*)H, ldh * es, T, nullptr, 0};
     const int kd = d / Op::kElems;
-    rc = large_tiles_pay(n, T)
-             ? softmax_grad_tiled<Op, LargeTile<Op>>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt, p.tp, st)
-             : softmax_grad_tiled<Op, SmallTile<Op>>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt, p.tp, st);
+    rc = with_shape<Op>(logits_shape(T, n, d, es), [&](auto tile) {
+      return softmax_grad_tiled<Op, decltype(tile)>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt, p.tp, st);
+    });
     if (rc) return rc;
     if (dW) {
       const Operand a = {(const char*)Ht, p.tp * es, d, nullptr, 0}, b = {(const char*)Gt, p.tp * es, n, nullptr, 0};
-      const ProductPlan whole = {large_tiles_pay(d, n), 1};
+      const ProductPlan whole = product_plan(product_type(es), d, n, steps_of(p.tp, es), 1);
       if ((rc = product<Op, E>(a, b, (int)(p.tp / Op::kElems), whole, unit, (E*)dW + v0 * lddw, lddw, 0, false, st))) return rc;
     }
     if (dH) {

@@ -159,41 +159,69 @@ int launch_mx4_quantize(const void* W, int32_t wdt, int64_t N, int d, int64_t ld
                         void* values, int32_t vdt, int64_t ldv, hipStream_t st);
 int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N, int d, void* W, int32_t odt,
                           int64_t ldo, hipStream_t st);
+size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st);
 
-// Tiles of a product (tile_product.h).  256 CUs run one large tile or two
-// small ones each; a pair of small tiles takes 0.64 of a large one's time per
-// K step (measured at 8192 x 8192 x 4096: 498 us for 8 rounds of pairs,
-// 392 us for 4 rounds of large tiles).
-constexpr int kLargeTile = 256, kSmallTile = 128, kCus = 256;
-inline int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
-inline bool large_tiles_pay(int64_t M, int64_t N) {
-  const int64_t large = tiles_of(tiles_of(M, kLargeTile) * tiles_of(N, kLargeTile), kCus);
-  const int64_t pairs = tiles_of(tiles_of(M, kSmallTile) * tiles_of(N, kSmallTile), 2 * kCus);
-  return 100 * large <= 64 * pairs;
+// ---- how a product [M][N] is cut into square tiles (tile_product.h).
+// The measured time of one K step (128 bytes of every row), in microseconds,
+// where every CU has L tiles of a shape to work on, for L = 1, 2 and per tile
+// beyond (M = 16 and N = 16 L tiles, 2048 to 8192 columns).  Small tiles
+// share a CU; they are for products that have too few large ones.
+enum ProductType { kProductBf16, kProductF32, kProductMx4 };
+constexpr int kCus = 256, kShapes = 3;
+constexpr int kShapeTile[kShapes] = {64, 128, 256};
+constexpr float kShapeStepUs[3][kShapes][3] = {
+    {{0.51f, 0.51f, 0.19f}, {0.74f, 0.98f, 0.49f}, {1.60f, 3.15f, 1.58f}},
+    {{0.62f, 1.09f, 0.50f}, {2.02f, 3.79f, 1.89f}, {7.47f, 15.0f, 7.48f}},
+    {{0.45f, 0.64f, 0.24f}, {0.92f, 1.27f, 0.60f}, {1.98f, 3.84f, 1.91f}}};
+inline int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+inline double step_us(ProductType t, int shape, int64_t load) {
+  const float* f = kShapeStepUs[t][shape];
+  return load <= 0 ? 0.0 : load <= 2 ? f[load - 1] : f[2] * (double)load > f[1] ? f[2] * (double)load : f[1];
 }
-// How a product [M][N] of `steps` K steps is cut: tile shape, and into how
-// many fp32 partial results along K (1, 2, 4, 8 or 16), by the estimated time:
-// rounds of workgroups times K steps, plus writing and reading the partial
-// results at 4 TB/s.  step_us: a large tile's K step with all CUs busy
-// (measured, microseconds).
-constexpr float kStepUsBf16 = 1.5f, kStepUsF32 = 7.4f, kStepUsMx4 = 2.0f;
+inline int64_t shape_tiles(int shape, int64_t M, int64_t N) {
+  return tiles_of(M, kShapeTile[shape]) * tiles_of(N, kShapeTile[shape]);
+}
+// writing and reading fp32 partial results at 4 TB/s, and the launch that adds them
+inline double partials_us(double elements) { return 3.0 + elements * 8e-6 / 4.0; }
+
 struct ProductPlan {
-  bool large;
-  int splits;
+  int shape;
+  int splits;                      // along K, of every tile: as many fp32 results, added later
 };
-inline ProductPlan product_plan(int64_t M, int64_t N, int64_t steps, float step_us) {
-  ProductPlan best = {large_tiles_pay(M, N), 1};
+inline ProductPlan product_plan(ProductType t, int64_t M, int64_t N, int64_t steps, int most_splits) {
+  ProductPlan best = {0, 1};
   double best_us = 1e30;
-  for (int s = 1; s <= 16; s *= 2) {
-    if (s > 1 && steps < 8 * s) break;                 // at least 8 steps a workgroup
-    for (int large = 0; large < 2; ++large) {
-      const int tile = large ? kLargeTile : kSmallTile;
-      const int64_t wgs = tiles_of(M, tile) * tiles_of(N, tile) * s;
-      const double rounds = large ? (double)tiles_of(wgs, kCus) : 0.64 * (double)tiles_of(wgs, 2 * kCus);
-      const double us = rounds * step_us * (double)tiles_of(steps, s) + (s > 1 ? (double)s * M * N * 8e-6 / 4.0 : 0.0);
-      if (us < 0.98 * best_us) best_us = us, best = {large != 0, s};
+  for (int s = 1; s <= most_splits; s *= 2) {
+    if (s > 1 && steps < 4 * s) break;                 // at least 4 steps a workgroup
+    for (int shape = kShapes - 1; shape >= 0; --shape) {
+      const double us = step_us(t, shape, tiles_of(shape_tiles(shape, M, N) * s, kCus)) * (double)tiles_of(steps, s) +
+                        (s > 1 ? partials_us((double)s * M * N) : 0.0);
+      if (us < 0.98 * best_us) best_us = us, best = {shape, s};
+    }
+  }
+  return best;
+}
+
+// For a result that is written once: `whole` tiles run over all of K; the
+// rest, too few to give every CU one more, are split along K.
+struct TailPlan {
+  int shape;
+  int64_t whole;
+  int splits;                      // of each tile past `whole`
+};
+inline TailPlan tail_plan(ProductType t, int64_t M, int64_t N, int64_t steps) {
+  TailPlan best = {0, 0, 1};
+  double best_us = 1e30;
+  for (int shape = kShapes - 1; shape >= 0; --shape) {
+    const int64_t n = shape_tiles(shape, M, N), full = n / kCus, rem = n % kCus;
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && (rem * s > kCus || rem == 0 || steps < 4 * s)) break;
+      // the CUs work on full + 1 tiles until the split ones end, then on the others
+      const double us = (double)steps * (step_us(t, shape, full + (rem ? 1 : 0)) / s + step_us(t, shape, full) * (1.0 - 1.0 / s)) +
+                        (s > 1 ? partials_us((double)s * rem * kShapeTile[shape] * kShapeTile[shape]) : 0.0);
+      if (us < 0.97 * best_us) best_us = us, best = {shape, s > 1 ? n - rem : n, s};
     }
   }
   return best;
@@ -203,7 +231,7 @@ inline ProductPlan product_plan(int64_t M, int64_t N, int64_t steps, float step_
 constexpr int64_t kMaxRowBytes = int64_t(1) << 22;
 
 // ---- vocabulary cross entropy (cross_entropy.hip)
-size_t ce_workspace_bytes(int64_t T, int64_t V);
+size_t ce_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt);
 size_t ce_grad_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt);
 int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                          const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st);

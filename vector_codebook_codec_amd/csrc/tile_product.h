@@ -28,6 +28,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "qamw_device.h"
 #include "qamw_internal.h"
 
@@ -241,27 +243,41 @@ struct Tile {
   }
 };
 
-// The two tile shapes.  256 x 256 moves half as many operand bytes through
-// LDS per product; one workgroup fills a CU.  128 x 128 serves products with
-// too few large tiles; two workgroups share a CU.  8192 x 8192 x 4096 bf16:
-// 392 us (1.40 PFLOP/s) and 498 us.
-template <class Op> using LargeTile = Tile<Op, 256, 256, 4, 2>;
-template <class Op> using SmallTile = Tile<Op, 128, 128, 4, 2>;
+// The tile shapes (qamw_internal.h says when each is taken).  The larger a
+// tile, the fewer operand bytes go through LDS per product: at 8192 x 8192 x
+// 4096 in bf16, 392 us (1.40 PFLOP/s) and 498 us with 256 and 128.  One
+// workgroup of 256 x 256, two of 128 x 128, five of 64 x 64 share a CU.
+template <class Op, int kShape> struct ShapeTile;
+template <class Op> struct ShapeTile<Op, 0> { typedef Tile<Op, 64, 64, 2, 2> T; };
+template <class Op> struct ShapeTile<Op, 1> { typedef Tile<Op, 128, 128, 4, 2> T; };
+template <class Op> struct ShapeTile<Op, 2> { typedef Tile<Op, 256, 256, 4, 2> T; };
+
+// f(Tile()) for a shape chosen at run time
+template <class Op, class F>
+inline int with_shape(int shape, F&& f) {
+  if (shape == 2) return f(typename ShapeTile<Op, 2>::T());
+  if (shape == 1) return f(typename ShapeTile<Op, 1>::T());
+  return f(typename ShapeTile<Op, 0>::T());
+}
 
 // Workgroup -> tile.  Consecutive workgroups go to the 8 XCDs in turn, each
-// with an L2 of its own: XCD x takes one contiguous run of tiles, and runs go
-// through groups of 8 tiles of B (n) by all tiles of A (m), m fastest inside
-// a column of the group, so that the tiles that an XCD works on at one time
-// share rows of both operands.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int total = tiles_m * tiles_n;
-  const int x = id % 8, q = total / 8, rem = total % 8;
-  const int t = x * q + (x < rem ? x : rem) + id / 8;
+// with an L2 of its own: XCD x takes one contiguous run of the `count` places.
+// Places go through groups of 8 tiles of B (n) by all tiles of A (m), n
+// fastest, so that the tiles that an XCD works on at one time share rows of
+// both operands.
+__device__ __forceinline__ int xcd_place(int id, int count) {
+  const int x = id % 8, q = count / 8, rem = count % 8;
+  return x * q + (x < rem ? x : rem) + id / 8;
+}
+__device__ __forceinline__ void tile_at(int place, int tiles_m, int tiles_n, int& tm, int& tn) {
   constexpr int kGroup = 8;
-  const int group = t / (kGroup * tiles_m), in = t % (kGroup * tiles_m);
+  const int group = place / (kGroup * tiles_m), in = place % (kGroup * tiles_m);
   const int first = group * kGroup, width = tiles_n - first < kGroup ? tiles_n - first : kGroup;
   tn = first + in % width;
   tm = in / width;
+}
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  tile_at(xcd_place(id, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
 }
 
 // A tile of 16-bit results [BN rows n][BM columns m] in LDS, to be written out
@@ -291,5 +307,84 @@ struct Tile16 {
     }
   }
 };
+
+// ---------------------------------------------------------------------------
+// Products with few rows of B: bound by reading A once.  A workgroup of 8
+// wavefronts takes 16 RF rows of A and all rows of B (at most 16 TF); the
+// wavefronts split K and load their fragments straight from global memory in
+// matrix-instruction layout, many loads ahead and with no barrier until their
+// sums are added, in a fixed order, in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kThinWaves = 8, kThinThreads = kThinWaves * kWave;
+template <int RF, int TF> constexpr int thin_lds_bytes() { return kThinWaves / 2 * RF * TF * kWave * 16; }
+
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
+}
+
+// Sum of the wavefronts' results, in wavefront 0: 4 + 4, 2 + 2, 1 + 1.
+template <int RF, int TF>
+__device__ __forceinline__ void thin_sum(f32x4 (&acc)[RF][TF], char* lds) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int h = kThinWaves / 2; h; h >>= 1) {
+    f32x4* red = reinterpret_cast<f32x4*>(lds) + (wave & (h - 1)) * RF * TF * kWave + lane;
+    if (wave >= h && wave < 2 * h)
+#pragma unroll
+      for (int i = 0; i < RF * TF; ++i) red[i * kWave] = acc[i / TF][i % TF];
+    __syncthreads();
+    if (wave < h)
+#pragma unroll
+      for (int i = 0; i < RF * TF; ++i) acc[i / TF][i % TF] += red[i * kWave];
+    __syncthreads();
+  }
+}
+
+// acc of this wavefront's share of K, unscaled operands: 4 chunks of every row
+// a unit, chunk 4 u + l / 16 in lane l; U units a batch, the next batch in
+// flight while one is multiplied.
+template <class Op, int RF, int TF, int U>
+__device__ __forceinline__ void thin_run(f32x4 (&acc)[RF][TF], const Operand& A, int64_t m0, const Operand& B, int kchunks) {
+  const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t row_bytes = (uint32_t)kchunks * 16u;
+  const int64_t ra = A.rows - m0 < 16 * RF ? A.rows - m0 : 16 * RF;
+  const __amdgpu_buffer_rsrc_t bufa = buffer_of(A.p + m0 * A.pitch, (uint32_t)((ra - 1) * A.pitch) + row_bytes);
+  const __amdgpu_buffer_rsrc_t bufb = buffer_of(B.p, (uint32_t)((B.rows - 1) * B.pitch) + row_bytes);
+  const uint32_t va = (uint32_t)l16 * (uint32_t)A.pitch + 16u * g, vb = (uint32_t)l16 * (uint32_t)B.pitch + 16u * g;
+  const int units = (kchunks + 3) / 4, per = (units + kThinWaves - 1) / kThinWaves;
+  const int u0 = min(wave * per, units), u1 = min(u0 + per, units);
+  i32x4 a[2][U][RF], b[2][U][TF];
+  auto load = [&](int u, auto set) __attribute__((always_inline)) {
+    constexpr int S = decltype(set)::value;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const bool in = u + k < u1 && 4 * (u + k) + g < kchunks;
+      const uint32_t soff = u + k < u1 ? (uint32_t)(u + k) * 64u : 0u;      // below every buffer's size
+#pragma unroll
+      for (int i = 0; i < RF; ++i) a[S][k][i] = load16(bufa, in ? va + (uint32_t)(16 * i) * (uint32_t)A.pitch : kPastEnd, soff);
+#pragma unroll
+      for (int j = 0; j < TF; ++j) b[S][k][j] = load16(bufb, in ? vb + (uint32_t)(16 * j) * (uint32_t)B.pitch : kPastEnd, soff);
+    }
+  };
+  auto multiply = [&](auto set) __attribute__((always_inline)) {
+    constexpr int S = decltype(set)::value;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int i = 0; i < RF; ++i)
+#pragma unroll
+        for (int j = 0; j < TF; ++j) acc[i][j] = Op::mma(a[S][k][i], b[S][k][j], acc[i][j], 0, 0, 0);
+  };
+  typedef std::integral_constant<int, 0> S0;
+  typedef std::integral_constant<int, 1> S1;
+  load(u0, S0());
+  for (int u = u0; u < u1; u += 2 * U) {
+    load(u + U, S1());
+    multiply(S0());
+    load(u + 2 * U, S0());
+    multiply(S1());
+  }
+}
 
 }  // namespace qamw

@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _ODT, _dev, _rows, _stream, _temporary
+from .codec import _ODT, _WDT, _dev, _matrix, _raw_stream, _temporary
 
 __all__ = [
     "qamw_mxfp4_dequantize",
@@ -35,22 +35,21 @@ def qamw_mxfp4_matmul_workspace_bytes(T: int, N: int, d: int) -> int:
     return int(_lib.load().qamw_mxfp4_matmul_workspace_bytes(T, N, d))
 
 
-def _pitch(W: torch.Tensor, name: str):
-    """Rows, columns and a leading dimension of at least the columns (an empty or one-row matrix has none of its own)."""
-    n, d, ld = _rows(W, name)
-    return n, d, max(ld, d) if n <= 1 else ld
+def _sizes(d: int):
+    """Bytes of a row of codes and of a row of scales (the library's qamw_mxfp4_row_bytes and _scale_bytes)."""
+    if not 1 <= d <= 1 << 20:
+        raise ValueError(f"unsupported d={d}")
+    blocks = (d + 31) >> 5
+    return blocks << 4, (blocks + 15) & ~15
 
 
 def _quantised(codes: torch.Tensor, scales: torch.Tensor, d: int) -> int:
-    _dev(codes, "codes")
-    _dev(scales, "scales")
-    lib = _lib.load()
-    rb, sb = int(lib.qamw_mxfp4_row_bytes(d)), int(lib.qamw_mxfp4_scale_bytes(d))
-    if rb < 0:
-        raise ValueError(f"unsupported d={d}")
+    rb, sb = _sizes(d)
     N = codes.shape[0] if codes.dim() == 2 else -1
     for t, name, width in ((codes, "codes", rb), (scales, "scales", sb)):
-        if t.dtype != torch.uint8 or tuple(t.shape) != (N, width) or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.dtype is not torch.uint8 or t.shape != (N, width) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous uint8 tensor of {width} columns (d={d}), a row per matrix row")
     return N
 
@@ -59,29 +58,32 @@ def qamw_mxfp4_quantize(W: torch.Tensor, values_dtype=None, codes: Optional[torc
                         scales: Optional[torch.Tensor] = None, values: Optional[torch.Tensor] = None, stream=None):
     """W [N][d] (fp32, bf16 or fp16) -> (codes, scales), or (codes, scales, values) when values_dtype or values is
     given: values [N][d] is what the codes stand for, as qamw_output_error's W_hat."""
-    N, d, ldw = _pitch(W, "W")
-    if W.dtype not in _ODT:
+    N, d, ldw = _matrix(W, "W")
+    wdt = _ODT.get(W.dtype)
+    if wdt is None:
         raise ValueError("W must be float32, bfloat16 or float16")
-    lib = _lib.load()
-    rb = int(lib.qamw_mxfp4_row_bytes(d))
-    if rb < 0:
-        raise ValueError(f"unsupported d={d}")
-    if codes is None:
+    rb, sb = _sizes(d)
+    if codes is None and scales is None:
         codes = torch.empty((N, rb), dtype=torch.uint8, device=W.device)
-    if scales is None:
-        scales = torch.empty((N, int(lib.qamw_mxfp4_scale_bytes(d))), dtype=torch.uint8, device=W.device)
-    if _quantised(codes, scales, d) != N:
-        raise ValueError(f"codes and scales must have {N} rows")
-    if values is None and values_dtype is not None:
-        values = torch.empty((N, d), dtype=values_dtype, device=W.device)
-    vptr, vdt, ldv = None, _lib.QAMW_F32, d
-    if values is not None:
-        n2, d2, ldv = _pitch(values, "values")
-        if (n2, d2) != (N, d) or values.dtype not in _ODT or (values_dtype or values.dtype) != values.dtype:
+        scales = torch.empty((N, sb), dtype=torch.uint8, device=W.device)
+    else:
+        codes = torch.empty((N, rb), dtype=torch.uint8, device=W.device) if codes is None else codes
+        scales = torch.empty((N, sb), dtype=torch.uint8, device=W.device) if scales is None else scales
+        if _quantised(codes, scales, d) != N:
+            raise ValueError(f"codes and scales must have {N} rows")
+    vptr, vdt, ldv = None, 0, d
+    if values is not None or values_dtype is not None:
+        if values is None:
+            values = torch.empty((N, d), dtype=values_dtype, device=W.device)
+        n2, d2, ldv = _matrix(values, "values")
+        vdt = _ODT.get(values.dtype)
+        if n2 != N or d2 != d or vdt is None or (values_dtype or values.dtype) != values.dtype:
             raise ValueError("values must be N x d of values_dtype: float32, bfloat16 or float16")
-        vptr, vdt = values.data_ptr(), _ODT[values.dtype]
-    _lib.check("qamw_mxfp4_quantize", lib.qamw_mxfp4_quantize(
-        W.data_ptr(), _ODT[W.dtype], N, d, ldw, codes.data_ptr(), scales.data_ptr(), vptr, vdt, ldv, _stream(stream)))
+        vptr = values.data_ptr()
+    status = _lib.load().qamw_mxfp4_quantize(W.data_ptr(), wdt, N, d, ldw, codes.data_ptr(), scales.data_ptr(), vptr, vdt,
+                                             ldv, _raw_stream(stream))
+    if status:
+        _lib.check("qamw_mxfp4_quantize", status)
     return (codes, scales) if values is None else (codes, scales, values)
 
 
@@ -91,11 +93,14 @@ def qamw_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int, out
     N = _quantised(codes, scales, d)
     if out is None:
         out = torch.empty((N, d), dtype=out_dtype, device=codes.device)
-    n2, d2, ldo = _pitch(out, "out")
-    if (n2, d2) != (N, d) or out.dtype not in _ODT:
+    n2, d2, ldo = _matrix(out, "out")
+    odt = _ODT.get(out.dtype)
+    if n2 != N or d2 != d or odt is None:
         raise ValueError("out must be N x d of float32, bfloat16 or float16")
-    _lib.check("qamw_mxfp4_dequantize", _lib.load().qamw_mxfp4_dequantize(
-        codes.data_ptr(), scales.data_ptr(), N, d, out.data_ptr(), _ODT[out.dtype], ldo, _stream(stream)))
+    status = _lib.load().qamw_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), N, d, out.data_ptr(), odt, ldo,
+                                               _raw_stream(stream))
+    if status:
+        _lib.check("qamw_mxfp4_dequantize", status)
     return out
 
 
@@ -104,20 +109,24 @@ def qamw_mxfp4_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                       stream=None) -> torch.Tensor:
     """Y [T][N] = X^ W^^T in out_dtype (fp32 or bf16): W^ the quantised matrix, X^ the activations X [T][d] (fp32,
     bf16 or fp16) quantised by the same rule within the call."""
-    T, d, ldx = _pitch(X, "X")
-    if X.dtype not in _ODT:
+    T, d, ldx = _matrix(X, "X")
+    xdt = _ODT.get(X.dtype)
+    if xdt is None:
         raise ValueError("X must be float32, bfloat16 or float16")
     N = _quantised(codes, scales, d)
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype, device=X.device)
-    t2, n2, ldy = _pitch(out, "out")
-    if (t2, n2) != (T, N) or out.dtype not in (torch.float32, torch.bfloat16):
+    t2, n2, ldy = _matrix(out, "out")
+    ydt = _WDT.get(out.dtype)
+    if t2 != T or n2 != N or ydt is None:
         raise ValueError("out must be T x N of float32 or bfloat16")
     lib = _lib.load()
     if workspace is None:
-        workspace = _temporary(int(lib.qamw_mxfp4_matmul_workspace_bytes(T, N, d)), X.device, stream)
-    _dev(workspace, "workspace")
-    _lib.check("qamw_mxfp4_matmul", lib.qamw_mxfp4_matmul(
-        X.data_ptr(), _ODT[X.dtype], T, d, ldx, codes.data_ptr(), scales.data_ptr(), N, out.data_ptr(),
-        _ODT[out.dtype], ldy, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace = _temporary(lib.qamw_mxfp4_matmul_workspace_bytes(T, N, d), X.device, stream)
+    else:
+        _dev(workspace, "workspace")
+    status = lib.qamw_mxfp4_matmul(X.data_ptr(), xdt, T, d, ldx, codes.data_ptr(), scales.data_ptr(), N, out.data_ptr(), ydt,
+                                   ldy, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream))
+    if status:
+        _lib.check("qamw_mxfp4_matmul", status)
     return out
