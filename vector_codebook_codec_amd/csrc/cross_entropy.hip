@@ -258,12 +258,9 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
   if constexpr (sizeof(E) == 2) {
     // 16-bit results go through LDS: rows of G and of Gt in runs of 16 bytes a lane
     __syncthreads();
-    for (int k = threadIdx.x; k < Tl::BN * (Tl::BM / 8); k += Tl::kThreads) {
-      const int t = k / (Tl::BM / 8), v = k % (Tl::BM / 8) * 8;
-      if (n0 + t < H.rows && m0 + v < vp)
-        *reinterpret_cast<u32x4*>(G + (n0 + t) * vp + m0 + v) =
-            *reinterpret_cast<const u32x4*>(Tile16<Tl::BM>::at(tile_lds, t, v));
-    }
+    tile16_rows<Tl>(tile_lds, [&](int t, int v, u32x4 q) {
+      if (n0 + t < H.rows && m0 + v < vp) *reinterpret_cast<u32x4*>(G + (n0 + t) * vp + m0 + v) = q;
+    });
     for (int k = threadIdx.x; k < Tl::BM / 2 * (Tl::BN / 8); k += Tl::kThreads) {
       // 8 lanes along the tokens, 8 along the vocabulary
       const int cell = k / 64, o = cell % (Tl::BN / 64) * 8 + (k & 7), v = (cell / (Tl::BN / 64) * 8 + (k >> 3 & 7)) * 2;
@@ -347,23 +344,29 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
   f32x4 acc[Tl::TM][Tl::TN] = {};
   if (s0 < s1) Tl::run(acc, A, m0, B, n0, kchunks, s0, s1, tile_lds);
   Out* out = C + blockIdx.y * split_stride;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int64_t m = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
-  const int64_t n = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
   const float u = unit ? *unit : 1.0f;
+  if constexpr (sizeof(Out) == 2) {
+    tile16_put<Tl>(tile_lds, acc, [&](f32x4 v) { return make_uint2(pack_bf16x2(v[0] * u, v[1] * u), pack_bf16x2(v[2] * u, v[3] * u)); });
+    tile16_rows<Tl>(tile_lds, [&](int n, int m, u32x4 q) {            // A.rows is a multiple of 8
+      if (n0 + n < B.rows && m0 + m < A.rows) *reinterpret_cast<u32x4*>(out + (n0 + n) * ldc + m0 + m) = q;
+    });
+    return;
+  } else {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+    const int64_t m = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
+    const int64_t n = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
 #pragma unroll
-  for (int j = 0; j < Tl::TN; ++j)
-    if (n + 16 * j < B.rows)
+    for (int j = 0; j < Tl::TN; ++j)
+      if (n + 16 * j < B.rows)
 #pragma unroll
-      for (int i = 0; i < Tl::TM; ++i)
-        if (m + 16 * i < A.rows) {                                  // A.rows is a multiple of 4
-          Out* p = out + (n + 16 * j) * ldc + m + 16 * i;
-          acc[i][j] *= u;
-          if constexpr (sizeof(Out) == 4) {
+        for (int i = 0; i < Tl::TM; ++i)
+          if (m + 16 * i < A.rows) {
+            Out* p = out + (n + 16 * j) * ldc + m + 16 * i;
+            acc[i][j] *= u;
             if (add) acc[i][j] += *reinterpret_cast<const f32x4*>(p);
+            store4(p, acc[i][j]);
           }
-          store4(p, acc[i][j]);
-        }
+  }
 }
 
 // dH = unit times the fp32 sums of the splits, in order, rounded once

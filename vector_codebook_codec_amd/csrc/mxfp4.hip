@@ -41,18 +41,26 @@ struct MemF16 {
   static __device__ __forceinline__ uint16_t put(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 };
 
-// 8 consecutive elements of a row from column j: as 16-byte loads where the
-// launcher found every row 16-byte aligned and the columns are all there,
-// else one by one, with 0 past the row's end.
+// 8 consecutive elements of a row from column j; past the row's end 0 is read
+// and nothing written.  Rows start anywhere (an odd row length puts them off
+// every boundary): whole groups go as 16-byte accesses of any alignment, which
+// the memory pipeline takes, only the last group of a row one by one.
+template <class V, class T> __device__ __forceinline__ V load_any(const T* p) {
+  V v;
+  __builtin_memcpy(&v, p, sizeof v);
+  return v;
+}
+template <class V, class T> __device__ __forceinline__ void store_any(T* p, V v) { __builtin_memcpy(p, &v, sizeof v); }
+
 template <class Mem>
-__device__ __forceinline__ void load8(const typename Mem::T* row, int j, int d, bool wide, float (&x)[8]) {
-  if (wide && j + 8 <= d) {
+__device__ __forceinline__ void load8(const typename Mem::T* row, int j, int d, float (&x)[8]) {
+  if (j + 8 <= d) {
     if constexpr (sizeof(typename Mem::T) == 4) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(row + j), b = *reinterpret_cast<const f32x4*>(row + j + 4);
+      const f32x4 a = load_any<f32x4>(row + j), b = load_any<f32x4>(row + j + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(row + j);
+      const u32x4 a = load_any<u32x4>(row + j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[2 * i] = Mem::get((uint16_t)(a[i] & 0xffffu));
@@ -65,16 +73,16 @@ __device__ __forceinline__ void load8(const typename Mem::T* row, int j, int d, 
   }
 }
 template <class Mem>
-__device__ __forceinline__ void store8(typename Mem::T* row, int j, int d, bool wide, const float (&x)[8]) {
-  if (wide && j + 8 <= d) {
+__device__ __forceinline__ void store8(typename Mem::T* row, int j, int d, const float (&x)[8]) {
+  if (j + 8 <= d) {
     if constexpr (sizeof(typename Mem::T) == 4) {
-      *reinterpret_cast<f32x4*>(row + j) = f32x4{x[0], x[1], x[2], x[3]};
-      *reinterpret_cast<f32x4*>(row + j + 4) = f32x4{x[4], x[5], x[6], x[7]};
+      store_any(row + j, f32x4{x[0], x[1], x[2], x[3]});
+      store_any(row + j + 4, f32x4{x[4], x[5], x[6], x[7]});
     } else {
       u32x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = (uint32_t)Mem::put(x[2 * i]) | ((uint32_t)Mem::put(x[2 * i + 1]) << 16);
-      *reinterpret_cast<u32x4*>(row + j) = v;
+      store_any(row + j, v);
     }
   } else {
 #pragma unroll
@@ -162,15 +170,14 @@ template <> struct RawBlock<MemF16> : RawBlock16<false> {};
 // ---------------------------------------------------------------------------
 template <class In, class Val>
 __global__ __launch_bounds__(kBlockThreads) void mx4_quantize_kernel(
-    const typename In::T* __restrict__ W, int64_t N, int d, int64_t ldw, bool wide_in, uint8_t* __restrict__ codes,
-    uint8_t* __restrict__ scales, int nb, int scale_pitch, typename Val::T* __restrict__ values, int64_t ldv,
-    bool wide_val) {
+    const typename In::T* __restrict__ W, int64_t N, int d, int64_t ldw, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales, int nb, int scale_pitch, typename Val::T* __restrict__ values, int64_t ldv) {
   const int per_row = 4 * nb;                                             // lanes of a row
   for (int64_t n = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; n < N; n += (int64_t)gridDim.y * blockDim.y) {
     const int u = blockIdx.x * blockDim.x + threadIdx.x;                  // whole quads are in or out
     if (u >= per_row) continue;
     float x[8];
-    load8<In>(W + n * ldw, 8 * u, d, wide_in, x);
+    load8<In>(W + n * ldw, 8 * u, d, x);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
@@ -185,7 +192,7 @@ __global__ __launch_bounds__(kBlockThreads) void mx4_quantize_kernel(
     }
     if (values) {
       decode8(c, code, x);
-      store8<Val>(values + n * ldv, 8 * u, d, wide_val, x);
+      store8<Val>(values + n * ldv, 8 * u, d, x);
     }
   }
 }
@@ -194,15 +201,14 @@ template <class Out>
 __global__ __launch_bounds__(kBlockThreads) void mx4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                        const uint8_t* __restrict__ scales, int64_t N,
                                                                        int d, int nb, int scale_pitch,
-                                                                       typename Out::T* __restrict__ W, int64_t ldo,
-                                                                       bool wide) {
+                                                                       typename Out::T* __restrict__ W, int64_t ldo) {
   const int per_row = 4 * nb;
   for (int64_t n = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; n < N; n += (int64_t)gridDim.y * blockDim.y) {
     const int u = blockIdx.x * blockDim.x + threadIdx.x;
     if (u >= per_row) continue;
     float x[8];
     decode8(*reinterpret_cast<const uint32_t*>(codes + n * (int64_t)nb * 16 + 4 * u), scales[n * scale_pitch + (u >> 2)], x);
-    store8<Out>(W + n * ldo, 8 * u, d, wide, x);
+    store8<Out>(W + n * ldo, 8 * u, d, x);
   }
 }
 
@@ -213,19 +219,51 @@ __global__ __launch_bounds__(kBlockThreads) void mx4_dequantize_kernel(const uin
 // then holds 4 consecutive channels n of one token.
 // ---------------------------------------------------------------------------
 template <class Out>
-__device__ __forceinline__ void store_y(typename Out::T* Y, int64_t ldy, int64_t t, int64_t n, int64_t N, bool wide,
-                                        f32x4 v) {
+__device__ __forceinline__ void store_y(typename Out::T* Y, int64_t ldy, int64_t t, int64_t n, int64_t N, f32x4 v) {
   typename Out::T* p = Y + t * ldy + n;
-  if (wide && n + 4 <= N) {
+  if (n + 4 <= N) {
     if constexpr (sizeof(typename Out::T) == 4)
-      *reinterpret_cast<f32x4*>(p) = v;
+      store_any(p, v);
     else
-      *reinterpret_cast<uint2*>(p) = make_uint2((uint32_t)Out::put(v[0]) | ((uint32_t)Out::put(v[1]) << 16),
-                                                (uint32_t)Out::put(v[2]) | ((uint32_t)Out::put(v[3]) << 16));
+      store_any(p, make_uint2((uint32_t)Out::put(v[0]) | ((uint32_t)Out::put(v[1]) << 16),
+                              (uint32_t)Out::put(v[2]) | ((uint32_t)Out::put(v[3]) << 16)));
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       if (n + r < N) p[r] = Out::put(v[r]);
+  }
+}
+
+template <class Tl, class Out>
+__device__ __forceinline__ void store_tile(typename Out::T* Y, int64_t ldy, int64_t n0, int64_t T, int64_t m0, int64_t N,
+                                           f32x4 (&acc)[Tl::TM][Tl::TN], char* lds) {
+  typedef typename Out::T E;
+  if constexpr (sizeof(E) == 2) {
+    tile16_put<Tl>(lds, acc, [](f32x4 v) {
+      return make_uint2((uint32_t)Out::put(v[0]) | ((uint32_t)Out::put(v[1]) << 16),
+                        (uint32_t)Out::put(v[2]) | ((uint32_t)Out::put(v[3]) << 16));
+    });
+    tile16_rows<Tl>(lds, [&](int r, int c, u32x4 v) {
+      if (n0 + r >= T || m0 + c >= N) return;
+      E* p = Y + (n0 + r) * ldy + m0 + c;
+      if (m0 + c + 8 <= N) {
+        store_any(p, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (m0 + c + e < N) p[e] = (E)(v[e / 2] >> (16 * (e & 1)));
+      }
+    });
+  } else {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+    const int64_t m = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
+    const int64_t t = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < Tl::TN; ++j)
+      if (t + 16 * j < T)
+#pragma unroll
+        for (int i = 0; i < Tl::TM; ++i)
+          if (m + 16 * i < N) store_y<Out>(Y, ldy, t + 16 * j, m + 16 * i, N, acc[i][j]);
   }
 }
 
@@ -235,7 +273,7 @@ __device__ __forceinline__ void store_y(typename Out::T* Y, int64_t ldy, int64_t
 template <class Tl, class Out>
 __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Operand X, int kchunks, int tiles_m,
                                                                   int tiles_n, int whole, int splits,
-                                                                  typename Out::T* __restrict__ Y, int64_t ldy, bool wide,
+                                                                  typename Out::T* __restrict__ Y, int64_t ldy,
                                                                   float* __restrict__ part) {
   extern __shared__ __align__(1024) char tile_lds[];
   const int id = blockIdx.x, steps = (kchunks + kStepChunks - 1) / kStepChunks;
@@ -253,30 +291,24 @@ __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Ope
   const int64_t m0 = (int64_t)tm * Tl::BM, n0 = (int64_t)tn * Tl::BN;
   f32x4 acc[Tl::TM][Tl::TN] = {};
   if (s0 < s1) Tl::run(acc, W, m0, X, n0, kchunks, s0, s1, tile_lds);
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int ml = (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4), tl = (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
-  if (split) {
-    float* p = part + ((int64_t)(id - whole) * Tl::BN + tl) * Tl::BM + ml;
-#pragma unroll
-    for (int j = 0; j < Tl::TN; ++j)
-#pragma unroll
-      for (int i = 0; i < Tl::TM; ++i) *reinterpret_cast<f32x4*>(p + 16 * j * Tl::BM + 16 * i) = acc[i][j];
+  if (!split) {
+    store_tile<Tl, Out>(Y, ldy, n0, X.rows, m0, W.rows, acc, tile_lds);
     return;
   }
-  const int64_t m = m0 + ml, t = n0 + tl;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int ml = (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4), tl = (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+  float* p = part + ((int64_t)(id - whole) * Tl::BN + tl) * Tl::BM + ml;
 #pragma unroll
   for (int j = 0; j < Tl::TN; ++j)
-    if (t + 16 * j < X.rows)
 #pragma unroll
-      for (int i = 0; i < Tl::TM; ++i)
-        if (m + 16 * i < W.rows) store_y<Out>(Y, ldy, t + 16 * j, m + 16 * i, W.rows, wide, acc[i][j]);
+    for (int i = 0; i < Tl::TM; ++i) *reinterpret_cast<f32x4*>(p + 16 * j * Tl::BM + 16 * i) = acc[i][j];
 }
 
 // Y of the split tiles: a tile per blockIdx.y, its shares added in order
 template <class Tl, class Out>
 __global__ __launch_bounds__(256) void mx4_sum_tail_kernel(const float* __restrict__ part, int whole, int splits, int tiles_m,
                                                            int tiles_n, int64_t T, int64_t N,
-                                                           typename Out::T* __restrict__ Y, int64_t ldy, bool wide) {
+                                                           typename Out::T* __restrict__ Y, int64_t ldy) {
   int tm, tn;
   tile_at(whole + (int)blockIdx.y, tiles_m, tiles_n, tm, tn);
   const int e = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4, m = e % Tl::BM, n = e / Tl::BM;
@@ -285,7 +317,7 @@ __global__ __launch_bounds__(256) void mx4_sum_tail_kernel(const float* __restri
   const float* p = part + (int64_t)blockIdx.y * splits * (Tl::BM * Tl::BN) + e;
   f32x4 s = *reinterpret_cast<const f32x4*>(p);
   for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(p + (int64_t)k * (Tl::BM * Tl::BN));
-  store_y<Out>(Y, ldy, t, c, N, wide, s);
+  store_y<Out>(Y, ldy, t, c, N, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -299,7 +331,7 @@ __global__ __launch_bounds__(256) void mx4_sum_tail_kernel(const float* __restri
 template <int RF, int TF, class In, class Out, bool kFused>
 __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Operand Xq, const typename In::T* __restrict__ X,
                                                                 int d, int ldx_bytes, int kchunks,
-                                                                typename Out::T* __restrict__ Y, int64_t ldy, bool wide) {
+                                                                typename Out::T* __restrict__ Y, int64_t ldy) {
   __shared__ __align__(16) char red[thin_lds_bytes<RF, TF>()];
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -375,7 +407,7 @@ __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Op
     if (16 * j + l16 < Xq.rows)
 #pragma unroll
       for (int i = 0; i < RF; ++i)
-        if (m0 + 16 * i + 4 * g < W.rows) store_y<Out>(Y, ldy, 16 * j + l16, m0 + 16 * i + 4 * g, W.rows, wide, acc[i][j]);
+        if (m0 + 16 * i + 4 * g < W.rows) store_y<Out>(Y, ldy, 16 * j + l16, m0 + 16 * i + 4 * g, W.rows, acc[i][j]);
 }
 
 // ===========================================================================
@@ -386,7 +418,6 @@ static void row_grid(int64_t N, int per_row, dim3* grid, dim3* block) {
   *block = dim3((unsigned)bx, (unsigned)by);
   *grid = dim3((unsigned)((per_row + bx - 1) / bx), (unsigned)std::min<int64_t>((N + by - 1) / by, 65535));
 }
-static bool wide_rows(const void* p, int64_t ld, int es) { return aligned16(p) && (ld * es) % 16 == 0; }
 
 template <class In, class Val>
 static int quantize_as(const void* W, int64_t N, int d, int64_t ldw, uint8_t* codes, uint8_t* scales, void* values,
@@ -394,9 +425,8 @@ static int quantize_as(const void* W, int64_t N, int d, int64_t ldw, uint8_t* co
   dim3 grid, block;
   const int nb = (int)mx4_blocks(d);
   row_grid(N, 4 * nb, &grid, &block);
-  hipLaunchKernelGGL((mx4_quantize_kernel<In, Val>), grid, block, 0, st, (const typename In::T*)W, N, d, ldw,
-                     wide_rows(W, ldw, sizeof(typename In::T)), codes, scales, nb, (int)mx4_scale_bytes(d),
-                     (typename Val::T*)values, ldv, wide_rows(values, ldv, sizeof(typename Val::T)));
+  hipLaunchKernelGGL((mx4_quantize_kernel<In, Val>), grid, block, 0, st, (const typename In::T*)W, N, d, ldw, codes, scales, nb, (int)mx4_scale_bytes(d),
+                     (typename Val::T*)values, ldv);
   return check_launch("mx4_quantize_kernel");
 }
 template <class In>
@@ -420,7 +450,7 @@ static int dequantize_to(const uint8_t* codes, const uint8_t* scales, int64_t N,
   const int nb = (int)mx4_blocks(d);
   row_grid(N, 4 * nb, &grid, &block);
   hipLaunchKernelGGL((mx4_dequantize_kernel<Out>), grid, block, 0, st, codes, scales, N, d, nb, (int)mx4_scale_bytes(d),
-                     (typename Out::T*)W, ldo, wide_rows(W, ldo, sizeof(typename Out::T)));
+                     (typename Out::T*)W, ldo);
   return check_launch("mx4_dequantize_kernel");
 }
 int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N, int d, void* W, int32_t odt,
@@ -454,24 +484,19 @@ static Mx4Plan mx4_plan(int64_t T, int64_t N, int64_t d) {
 }
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) { return mx4_plan(T, N, d).bytes; }
 
-template <class Out> static bool wide_y(const void* Y, int64_t ldy) {
-  return ldy % 4 == 0 && (uintptr_t)Y % (4 * sizeof(typename Out::T)) == 0;
-}
-
 template <class Tl, class Out>
 static int matmul_tiled(const TailPlan& p, const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, float* part,
                         hipStream_t st) {
   typedef typename Out::T E;
   const int tm = (int)tiles_of(W.rows, Tl::BM), tn = (int)tiles_of(X.rows, Tl::BN), whole = (int)p.whole, tail = tm * tn - whole;
-  const bool wide = wide_y<Out>(Y, ldy);
   auto kernel = mx4_matmul_kernel<Tl, Out>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(whole + tail * p.splits)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, X, kchunks,
-                     tm, tn, whole, p.splits, (E*)Y, ldy, wide, part);
+                     tm, tn, whole, p.splits, (E*)Y, ldy, part);
   const int rc = check_launch("mx4_matmul_kernel");
   if (rc || !tail) return rc;
   auto sum = mx4_sum_tail_kernel<Tl, Out>;
   hipLaunchKernelGGL(sum, dim3((unsigned)(Tl::BM * Tl::BN / 1024), (unsigned)tail), dim3(256), 0, st, part, whole, p.splits, tm,
-                     tn, X.rows, W.rows, (E*)Y, ldy, wide);
+                     tn, X.rows, W.rows, (E*)Y, ldy);
   return check_launch("mx4_sum_tail_kernel");
 }
 template <class Out>
@@ -490,7 +515,7 @@ static int thin_rows(const Operand& W, const Operand& Xq, const void* X, int d, 
                      hipStream_t st) {
   hipLaunchKernelGGL((mx4_thin_kernel<RF, TF, In, Out, kFused>), dim3((unsigned)tiles_of(W.rows, 16 * RF)), dim3(kThinThreads), 0,
                      st, W, Xq, (const typename In::T*)X, d, (int)(ldx * sizeof(typename In::T)), kchunks,
-                     (typename Out::T*)Y, ldy, wide_y<Out>(Y, ldy));
+                     (typename Out::T*)Y, ldy);
   return check_launch("mx4_thin_kernel");
 }
 template <int TF, class In, class Out, bool kFused>
@@ -528,7 +553,7 @@ int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx,
   const Operand w = {(const char*)wcodes, (int64_t)nb * 16, N, wscales, mx4_scale_bytes(d)};
   const Operand x = {(const char*)xcodes, (int64_t)nb * 16, T, xscales, mx4_scale_bytes(d)};
   // the fused form reads X by 16-byte loads with 32-bit offsets
-  if (T <= kFusedTokens && es == 2 && d % 8 == 0 && wide_rows(X, ldx, es) && ldx * es <= kMaxRowBytes)
+  if (T <= kFusedTokens && es == 2 && d % 8 == 0 && aligned16(X) && ldx % 8 == 0 && ldx * es <= kMaxRowBytes)
     return ydt == QAMW_F32 ? matmul_fused<MemF32>(xdt, w, x, X, d, ldx, nb, Y, ldy, st)
                            : matmul_fused<MemBf16>(xdt, w, x, X, d, ldx, nb, Y, ldy, st);
   const int rc = launch_mx4_quantize(X, xdt, T, d, ldx, xcodes, xscales, nullptr, QAMW_BF16, 0, st);

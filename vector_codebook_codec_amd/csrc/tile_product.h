@@ -308,6 +308,29 @@ struct Tile16 {
   }
 };
 
+// A workgroup's 16-bit tile into LDS (pack: four consecutive results of a row
+// to 8 bytes), once nobody reads the operands there any more ...
+template <class Tl, class Pack>
+__device__ __forceinline__ void tile16_put(char* lds, const f32x4 (&acc)[Tl::TM][Tl::TN], Pack&& pack) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+  const int m = (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4), n = (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < Tl::TN; ++j)
+#pragma unroll
+    for (int i = 0; i < Tl::TM; ++i)
+      *reinterpret_cast<uint2*>(Tile16<Tl::BM>::at(lds, n + 16 * j, m + 16 * i)) = pack(acc[i][j]);
+  __syncthreads();
+}
+// ... and f(row n, column m, 8 results) over the tile, a run of lanes along a row
+template <class Tl, class F>
+__device__ __forceinline__ void tile16_rows(char* lds, F&& f) {
+  for (int k = threadIdx.x; k < Tl::BN * (Tl::BM / 8); k += Tl::kThreads) {
+    const int n = k / (Tl::BM / 8), m = k % (Tl::BM / 8) * 8;
+    f(n, m, *reinterpret_cast<const u32x4*>(Tile16<Tl::BM>::at(lds, n, m)));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Products with few rows of B: bound by reading A once.  A workgroup of 8
 // wavefronts takes 16 RF rows of A and all rows of B (at most 16 TF); the
