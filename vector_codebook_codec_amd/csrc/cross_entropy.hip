@@ -395,21 +395,18 @@ __global__ __launch_bounds__(256) void ce_zero_kernel(E* __restrict__ out, int64
 // ===========================================================================
 static unsigned blocks_for(int64_t n, int per) { return (unsigned)std::min<int64_t>((n + per - 1) / per, 65536); }
 
-// Up to this many tokens the loss reads the head in thin tiles.  V = 32000,
-// d = 4096, bf16: 69.6 us thin at 16 tokens; at 32, 77.2 us thin against 70.6
-// us in 64 x 64 tiles.
-constexpr int64_t kThinTokens = 16;
-// Vocabulary entries of a thin tile: 16 for a few tokens (T = 1: 56.9 us
-// against 62.7 us with 64), 64 where the hidden states that every tile reads
-// weigh more (T = 16: 69.6 us against 83.5 us with 16).
-constexpr int64_t kFewTokens = 4;
+// Up to this many tokens the loss reads the head in thin tiles of 16 entries
+// (V = 32000, d = 4096, bf16: T = 1 56.9 us, T = 4 60.0 us; with 64 entries 62.7
+// us at T = 1, in 64 x 64 tiles 58.2 us at T = 20).
+constexpr int64_t kThinTokens = 4;
+constexpr int kThinRows = 16;
 
 static ProductType product_type(int es) { return es == 4 ? kProductF32 : kProductBf16; }
 static int64_t steps_of(int64_t elements, int es) { return tiles_of(elements * es, kStepBytes); }
 // tile shape of the logits, and its vocabulary entries
 static int logits_shape(int64_t T, int64_t V, int d, int es) { return product_plan(product_type(es), V, T, steps_of(d, es), 1).shape; }
 static int logits_tile(int64_t T, int64_t V, int d, int es) {
-  return T <= kFewTokens ? 16 : T <= kThinTokens ? 64 : kShapeTile[logits_shape(T, V, d, es)];
+  return T <= kThinTokens ? kThinRows : kShapeTile[logits_shape(T, V, d, es)];
 }
 size_t ce_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt) {
   return round_up((size_t)tiles_of(V, logits_tile(T, V, d, elem_size(dt))) * T * sizeof(float2), 256) +
@@ -438,15 +435,15 @@ static int ce_tiled(const Operand& W, const Operand& H, int kchunks, const int64
   const int rc = check_launch("ce_stats_kernel");
   return rc ? rc : ce_finish(part, zt, targets, T, W.rows, tm, loss, lse, st);
 }
-template <class Op, int RF, int TF, int U>
+template <class Op>
 static int ce_thin(const Operand& W, const Operand& H, int kchunks, const int64_t* targets, float* loss, float* lse, void* ws,
                    hipStream_t st) {
-  const int tm = (int)tiles_of(W.rows, 16 * RF);
+  const int tm = (int)tiles_of(W.rows, kThinRows);
   const int64_t T = H.rows;
   float2* part = (float2*)ws;
   float* zt = (float*)((char*)ws + round_up((size_t)tm * T * sizeof(float2), 256));
-  hipLaunchKernelGGL((ce_stats_thin_kernel<Op, RF, TF, U>), dim3((unsigned)tm), dim3(kThinThreads), 0, st, W, H, kchunks, targets,
-                     part, zt);
+  hipLaunchKernelGGL((ce_stats_thin_kernel<Op, kThinRows / 16, 1, 4>), dim3((unsigned)tm), dim3(kThinThreads), 0, st, W, H, kchunks,
+                     targets, part, zt);
   const int rc = check_launch("ce_stats_thin_kernel");
   return rc ? rc : ce_finish(part, zt, targets, T, W.rows, tm, loss, lse, st);
 }
@@ -455,8 +452,7 @@ static int ce_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, in
                  const int64_t* targets, float* loss, float* lse, void* ws, hipStream_t st) {
   const int es = sizeof(typename Elem<Op>::T), kchunks = d / Op::kElems;
   const Operand a = {(const char*)W, ldw * es, V, nullptr, 0}, b = {(const char*)H, ldh * es, T, nullptr, 0};
-  if (T <= kFewTokens) return ce_thin<Op, 1, 1, 4>(a, b, kchunks, targets, loss, lse, ws, st);
-  if (T <= kThinTokens) return ce_thin<Op, 4, 1, 2>(a, b, kchunks, targets, loss, lse, ws, st);
+  if (T <= kThinTokens) return ce_thin<Op>(a, b, kchunks, targets, loss, lse, ws, st);
   return with_shape<Op>(logits_shape(T, V, d, es),
                         [&](auto tile) { return ce_tiled<Op, decltype(tile)>(a, b, kchunks, targets, loss, lse, ws, st); });
 }

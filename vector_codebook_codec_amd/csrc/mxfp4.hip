@@ -466,16 +466,17 @@ struct Mx4Plan {
   TailPlan tiles;
   size_t scales, part, bytes;
 };
-// Up to this many tokens the weights are read in thin tiles (11008 x 4096: 17.5
-// us at 32 tokens; at 64, 21.8 us thin against 16.1 us tiled).
-constexpr int64_t kThinTokens = 32;
+// Whether the weights are read in thin tiles: up to 16 tokens, and up to 32
+// where 64 x 64 tiles would leave half the CUs idle (T = 32: 4096 x 4096 10.2
+// us thin, 12.6 us tiled; 11008 x 4096 16.2 us and 13.4 us).
+static bool thin_pays(int64_t T, int64_t N) { return T <= 16 || (T <= 32 && 2 * tiles_of(N, 64) <= kCus); }
 static Mx4Plan mx4_plan(int64_t T, int64_t N, int64_t d) {
   Mx4Plan p;
   p.tiles = {0, 0, 1};
   p.scales = round_up((size_t)T * mx4_blocks(d) * 16, 256);
   p.part = p.scales + round_up((size_t)T * mx4_scale_bytes(d), 256);
   p.bytes = p.part;
-  if (T > kThinTokens) {
+  if (!thin_pays(T, N)) {
     p.tiles = tail_plan(kProductMx4, N, T, tiles_of(mx4_blocks(d), kStepChunks));
     const int64_t tile = kShapeTile[p.tiles.shape], tail = shape_tiles(p.tiles.shape, N, T) - p.tiles.whole;
     p.bytes += (size_t)(tail * p.tiles.splits * tile * tile) * sizeof(float);
@@ -535,7 +536,7 @@ template <class Out>
 static int matmul_quantised(const Mx4Plan& p, const Operand& W, const Operand& X, int d, int kchunks, void* Y, int64_t ldy,
                             float* part, hipStream_t st) {
   if (X.rows <= 16) return matmul_thin<1, MemBf16, Out, false>(W, X, nullptr, d, 0, kchunks, Y, ldy, st);
-  if (X.rows <= kThinTokens) return matmul_thin<2, MemBf16, Out, false>(W, X, nullptr, d, 0, kchunks, Y, ldy, st);
+  if (thin_pays(X.rows, W.rows)) return matmul_thin<2, MemBf16, Out, false>(W, X, nullptr, d, 0, kchunks, Y, ldy, st);
   return matmul_to<Out>(p.tiles, W, X, kchunks, Y, ldy, part, st);
 }
 

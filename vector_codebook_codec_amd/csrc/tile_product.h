@@ -97,7 +97,7 @@ struct OpMx4 {
   }
 };
 
-template <class Op, int BM_, int BN_, int WM_, int WN_>
+template <class Op, int BM_, int BN_, int WM_, int WN_, int S_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;    // tile, wavefront grid
   static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
@@ -105,7 +105,8 @@ struct Tile {
   static constexpr int kRows = BM + BN;
   static constexpr int kDataBytes = kRows * kStepBytes;
   static constexpr int kScaleBytes = Op::kScaled ? kRows * 16 : 0;         // codes of two K steps
-  static constexpr int kLdsBytes = 2 * (kDataBytes + kScaleBytes);
+  static constexpr int S = S_;                                    // K steps in LDS, a power of two
+  static constexpr int kLdsBytes = S * (kDataBytes + kScaleBytes);
   static constexpr int kCopiesA = BM / 8 / kWaves, kCopiesB = BN / 8 / kWaves;   // 8 rows per wavefront copy
   static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && (8 * kWaves) % 16 == 0, "whole copies");
   static_assert(!Op::kScaled || (BM % kWave == 0 && BN % kWave == 0), "whole scale copies");
@@ -114,13 +115,13 @@ struct Tile {
   // step1; kchunks = chunks of a row.  Every thread of the workgroup calls it;
   // lds holds kLdsBytes.
   //
-  // Two LDS buffers take the K steps in turn.  Fragments are read from LDS
+  // S LDS buffers take the K steps in turn.  Fragments are read from LDS
   // half a step before the matrix instructions that use them, so that one
   // barrier a step is enough and stands between two runs of matrix
   // instructions whose operands are already in registers:
   //   read (k, half 1)       | multiply (k, half 0)
   //   wait for the copies of step k + 1, barrier: nobody reads buffer k again
-  //   copy step k + 2 into it; read (k + 1, half 0) | multiply (k, half 1)
+  //   copy step k + S into it; read (k + 1, half 0) | multiply (k, half 1)
   static __device__ __forceinline__ void run(f32x4 (&acc)[TM][TN], const Operand& A, int64_t m0, const Operand& B,
                                              int64_t n0, int kchunks, int step0, int step1, char* lds) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -143,12 +144,14 @@ struct Tile {
       bsa = buffer_of(A.scale + m0 * A.scale_pitch, (uint32_t)(ra * A.scale_pitch));
       bsb = buffer_of(B.scale + n0 * B.scale_pitch, (uint32_t)(rb * B.scale_pitch));
     }
-    char* const scales = lds + 2 * kDataBytes;
+    char* const scales = lds + S * kDataBytes;
 
+    // With S > 2 steps past the last one are copied too, as zeros: the number of copies in flight then is the
+    // same in every step.
     auto copy = [&](int step) __attribute__((always_inline)) {
-      char* st = lds + ((step - step0) & 1) * kDataBytes;
-      const bool in = step * kStepChunks + chunk < kchunks;
-      const uint32_t soff = (uint32_t)step * kStepBytes;
+      char* st = lds + ((step - step0) & (S - 1)) * kDataBytes;
+      const bool in = (S == 2 || step < step1) && step * kStepChunks + chunk < kchunks;
+      const uint32_t soff = S == 2 || step < step1 ? (uint32_t)step * kStepBytes : 0u;   // below every buffer's size
 #pragma unroll
       for (int i = 0; i < kCopiesA; ++i)
         copy16_to_lds(bufa, st + (wave + kWaves * i) * 1024, in ? va[i] : kPastEnd, soff);
@@ -158,8 +161,8 @@ struct Tile {
       if constexpr (Op::kScaled) {
         // 16 codes of a row, those of this step and the next; a scale row is
         // whole 16-byte groups
-        if (((step - step0) & 1) == 0) {
-          char* sc = scales + (((step - step0) >> 1) & 1) * kScaleBytes;
+        if (((step - step0) & 1) == 0 && (S == 2 || step < step1)) {
+          char* sc = scales + (((step - step0) >> 1) & (S - 1)) * kScaleBytes;
           const uint32_t ks = (uint32_t)step * kStepChunks;
 #pragma unroll
           for (int r0 = 0; r0 < kRows; r0 += kThreads) {
@@ -179,7 +182,7 @@ struct Tile {
     i32x4 a[2][TM], b[2][TN];
     int sa[TM] = {}, sb[TN] = {}, na[TM] = {}, nb[TN] = {};
     auto fetch = [&](int step, int s) __attribute__((always_inline)) {
-      const char* st = lds + ((step - step0) & 1) * kDataBytes + pos[s];
+      const char* st = lds + ((step - step0) & (S - 1)) * kDataBytes + pos[s];
 #pragma unroll
       for (int i = 0; i < TM; ++i) a[s][i] = *reinterpret_cast<const i32x4*>(st + (arow + 16 * i) * kStepBytes);
 #pragma unroll
@@ -188,7 +191,7 @@ struct Tile {
     auto fetch_scales = [&](int step) __attribute__((always_inline)) {
       if constexpr (Op::kScaled) {
         const int k = step - step0;
-        const char* sc = scales + ((k >> 1) & 1) * kScaleBytes + (k & 1) * 8 + 2 * pair;
+        const char* sc = scales + ((k >> 1) & (S - 1)) * kScaleBytes + (k & 1) * 8 + 2 * pair;
 #pragma unroll
         for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint16_t*>(sc + (arow + 16 * i) * 16);
 #pragma unroll
@@ -221,8 +224,9 @@ struct Tile {
       }
     };
 
-    copy(step0);
-    if (step0 + 1 < step1) copy(step0 + 1);
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+      if (S > 2 || step0 + k < step1) copy(step0 + k);
     __builtin_amdgcn_s_waitcnt(0x0f70);                      // vmcnt(0): this wavefront's copies are in LDS
     __syncthreads();
     fetch(step0, 0);
@@ -232,32 +236,41 @@ struct Tile {
       fetch(step, 1);
       multiply(0);
       interleave();
-      __builtin_amdgcn_s_waitcnt(0x0f70);
+      // vmcnt: all copies but those of steps k + 2 to k + S - 1 (copies complete in order; those of scale codes
+      // come on top, which only makes the wait a little longer)
+      constexpr int kLater = (S - 2) * (kCopiesA + kCopiesB);
+      static_assert(kLater < 64, "vmcnt has 6 bits");
+      __builtin_amdgcn_s_waitcnt(0x0f70 | (kLater & 15) | (kLater >> 4) << 14);
       __syncthreads();
-      if (step + 2 < step1) copy(step + 2);
-      fetch(step + 1, 0);                                    // past the last step: stale, not used
+      if (S > 2 || step + S < step1) copy(step + S);
+      fetch(step + 1, 0);                                    // past the last step: zero or stale, not used
       fetch_scales(step + 1);
       multiply(1);
       interleave();
     }
+    if (S > 2) __builtin_amdgcn_s_waitcnt(0x0f70);           // no copy outlives the call
   }
 };
 
 // The tile shapes (qamw_internal.h says when each is taken).  The larger a
 // tile, the fewer operand bytes go through LDS per product: at 8192 x 8192 x
 // 4096 in bf16, 392 us (1.40 PFLOP/s) and 498 us with 256 and 128.  One
-// workgroup of 256 x 256, two of 128 x 128, five of 64 x 64 share a CU.
+// workgroup of 256 x 256, two of 128 x 128 share a CU, of 64 x 64 five with two
+// K steps in LDS and two with four.
 template <class Op, int kShape> struct ShapeTile;
-template <class Op> struct ShapeTile<Op, 0> { typedef Tile<Op, 64, 64, 2, 2> T; };
-template <class Op> struct ShapeTile<Op, 1> { typedef Tile<Op, 128, 128, 4, 2> T; };
-template <class Op> struct ShapeTile<Op, 2> { typedef Tile<Op, 256, 256, 4, 2> T; };
+template <class Op> struct ShapeTile<Op, 0> { typedef Tile<Op, 64, 64, 2, 2, 4> T; };
+template <class Op> struct ShapeTile<Op, 1> { typedef Tile<Op, 64, 64, 2, 2> T; };
+template <class Op> struct ShapeTile<Op, 2> { typedef Tile<Op, 128, 128, 4, 2> T; };
+template <class Op> struct ShapeTile<Op, 3> { typedef Tile<Op, 256, 256, 4, 2> T; };
 
 // f(Tile()) for a shape chosen at run time
 template <class Op, class F>
 inline int with_shape(int shape, F&& f) {
+  if (shape == 3) return f(typename ShapeTile<Op, 3>::T());
   if (shape == 2) return f(typename ShapeTile<Op, 2>::T());
-  if (shape == 1) return f(typename ShapeTile<Op, 1>::T());
-  return f(typename ShapeTile<Op, 0>::T());
+  if constexpr (!std::is_same<Op, OpF32>::value)
+    if (shape == 0) return f(typename ShapeTile<Op, 0>::T());
+  return f(typename ShapeTile<Op, 1>::T());
 }
 
 // Workgroup -> tile.  Consecutive workgroups go to the 8 XCDs in turn, each
