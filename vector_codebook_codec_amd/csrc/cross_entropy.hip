@@ -210,7 +210,7 @@ template <class Tl, class Op>
 __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
     Operand W, Operand H, int kchunks, int tiles_m, int tiles_n, const int64_t* __restrict__ targets, int64_t v_first,
     int64_t V, const float* __restrict__ lse, const float* __restrict__ dloss, const float* __restrict__ unit,
-    typename Elem<Op>::T* __restrict__ G, int64_t vp, typename Elem<Op>::T* __restrict__ Gt, int64_t tp) {
+    typename Elem<Op>::T* __restrict__ G, int64_t vp, typename Elem<Op>::T* __restrict__ Gt, int64_t tp) {   // Gt may be NULL
   typedef typename Elem<Op>::T E;
   extern __shared__ __align__(1024) char tile_lds[];
   int tm, tn;
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
             make_uint2(pack_bf16x2(q[0], q[1]), pack_bf16x2(q[2], q[3]));
       } else {
         if (t < H.rows && v < vp) store4(G + t * vp + v, q);
-        if (t < tp)
+        if (Gt && t < tp)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (v + r < W.rows) Gt[(v + r) * tp + t] = q[r];
@@ -261,6 +261,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
     tile16_rows<Tl>(tile_lds, [&](int t, int v, u32x4 q) {
       if (n0 + t < H.rows && m0 + v < vp) *reinterpret_cast<u32x4*>(G + (n0 + t) * vp + m0 + v) = q;
     });
+    if (!Gt) return;
     for (int k = threadIdx.x; k < Tl::BM / 2 * (Tl::BN / 8); k += Tl::kThreads) {
       // 8 lanes along the tokens, 8 along the vocabulary
       const int cell = k / 64, o = cell % (Tl::BN / 64) * 8 + (k & 7), v = (cell / (Tl::BN / 64) * 8 + (k >> 3 & 7)) * 2;
@@ -369,6 +370,157 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
   }
 }
 
+// ---------------------------------------------------------------------------
+// The two products for a few tokens: bound by reading W and writing dW once,
+// with no transposed copies.  A thread owns 16 bytes of columns and walks the
+// workgroup's vocabulary entries, whose G lies in LDS as fp32.
+// ---------------------------------------------------------------------------
+template <class E> constexpr int cols_of() { return 16 / sizeof(E); }
+template <class E>
+__device__ __forceinline__ void unpack_cols(u32x4 v, float (&x)[16 / sizeof(E)]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(E) == 2) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(v[i]);
+    }
+  }
+}
+constexpr int kThinEntries = 128;                                  // vocabulary entries whose G is in LDS at a time
+// g[v][t] = G[t][v0 + v] for v < count, t < T; 0 for T <= t < TT
+template <class E, int TT>
+__device__ __forceinline__ void stage_g(float (&g)[kThinEntries][TT], const E* G, int64_t vp, int64_t v0, int count, int T) {
+  for (int k = threadIdx.x; k < kThinEntries * TT; k += 256) {
+    const int t = k / kThinEntries, v = k % kThinEntries;
+    float x = 0.0f;
+    if (t < T && v < count) {
+      if constexpr (sizeof(E) == 2) x = bf16_bits_to_f32(G[t * vp + v0 + v]);
+      else x = G[t * vp + v0 + v];
+    }
+    g[v][t] = x;
+  }
+}
+
+// sum[block][t][d] (+)= sum over the block's entries v of G[t][v] W[v][:]
+template <class E, int TT>
+__global__ __launch_bounds__(256) void ce_dh_thin_kernel(const E* __restrict__ G, int64_t vp, const E* __restrict__ W,
+                                                         int64_t ldw, int64_t n, int per_block, int T, int d,
+                                                         float* __restrict__ sum, bool add) {
+  constexpr int C = cols_of<E>();
+  __shared__ __align__(16) float g[kThinEntries][TT];
+  const int c = (blockIdx.y * 256 + threadIdx.x) * C;
+  const int64_t v0 = min((int64_t)blockIdx.x * per_block, n), v1 = min(v0 + per_block, n);
+  float acc[TT][C] = {};
+  for (int64_t vb = v0; vb < v1; vb += kThinEntries) {
+    const int count = (int)min((int64_t)kThinEntries, v1 - vb);
+    __syncthreads();
+    stage_g<E, TT>(g, G, vp, vb, count, T);
+    __syncthreads();
+    if (c >= d) continue;
+    const E* p = W + vb * ldw + c;
+    // U rows are multiplied while the next U are on their way; past the end the last row is read, and G is 0
+    constexpr int U = 8;
+    u32x4 now[U], next[U];
+    auto load = [&](u32x4 (&r)[U], int v) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) r[k] = *reinterpret_cast<const u32x4*>(p + (int64_t)min(v + k, count - 1) * ldw);
+    };
+    load(now, 0);
+    for (int v = 0; v < count; v += U) {
+      load(next, v + U);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        float w[C];
+        unpack_cols<E>(now[k], w);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[t][i] = fmaf(g[v + k][t], w[i], acc[t][i]);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) now[k] = next[k];
+    }
+  }
+  if (c >= d) return;
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+    if (t < T) {
+      float* p = sum + ((int64_t)blockIdx.x * T + t) * d + c;
+#pragma unroll
+      for (int i = 0; i < C; i += 4) {
+        f32x4 a = {acc[t][i], acc[t][i + 1], acc[t][i + 2], acc[t][i + 3]};
+        if (add) a += *reinterpret_cast<const f32x4*>(p + i);
+        *reinterpret_cast<f32x4*>(p + i) = a;
+      }
+    }
+}
+
+// dW[v][:] = unit sum_t G[t][v] H[t][:], the counted tokens t
+template <class E, int TT>
+__global__ __launch_bounds__(256) void ce_dw_thin_kernel(const E* __restrict__ G, int64_t vp, const E* __restrict__ H,
+                                                         int64_t ldh, const int64_t* __restrict__ targets, int64_t V,
+                                                         int64_t n, int per_block, int T, int d,
+                                                         const float* __restrict__ unit, E* __restrict__ dW, int64_t lddw) {
+  constexpr int C = cols_of<E>();
+  __shared__ __align__(16) float g[kThinEntries][TT];
+  const int c = (blockIdx.y * 256 + threadIdx.x) * C;
+  const int64_t v0 = (int64_t)blockIdx.x * per_block;               // per_block <= kThinEntries
+  const int count = (int)min((int64_t)per_block, n - v0);
+  stage_g<E, TT>(g, G, vp, v0, count, T);
+  __syncthreads();
+  if (c >= d) return;
+  const float u = *unit;
+  float h[TT][C];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t y = t < T ? targets[t] : -1;
+    if (y >= 0 && y < V) {
+      unpack_cols<E>(*reinterpret_cast<const u32x4*>(H + t * ldh + c), h[t]);
+#pragma unroll
+      for (int i = 0; i < C; ++i) h[t][i] *= u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i) h[t][i] = 0.0f;
+    }
+  }
+  E* p = dW + v0 * lddw + c;
+  for (int v = 0; v < count; ++v, p += lddw) {
+    float a[C] = {};
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < C; ++i) a[i] = fmaf(g[v][t], h[t][i], a[i]);
+    if constexpr (sizeof(E) == 2)
+      *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                           pack_bf16x2(a[6], a[7])};
+    else
+      *reinterpret_cast<f32x4*>(p) = f32x4{a[0], a[1], a[2], a[3]};
+  }
+}
+
+// dH = unit times many fp32 sums, 16 threads an element: thread k adds sums k,
+// k + 16, ..., then the 16 in order; rounded once.
+template <class E>
+__global__ __launch_bounds__(256) void ce_sum_blocks_kernel(const float* __restrict__ part, int blocks, int64_t stride,
+                                                            int64_t T, int d, const float* __restrict__ unit,
+                                                            E* __restrict__ out, int64_t ldo) {
+  __shared__ f32x4 red[16][16];
+  const int i = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int64_t per = d / 4, n = T * per, e = (int64_t)blockIdx.x * 16 + i;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (e < n)
+#pragma unroll 8
+    for (int q = k; q < blocks; q += 16) s += *reinterpret_cast<const f32x4*>(part + q * stride + 4 * e);
+  red[k][i] = s;
+  __syncthreads();
+  if (k || e >= n) return;
+#pragma unroll
+  for (int q = 1; q < 16; ++q) s += red[q][i];
+  store4(out + e / per * ldo + e % per * 4, s * *unit);
+}
+
 // dH = unit times the fp32 sums of the splits, in order, rounded once
 template <class E>
 __global__ __launch_bounds__(256) void ce_sum_splits_kernel(const float* __restrict__ part, int splits, int64_t stride,
@@ -468,10 +620,18 @@ int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ld
 // 820 MiB.
 constexpr int64_t kPieceTile = kShapeTile[kShapes - 1];
 constexpr int64_t kCeBudget = (int64_t)512 << 20;
+// Whether the products run without transposed copies and matrix instructions:
+// for a few tokens and a head of some size, whose copies would cost more than
+// all else (V = 32000, d = 4096, bf16: T = 1 224 us against 356 us, T = 16 273
+// us, T = 17 361 us; V = 5003, d = 512: fp32, 10 MB, T = 16 57 us, T = 17 66
+// us, but bf16, 5 MB, 50 us and 42 us).
+static bool thin_gradient(int64_t T, int64_t V, int d, int es) { return T <= 16 && V * d * es >= (int64_t(8) << 20); }
 // Sizes and places of the gradient's workspace.
 struct CeGradPlan {
   int64_t piece;            // vocabulary entries per piece
   int64_t vp, tp;           // row pitches of G and Wt, of Gt and Ht (elements)
+  bool thin;                // a few tokens: no transposed copies
+  int blocks;               // thin: vocabulary blocks of a piece, each with an fp32 sum of dH
   ProductPlan dh;           // dH's product over one piece: splits hold fp32 sums of their own over all pieces
   size_t unit, g, gt, wt, ht, sum, bytes;
 };
@@ -492,14 +652,20 @@ static CeGradPlan ce_grad_plan(int64_t T, int64_t V, int d, int es) {
   p.vp = p.piece;
   p.tp = (T + 7) / 8 * 8;
   p.dh = product_plan(product_type(es), d, T, steps_of(p.vp, es), 16);
+  p.thin = thin_gradient(T, V, d, es);
+  // enough blocks for two workgroups a CU, of at least 32 entries
+  p.blocks = (int)std::min<int64_t>(tiles_of(p.piece, 32), tiles_of(2 * kCus, tiles_of((int64_t)d * es, 4096)));
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += round_up(bytes, 256); return o; };
   p.unit = take(sizeof(float));
   p.g = take((size_t)T * p.vp * es);
-  p.gt = take((size_t)p.piece * p.tp * es);
-  p.wt = take((size_t)d * p.vp * es);
-  p.ht = take((size_t)d * p.tp * es);
-  p.sum = take((size_t)p.dh.splits * T * d * sizeof(float));
+  p.gt = p.wt = p.ht = 0;
+  if (!p.thin) {
+    p.gt = take((size_t)p.piece * p.tp * es);
+    p.wt = take((size_t)d * p.vp * es);
+    p.ht = take((size_t)d * p.tp * es);
+  }
+  p.sum = take((size_t)(p.thin ? p.blocks : p.dh.splits) * T * d * sizeof(float));
   p.bytes = at;
   return p;
 }
@@ -533,6 +699,37 @@ static int product(const Operand& A, const Operand& B, int kchunks, const Produc
   });
 }
 
+// f(std::integral_constant) with the smallest of 1, 4 and 16 that holds T
+template <class F>
+static int with_tokens(int64_t T, F&& f) {
+  if (T == 1) return f(std::integral_constant<int, 1>());
+  if (T <= 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, 16>());
+}
+template <class E>
+static int dh_thin(const E* G, int64_t vp, const E* W, int64_t ldw, int64_t n, int blocks, int64_t T, int d, float* sum, bool add,
+                   hipStream_t st) {
+  return with_tokens(T, [&](auto tt) {
+    auto kernel = ce_dh_thin_kernel<E, decltype(tt)::value>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks, (unsigned)tiles_of(d, 256 * cols_of<E>())), dim3(256), 0, st, G, vp, W, ldw,
+                       n, (int)tiles_of(n, blocks), (int)T, d, sum, add);
+    return check_launch("ce_dh_thin_kernel");
+  });
+}
+template <class E>
+static int dw_thin(const E* G, int64_t vp, const E* H, int64_t ldh, const int64_t* targets, int64_t V, int64_t n, int64_t T, int d,
+                   const float* unit, E* dW, int64_t lddw, hipStream_t st) {
+  return with_tokens(T, [&](auto tt) {
+    auto kernel = ce_dw_thin_kernel<E, decltype(tt)::value>;
+    // four workgroups a CU, of 8 to kThinEntries entries
+    const int64_t across = tiles_of(d, 256 * cols_of<E>());
+    const int per = (int)std::min<int64_t>(std::max<int64_t>(n * across / (4 * kCus), 8), kThinEntries);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles_of(n, per), (unsigned)across), dim3(256), 0, st, G, vp, H, ldh, targets, V, n,
+                       per, (int)T, d, unit, dW, lddw);
+    return check_launch("ce_dw_thin_kernel");
+  });
+}
+
 template <class Op>
 static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                       const int64_t* targets, const float* lse, const float* dloss, void* dH, int64_t lddh, void* dW,
@@ -548,7 +745,8 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
   hipLaunchKernelGGL(ce_upstream_kernel, dim3(1), dim3(1024), 0, st, dloss, targets, T, V, unit);
   int rc = check_launch("ce_upstream_kernel");
   if (rc) return rc;
-  if (dW) {
+  E* const Gt_out = dW && !p.thin ? Gt : nullptr;
+  if (dW && !p.thin) {
     hipLaunchKernelGGL((ce_transpose_kernel<E>), dim3((unsigned)((p.tp + 63) / 64), dtiles), dim3(256), 0, st,
                        (const E*)H, ldh, T, (int64_t)d, Ht, p.tp, targets, V);
     if ((rc = check_launch("ce_transpose_kernel"))) return rc;
@@ -559,9 +757,14 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
     const Operand Hp = {(const char*)H, ldh * es, T, nullptr, 0};
     const int kd = d / Op::kElems;
     rc = with_shape<Op>(logits_shape(T, n, d, es), [&](auto tile) {
-      return softmax_grad_tiled<Op, decltype(tile)>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt, p.tp, st);
+      return softmax_grad_tiled<Op, decltype(tile)>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt_out, p.tp, st);
     });
     if (rc) return rc;
+    if (p.thin) {
+      if (dW && (rc = dw_thin<E>(G, p.vp, (const E*)H, ldh, targets, V, n, T, d, unit, (E*)dW + v0 * lddw, lddw, st))) return rc;
+      if (dH && (rc = dh_thin<E>(G, p.vp, (const E*)W + v0 * ldw, ldw, n, p.blocks, T, d, sum, v0 > 0, st))) return rc;
+      continue;
+    }
     if (dW) {
       const Operand a = {(const char*)Ht, p.tp * es, d, nullptr, 0}, b = {(const char*)Gt, p.tp * es, n, nullptr, 0};
       const ProductPlan whole = product_plan(product_type(es), d, n, steps_of(p.tp, es), 1);
@@ -576,12 +779,15 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
       if ((rc = product<Op, float>(a, b, (int)(np / Op::kElems), p.dh, nullptr, sum, d, split_stride, v0 > 0, st))) return rc;
     }
   }
-  if (dH) {
-    hipLaunchKernelGGL((ce_sum_splits_kernel<E>), dim3(blocks_for(T * (d / 4), 256)), dim3(256), 0, st, sum, p.dh.splits,
+  if (!dH) return QAMW_OK;
+  if (p.thin) {
+    hipLaunchKernelGGL((ce_sum_blocks_kernel<E>), dim3((unsigned)tiles_of(T * (d / 4), 16)), dim3(256), 0, st, sum, p.blocks,
                        split_stride, T, d, unit, (E*)dH, lddh);
-    if ((rc = check_launch("ce_sum_splits_kernel"))) return rc;
+    return check_launch("ce_sum_blocks_kernel");
   }
-  return QAMW_OK;
+  hipLaunchKernelGGL((ce_sum_splits_kernel<E>), dim3(blocks_for(T * (d / 4), 256)), dim3(256), 0, st, sum, p.dh.splits,
+                     split_stride, T, d, unit, (E*)dH, lddh);
+  return check_launch("ce_sum_splits_kernel");
 }
 int launch_cross_entropy_grad(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V,
                               int64_t ldw, const int64_t* targets, const float* lse, const float* dloss, void* dH,
