@@ -96,6 +96,11 @@ def _matrix(t: torch.Tensor, name: str):
     return n, d, ld if n > 1 else d
 
 
+def _new(n: int, d: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    """An uninitialised n x d matrix on like's device."""
+    return torch.empty_strided((n, d), (d, 1), dtype=dtype, device=like.device)
+
+
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 

@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _WDT, _dev, _matrix, _raw_stream, _temporary, _vec
+from .codec import _WDT, _dev, _matrix, _new, _raw_stream, _temporary, _vec
 
 __all__ = [
     "qamw_cross_entropy",
@@ -69,9 +69,9 @@ def qamw_cross_entropy_grad(H: torch.Tensor, W: torch.Tensor, targets: torch.Ten
     _vec(lse, "lse", T)
     _vec(dloss, "dloss", T)
     if dH is None and need_dH:
-        dH = torch.empty((T, d), dtype=H.dtype, device=H.device)
+        dH = _new(T, d, H.dtype, H)
     if dW is None and need_dW:
-        dW = torch.empty((V, d), dtype=H.dtype, device=H.device)
+        dW = _new(V, d, H.dtype, H)
     lddh = lddw = d
     if dH is not None:
         n2, d2, lddh = _matrix(dH, "dH")

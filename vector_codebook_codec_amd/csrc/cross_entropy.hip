@@ -55,22 +55,31 @@ __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f3
 // Tile statistics of the logits: part[tile][t] = (max, sum of exp(z - max)),
 // and the target's logit from the one tile that holds it.
 // ---------------------------------------------------------------------------
-// Of one 16-token column of fragments: token t (target y, -1 for none), lane
-// group l / 16 holding entries v + 16 i + r.  The result is the same in all
-// four lanes of a token.
+// Of one 16-token column of fragments: lane group l / 16 holds the entries
+// 16 i + r past the lane's first one, `left` of them (or more) inside the
+// vocabulary, `y` the target's place among them (any other number: not here).
+// The result is the same in all four lanes of a token.  Targets and the
+// vocabulary's end are rare among tiles, so they are looked for once per
+// column, not at every logit.
 template <int TM, int TN>
-__device__ __forceinline__ float2 column_stats(f32x4 (&acc)[TM][TN], int j, int64_t v, int64_t V, int64_t t, int64_t y,
-                                               float* __restrict__ zt) {
+__device__ __forceinline__ float2 column_stats(f32x4 (&acc)[TM][TN], int j, int left, int y, float* zt) {
+  if (left < 16 * TM)                                               // not the same in all lanes, but so in few tiles
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (16 * i + r >= left) acc[i][j][r] = -INFINITY;
+  if (y >= 0 && y < 16 * TM && y < left && (y & 15) < 4)
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (y == 16 * i + r) *zt = acc[i][j][r];
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t e = v + 16 * i + r;
-      if (e >= V) acc[i][j][r] = -INFINITY;
-      m = fmaxf(m, acc[i][j][r]);
-      if (e == y && e < V) zt[t] = acc[i][j][r];
-    }
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
   m = fmaxf(m, __shfl_xor(m, 16));
   m = fmaxf(m, __shfl_xor(m, 32));
   const float base = m == -INFINITY ? 0.0f : m;                     // a tile of -inf alone sums to 0
@@ -83,6 +92,8 @@ __device__ __forceinline__ float2 column_stats(f32x4 (&acc)[TM][TN], int j, int6
   s += __shfl_xor(s, 32);
   return make_float2(m, s);
 }
+// 64-bit places relative to a lane's first entry, as far as 32 bits matter
+__device__ __forceinline__ int near32(int64_t x) { return (int)(x < -1 ? -1 : x > 1 << 20 ? 1 << 20 : x); }
 
 template <class Tl, class Op>
 __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Operand H, int kchunks, int tiles_m,
@@ -103,7 +114,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Opera
 #pragma unroll
   for (int j = 0; j < Tl::TN; ++j) {
     const int64_t t = n0 + tl + 16 * j;
-    const float2 s = column_stats(acc, j, v0, W.rows, t, t < H.rows ? targets[t] : -1, zt);
+    const float2 s = column_stats(acc, j, near32(W.rows - v0), t < H.rows ? near32(targets[t] - v0) : -1, zt + t);
     if (lane < 16) red[wm * Tl::BN + tl + 16 * j] = s;
   }
   __syncthreads();
@@ -134,7 +145,8 @@ __global__ __launch_bounds__(kThinThreads) void ce_stats_thin_kernel(Operand W, 
 #pragma unroll
   for (int j = 0; j < TF; ++j) {
     const int64_t t = 16 * j + (lane & 15);
-    const float2 s = column_stats(acc, j, m0 + 4 * (lane >> 4), W.rows, t, t < H.rows ? targets[t] : -1, zt);
+    const int64_t v = m0 + 4 * (lane >> 4);
+    const float2 s = column_stats(acc, j, near32(W.rows - v), t < H.rows ? near32(targets[t] - v) : -1, zt + t);
     if (lane < 16 && t < H.rows) part[blockIdx.x * H.rows + t] = s;
   }
 }
@@ -233,16 +245,28 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
       g = dloss[t] / *unit;
     }
     const bool counted = y >= 0 && y < V;
-    y = counted ? y - v_first : -1;
+    const int yl = counted ? near32(y - v_first - v0) : -1, left = near32(W.rows - v0);
+#pragma unroll
+    for (int i = 0; i < Tl::TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = exp_of(acc[i][j][r] - l) * g;
+    // the target and the vocabulary's end, rare among tiles, and tokens that are not counted
+    if (yl >= 0 && yl < 16 * Tl::TM && (yl & 15) < 4)
+#pragma unroll
+      for (int i = 0; i < Tl::TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (yl == 16 * i + r) acc[i][j][r] = acc[i][j][r] - g;
+    if (left < 16 * Tl::TM || !counted)
+#pragma unroll
+      for (int i = 0; i < Tl::TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * i + r >= left || !counted) acc[i][j][r] = 0.0f;
 #pragma unroll
     for (int i = 0; i < Tl::TM; ++i) {
+      const f32x4 q = acc[i][j];
       const int64_t v = v0 + 16 * i;
-      f32x4 q;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float p = exp_of(acc[i][j][r] - l) - (v + r == y ? 1.0f : 0.0f);
-        q[r] = counted && v + r < W.rows ? p * g : 0.0f;
-      }
       if constexpr (sizeof(E) == 2) {
         *reinterpret_cast<uint2*>(Tile16<Tl::BM>::at(tile_lds, (int)(t - n0), (int)(v - m0))) =
             make_uint2(pack_bf16x2(q[0], q[1]), pack_bf16x2(q[2], q[3]));

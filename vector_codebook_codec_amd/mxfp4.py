@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _ODT, _WDT, _dev, _matrix, _raw_stream, _temporary
+from .codec import _ODT, _WDT, _dev, _matrix, _new, _raw_stream, _temporary
 
 __all__ = [
     "qamw_mxfp4_dequantize",
@@ -64,17 +64,17 @@ def qamw_mxfp4_quantize(W: torch.Tensor, values_dtype=None, codes: Optional[torc
         raise ValueError("W must be float32, bfloat16 or float16")
     rb, sb = _sizes(d)
     if codes is None and scales is None:
-        codes = torch.empty((N, rb), dtype=torch.uint8, device=W.device)
-        scales = torch.empty((N, sb), dtype=torch.uint8, device=W.device)
+        codes = _new(N, rb, torch.uint8, W)
+        scales = _new(N, sb, torch.uint8, W)
     else:
-        codes = torch.empty((N, rb), dtype=torch.uint8, device=W.device) if codes is None else codes
-        scales = torch.empty((N, sb), dtype=torch.uint8, device=W.device) if scales is None else scales
+        codes = _new(N, rb, torch.uint8, W) if codes is None else codes
+        scales = _new(N, sb, torch.uint8, W) if scales is None else scales
         if _quantised(codes, scales, d) != N:
             raise ValueError(f"codes and scales must have {N} rows")
     vptr, vdt, ldv = None, 0, d
     if values is not None or values_dtype is not None:
         if values is None:
-            values = torch.empty((N, d), dtype=values_dtype, device=W.device)
+            values = _new(N, d, values_dtype, W)
         n2, d2, ldv = _matrix(values, "values")
         vdt = _ODT.get(values.dtype)
         if n2 != N or d2 != d or vdt is None or (values_dtype or values.dtype) != values.dtype:
@@ -92,7 +92,7 @@ def qamw_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int, out
     """The [N][d] values of a quantised matrix in out_dtype (fp32, bf16 or fp16)."""
     N = _quantised(codes, scales, d)
     if out is None:
-        out = torch.empty((N, d), dtype=out_dtype, device=codes.device)
+        out = _new(N, d, out_dtype, codes)
     n2, d2, ldo = _matrix(out, "out")
     odt = _ODT.get(out.dtype)
     if n2 != N or d2 != d or odt is None:
@@ -115,7 +115,7 @@ def qamw_mxfp4_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
         raise ValueError("X must be float32, bfloat16 or float16")
     N = _quantised(codes, scales, d)
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=X.device)
+        out = _new(T, N, out_dtype, X)
     t2, n2, ldy = _matrix(out, "out")
     ydt = _WDT.get(out.dtype)
     if t2 != T or n2 != N or ydt is None:
