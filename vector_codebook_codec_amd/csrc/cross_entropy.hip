@@ -53,7 +53,10 @@ __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f3
 
 // ---------------------------------------------------------------------------
 // Tile statistics of the logits: part[tile][t] = (max, sum of exp(z - max)),
-// and the target's logit from the one tile that holds it.
+// and the target's logit from the one tile that holds it.  Bound by the
+// matrix instructions, and by the power they draw: T = 2048, V = 32000, d = 4096
+// bf16 takes 425 us, 1.26 PFLOP/s, at 1.8 to 1.9 GHz; a library product of
+// that size runs at 1.20 PFLOP/s.
 // ---------------------------------------------------------------------------
 // Of one 16-token column of fragments: lane group l / 16 holds the entries
 // 16 i + r past the lane's first one, `left` of them (or more) inside the
@@ -130,7 +133,9 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Opera
   }
 }
 
-// The same for up to 16 TF tokens, a tile of 16 RF vocabulary entries.
+// The same for up to 16 TF tokens, a tile of 16 RF vocabulary entries: bound
+// by reading the head once (T = 1, V = 32000, d = 4096 bf16: 48 us, 5.4 TB/s of
+// the 5.9 that a plain read reaches).
 template <class Op, int RF, int TF, int U>
 __global__ __launch_bounds__(kThinThreads) void ce_stats_thin_kernel(Operand W, Operand H, int kchunks,
                                                                      const int64_t* __restrict__ targets,
@@ -215,7 +220,8 @@ __global__ __launch_bounds__(1024) void ce_upstream_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------------------
-// G / unit of one piece: vocabulary entries v_first + [0, W.rows).  G [T][vp] and
+// G / unit of one piece, in the logits' tiles (T = 4096, 20480 entries, d =
+// 4096 bf16: 535 us, 1.28 PFLOP/s, 60 us of it writing G twice): vocabulary entries v_first + [0, W.rows).  G [T][vp] and
 // Gt [W.rows][tp]; the columns past W.rows (to vp) and past T (to tp) are 0.
 // ---------------------------------------------------------------------------
 template <class Tl, class Op>
@@ -302,7 +308,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
 // ---------------------------------------------------------------------------
 // out[c][r] = in[r][c] for r < R and 0 for R <= r < rp; rows whose target is
 // not counted read as 0 (targets NULL: all rows count).  64 x 64 tiles
-// through LDS.
+// through LDS, 16 bytes a lane on both sides: 20480 x 4096 bf16 60 us, 5.6 TB/s.
 // ---------------------------------------------------------------------------
 template <class E>
 __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__ in, int64_t pitch, int64_t R, int64_t C,
@@ -353,6 +359,7 @@ __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__
 // ---------------------------------------------------------------------------
 // C[n][m] = unit sum_k A[m][k] B[n][k] (unit NULL: 1) over K steps split among
 // gridDim.y workgroups: split s writes (or adds to) C + s * split_stride.
+// 4096 x 20480 x 4096 bf16: 470 us, 1.46 PFLOP/s.
 // ---------------------------------------------------------------------------
 template <class Tl, class Out>
 __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Operand B, int kchunks, int tiles_m,
