@@ -199,7 +199,8 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(const float2* __restrict
 // The largest |dloss| of the counted tokens, or 1 where that is 0 or not
 // finite.  G is kept relative to it: under a mean loss, whose upstream
 // gradients are all the same number, -1 + p is then what is rounded to bf16,
-// and not a multiple of an arbitrary factor.
+// and not a multiple of an arbitrary factor.  (fp32 inputs go without: unit is
+// NULL for them, and 1.)
 __global__ __launch_bounds__(1024) void ce_upstream_kernel(const float* __restrict__ dloss,
                                                            const int64_t* __restrict__ targets, int64_t T, int64_t V,
                                                            float* __restrict__ unit) {
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
     if (t < H.rows) {
       y = targets[t];
       l = lse[t];
-      g = dloss[t] / *unit;
+      g = unit ? dloss[t] / *unit : dloss[t];
     }
     const bool counted = y >= 0 && y < V;
     const int yl = counted ? near32(y - v_first - v0) : -1, left = near32(W.rows - v0);
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(256) void ce_dw_thin_kernel(const E* __restrict__ G
   stage_g<E, TT>(g, G, vp, v0, count, T);
   __syncthreads();
   if (c >= d) return;
-  const float u = *unit;
+  const float u = unit ? *unit : 1.0f;
   float h[TT][C];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(256) void ce_sum_blocks_kernel(const float* __restr
   if (k || e >= n) return;
 #pragma unroll
   for (int q = 1; q < 16; ++q) s += red[q][i];
-  store4(out + e / per * ldo + e % per * 4, s * *unit);
+  store4(out + e / per * ldo + e % per * 4, unit ? s * *unit : s);
 }
 
 // dH = unit times the fp32 sums of the splits, in order, rounded once
@@ -557,7 +558,7 @@ template <class E>
 __global__ __launch_bounds__(256) void ce_sum_splits_kernel(const float* __restrict__ part, int splits, int64_t stride,
                                                             int64_t T, int d, const float* __restrict__ unit,
                                                             E* __restrict__ out, int64_t ldo) {
-  const float u = *unit;
+  const float u = unit ? *unit : 1.0f;
   const int64_t per = d / 4, n = T * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     f32x4 s = reinterpret_cast<const f32x4*>(part)[i];
@@ -773,9 +774,13 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
   float *unit = (float*)(w + p.unit), *sum = (float*)(w + p.sum);
   const int64_t split_stride = T * (int64_t)d;
   const unsigned dtiles = (unsigned)std::min<int64_t>((d + 63) / 64, 65535);
-  hipLaunchKernelGGL(ce_upstream_kernel, dim3(1), dim3(1024), 0, st, dloss, targets, T, V, unit);
-  int rc = check_launch("ce_upstream_kernel");
-  if (rc) return rc;
+  int rc;
+  if (es == 2) {
+    hipLaunchKernelGGL(ce_upstream_kernel, dim3(1), dim3(1024), 0, st, dloss, targets, T, V, unit);
+    if ((rc = check_launch("ce_upstream_kernel"))) return rc;
+  } else {
+    unit = nullptr;
+  }
   E* const Gt_out = dW && !p.thin ? Gt : nullptr;
   if (dW && !p.thin) {
     hipLaunchKernelGGL((ce_transpose_kernel<E>), dim3((unsigned)((p.tp + 63) / 64), dtiles), dim3(256), 0, st,
@@ -807,7 +812,10 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
                          (const E*)W + v0 * ldw, ldw, n, (int64_t)d, Wt, p.vp, (const int64_t*)nullptr, V);
       if ((rc = check_launch("ce_transpose_kernel"))) return rc;
       const Operand a = {(const char*)Wt, p.vp * es, d, nullptr, 0}, b = {(const char*)G, p.vp * es, T, nullptr, 0};
-      if ((rc = product<Op, float>(a, b, (int)(np / Op::kElems), p.dh, nullptr, sum, d, split_stride, v0 > 0, st))) return rc;
+      const int kc = (int)(np / Op::kElems);
+      if (n == V && p.dh.splits == 1)                               // one piece, one sum: the result itself
+        return product<Op, E>(a, b, kc, p.dh, unit, (E*)dH, lddh, 0, false, st);
+      if ((rc = product<Op, float>(a, b, kc, p.dh, nullptr, sum, d, split_stride, v0 > 0, st))) return rc;
     }
   }
   if (!dH) return QAMW_OK;
