@@ -120,6 +120,63 @@ def test_loss_and_gradient(q, T, V, d, dt, scale):
     check_grad(dH, dW, H, W, y, g, dt)
 
 
+@pytest.mark.parametrize("T,V,d,dt", [
+    (4001, 4100, 64, "bf16"), (4001, 4090, 32, "f32"),           # logits in the largest tiles
+    (4090, 300, 4096, "bf16"), (2050, 200, 2048, "f32"),         # dH in the largest tiles
+    (64, 4100, 4096, "bf16"), (1030, 1500, 1032, "bf16"),        # dW in the largest tiles; middle ones
+    (3, 2100, 2048, "bf16"), (16, 1100, 4096, "bf16"), (7, 4200, 520, "f32")])   # few tokens, a head over 8 MB
+def test_tile_shapes(q, T, V, d, dt):
+    """Sizes that take every tile shape and the few-token form in the logits and in both products."""
+    say(f"case tile shapes T={T} V={V} d={d} {dt}")
+    H, W, y, g = make(T, V, d, dt, T + V)
+    loss, lse = q.qamw_cross_entropy(H, W, y)
+    dH, dW = q.qamw_cross_entropy_grad(H, W, y, lse, g)
+    dH2, dW2 = q.qamw_cross_entropy_grad(H, W, y, lse, g)
+    torch.cuda.synchronize()
+    assert torch.equal(dH, dH2) and torch.equal(dW, dW2)
+    check_loss(loss, lse, H, W, y)
+    check_grad(dH, dW, H, W, y, g, dt)
+
+
+@pytest.mark.parametrize("T", [3, 16])
+def test_few_tokens_masks_and_strides(q, T):
+    """The few-token form: hidden states that are not counted hold NaN, operands and gradients are column ranges of
+    wider matrices, and the gradients come alone too."""
+    say(f"case few tokens T={T}")
+    V, d = 3000, 2048
+    H, W, y, g = make(T, V, d + 24, "bf16", 30 + T)
+    H, W = H[:, 8:8 + d], W[:, 16:16 + d]
+    y[0], y[T - 1], y[1] = 5, -7, 5
+    H[T - 1] = float("nan")
+    g[T - 1] = float("inf")
+    big_h = torch.full((T, d + 16), -77.0, dtype=torch.bfloat16, device=DEV)
+    big_w = torch.full((V, d + 32), -77.0, dtype=torch.bfloat16, device=DEV)
+    loss, lse = q.qamw_cross_entropy(H, W, y)
+    q.qamw_cross_entropy_grad(H, W, y, lse, g, dH=big_h[:, 8:8 + d], dW=big_w[:, 16:16 + d])
+    dH, _ = q.qamw_cross_entropy_grad(H, W, y, lse, g, need_dW=False)
+    _, dW = q.qamw_cross_entropy_grad(H, W, y, lse, g, need_dH=False)
+    torch.cuda.synchronize()
+    assert torch.equal(dH, big_h[:, 8:8 + d]) and torch.equal(dW, big_w[:, 16:16 + d])
+    check_grad(dH, dW, H, W, y, g, "bf16")
+    for b, o in ((big_h, 8), (big_w, 16)):
+        assert (b[:, :o] == -77).all() and (b[:, o + d:] == -77).all()
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1.0 / 3686, 1e20])
+def test_upstream_scale(q, scale):
+    """Upstream gradients far from 1, all the same or not: G is kept relative to the largest."""
+    say(f"case upstream scale {scale}")
+    H, W, y, g = make(90, 400, 64, "bf16", 21)
+    _, lse = q.qamw_cross_entropy(H, W, y)
+    for up in (torch.full_like(g, scale), g * scale):
+        dH, dW = q.qamw_cross_entropy_grad(H, W, y, lse, up)
+        torch.cuda.synchronize()
+        check_grad(dH, dW, H, W, y, up, "bf16")
+    dH, dW = q.qamw_cross_entropy_grad(H, W, y, lse, torch.zeros_like(g))
+    torch.cuda.synchronize()
+    assert not dH.any() and not dW.any()
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_one_gradient_alone(q, dt):
     H, W, y, g = make(70, 333, 96, dt, 4)

@@ -157,6 +157,23 @@ def test_product(q, T, N, d, xdt, ydt):
     check_product(Y, X, codes, scales, ydt)
 
 
+@pytest.mark.parametrize("T,N,d,ydt", [
+    (4001, 4090, 160, "bf16"), (4100, 4099, 72, "f32"),          # a round of the largest tiles, and one tile more
+    (130, 300, 8192, "bf16"), (1000, 900, 8200, "f32"),          # few tiles, long rows: K in shares
+    (1000, 2200, 1056, "bf16"), (32, 8185, 416, "f32"), (20, 600, 4000, "bf16"), (16, 8190, 640, "bf16")])
+def test_product_tile_shapes(q, T, N, d, ydt):
+    """Products large enough, or long enough, to take every tile shape and the splits of the contraction."""
+    say(f"case tile shapes T={T} N={N} d={d} {ydt}")
+    W = weights(N, d, "f32", N).to(DEV)
+    X = weights(T, d, "bf16", T).to(DEV)
+    codes, scales = q.qamw_mxfp4_quantize(W)
+    Y = q.qamw_mxfp4_matmul(X, codes, scales, out_dtype=DT[ydt])
+    Y2 = q.qamw_mxfp4_matmul(X, codes, scales, out_dtype=DT[ydt])
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Y2)
+    check_product(Y, X, codes, scales, ydt)
+
+
 @pytest.mark.parametrize("T", [1, 5, 40, 200])
 def test_product_wide_scales(q, T):
     """Block scales over the format's range, whose products stay inside fp32."""

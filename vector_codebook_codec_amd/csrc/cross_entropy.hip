@@ -18,7 +18,9 @@
 // over the pieces in fp32.  Every product contracts along the operands' rows,
 // which is why H and each piece of W are also laid out transposed.  G is
 // rounded to bf16 for bf16 inputs, like H and W themselves: its relative
-// error 2^-9 is below that of the rounded gradients it is summed into.
+// error 2^-9 is below that of the rounded gradients it is summed into.  For a
+// few tokens and a large head both products run without matrix instructions
+// and transposed copies.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -646,18 +648,20 @@ int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ld
                         : ce_as<OpBf16>(H, T, d, ldh, W, V, ldw, targets, loss, lse, ws, st);
 }
 
+constexpr int64_t kPieceTile = kShapeTile[kShapes - 1];
 // G, Gt and Wt of one piece.  More of it means fewer launches, each with a
 // last round of workgroups that fills the CUs badly: T = 4096, V = 131072,
 // d = 4096 takes 15.1 ms at 128 MiB, 14.7 ms at 420 MiB and 14.5 ms at
 // 820 MiB.
-constexpr int64_t kPieceTile = kShapeTile[kShapes - 1];
 constexpr int64_t kCeBudget = (int64_t)512 << 20;
+
 // Whether the products run without transposed copies and matrix instructions:
 // for a few tokens and a head of some size, whose copies would cost more than
 // all else (V = 32000, d = 4096, bf16: T = 1 224 us against 356 us, T = 16 273
 // us, T = 17 361 us; V = 5003, d = 512: fp32, 10 MB, T = 16 57 us, T = 17 66
 // us, but bf16, 5 MB, 50 us and 42 us).
 static bool thin_gradient(int64_t T, int64_t V, int d, int es) { return T <= 16 && V * d * es >= (int64_t(8) << 20); }
+
 // Sizes and places of the gradient's workspace.
 struct CeGradPlan {
   int64_t piece;            // vocabulary entries per piece

@@ -229,11 +229,11 @@ __global__ __launch_bounds__(kBlockThreads) void mx4_dequantize_kernel(const uin
 // instruction multiplies 128 four-bit products per result and applies both
 // blocks' scales, so nothing is decoded.  Weights are the A operand: a lane
 // then holds 4 consecutive channels n of one token.  T = 8192, 11008 x 4096: 240
-// us, 3.1 PFLOP/s (255 us with the quantisation of X).  The K steps alone run at
-// 4.4 PFLOP/s, where LDS, read and written through in each step, and the
-// matrix instructions (45 % busy) take turns; a sixth of the time are the sixth
-// round of tiles, of which 0.4 is used, and a tile's first loads and stores,
-// 1.5 K steps in 16.
+// us, 3.1 PFLOP/s (255 us with the quantisation of X).  Long rows run at 4.2 to
+// 4.4 PFLOP/s, whatever the order of LDS reads and matrix instructions, at a
+// falling clock: power (the instructions alone, on registers, reach 6.8).  With
+// 16 K steps a tile's first loads and its stores add 4 steps' time, and of the
+// sixth round of tiles 0.4 is used.
 // ---------------------------------------------------------------------------
 template <class Out>
 __device__ __forceinline__ void store_y(typename Out::T* Y, int64_t ldy, int64_t t, int64_t n, int64_t N, f32x4 v) {
@@ -533,7 +533,7 @@ static int matmul_to(const TailPlan& p, const Operand& W, const Operand& X, int 
 
 // A workgroup of the thin product takes 32 channels where that still gives
 // every CU one, else 16 (T = 13: 4096 x 11008 13.5 us with 16, 16.3 us with
-// 32; T = 32: 11008 x 4096 17.4 and 17.7 us).  The fused form takes 16: its
+// 32; T = 16: 11008 x 4096 13.6 us with 32).  The fused form takes 16: its
 // registers allow two workgroups a CU only then (T = 1, 11008 x 4096: 10.9 us
 // against 12.1 us).
 template <int RF, int TF, class In, class Out, bool kFused>
@@ -547,7 +547,7 @@ static int thin_rows(const Operand& W, const Operand& Xq, const void* X, int d, 
 template <int TF, class In, class Out, bool kFused>
 static int matmul_thin(const Operand& W, const Operand& Xq, const void* X, int d, int64_t ldx, int kchunks, void* Y, int64_t ldy,
                        hipStream_t st) {
-  if constexpr (!kFused)
+  if constexpr (!kFused && TF == 1)
     if (tiles_of(W.rows, 32) >= kCus) return thin_rows<2, TF, In, Out, kFused>(W, Xq, X, d, ldx, kchunks, Y, ldy, st);
   return thin_rows<1, TF, In, Out, kFused>(W, Xq, X, d, ldx, kchunks, Y, ldy, st);
 }
