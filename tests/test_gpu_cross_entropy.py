@@ -121,9 +121,10 @@ def test_loss_and_gradient(q, T, V, d, dt, scale):
 
 
 @pytest.mark.parametrize("T,V,d,dt", [
-    (4001, 4100, 64, "bf16"), (4001, 4090, 32, "f32"),           # logits in the largest tiles
+    (4001, 4100, 64, "bf16"), (4001, 4090, 64, "bf16"), (4001, 4090, 32, "f32"),   # logits in the largest tiles
     (4090, 300, 4096, "bf16"), (2050, 200, 2048, "f32"),         # dH in the largest tiles
-    (64, 4100, 4096, "bf16"), (1030, 1500, 1032, "bf16"),        # dW in the largest tiles; middle ones
+    (64, 4090, 4096, "bf16"), (32, 4090, 4096, "f32"),           # dW in the largest tiles
+    (64, 4100, 4096, "bf16"), (1030, 1500, 1032, "bf16"),        # middle ones
     (3, 2100, 2048, "bf16"), (16, 1100, 4096, "bf16"), (7, 4200, 520, "f32")])   # few tokens, a head over 8 MB
 def test_tile_shapes(q, T, V, d, dt):
     """Sizes that take every tile shape and the few-token form in the logits and in both products."""
