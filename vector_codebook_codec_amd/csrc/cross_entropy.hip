@@ -191,10 +191,11 @@ __global__ __launch_bounds__(256) void ce_finish_kernel(const float2* __restrict
   }
   if (k == 0 && t < T) {
     const float2 a = red[0][i];
-    const float l = (a.x == -INFINITY ? 0.0f : a.x) + logf(a.y);
+    const float top = a.x == -INFINITY ? 0.0f : a.x, rest = logf(a.y);
     const int64_t y = targets[t];
-    lse[t] = l;
-    loss[t] = (y >= 0 && y < V) ? l - zt[t] : 0.0f;
+    lse[t] = top + rest;
+    // the largest logit and the target's first: where they are one, a small loss keeps its digits
+    loss[t] = (y >= 0 && y < V) ? (top - zt[t]) + rest : 0.0f;
   }
 }
 
