@@ -466,8 +466,9 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  *            rows; either may be NULL and is then not computed
  *   lse      (gradient) as qamw_cross_entropy wrote it for these inputs
  * Arithmetic: products of the inputs as they are, summed in fp32 on matrix
- * cores; statistics in fp32.  For bf16 inputs G is rounded to bf16 before it
- * is multiplied; dH and dW are summed in fp32 and rounded once.  All sums have
+ * cores; statistics in fp32.  For bf16 inputs G, relative to the largest
+ * counted |dloss|, is rounded to bf16 before it is multiplied (not for few
+ * tokens); dH and dW are summed in fp32 and rounded once.  All sums have
  * a fixed order.  T = 0 is valid (dW is then written as 0).  Rows of H, W and
  * of a T-element row of dtype must be under 4 MiB (T <= 2^20 for fp32).
  *   workspace >= qamw_cross_entropy_workspace_bytes(T, V, d, dtype) or

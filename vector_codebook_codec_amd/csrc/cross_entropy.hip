@@ -228,12 +228,11 @@ __global__ __launch_bounds__(1024) void ce_upstream_kernel(const float* __restri
 // 4096 bf16: 535 us, 1.28 PFLOP/s, 60 us of it writing G twice): vocabulary entries v_first + [0, W.rows).  G [T][vp] and
 // Gt [W.rows][tp]; the columns past W.rows (to vp) and past T (to tp) are 0.
 // ---------------------------------------------------------------------------
-template <class Tl, class Op>
+template <class Tl, class Op, class E>
 __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
     Operand W, Operand H, int kchunks, int tiles_m, int tiles_n, const int64_t* __restrict__ targets, int64_t v_first,
     int64_t V, const float* __restrict__ lse, const float* __restrict__ dloss, const float* __restrict__ unit,
-    typename Elem<Op>::T* __restrict__ G, int64_t vp, typename Elem<Op>::T* __restrict__ Gt, int64_t tp) {   // Gt may be NULL
-  typedef typename Elem<Op>::T E;
+    E* __restrict__ G, int64_t vp, E* __restrict__ Gt, int64_t tp) {                     // Gt may be NULL
   extern __shared__ __align__(1024) char tile_lds[];
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
@@ -408,7 +407,8 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
 // ---------------------------------------------------------------------------
 // The two products for a few tokens: bound by reading W and writing dW once,
 // with no transposed copies.  A thread owns 16 bytes of columns and walks the
-// workgroup's vocabulary entries, whose G lies in LDS as fp32.
+// workgroup's vocabulary entries, whose G lies in LDS.  G is kept in fp32 here,
+// also for bf16 inputs: with few terms in the sums its rounding would show.
 // ---------------------------------------------------------------------------
 template <class E> constexpr int cols_of() { return 16 / sizeof(E); }
 template <class E>
@@ -425,22 +425,17 @@ __device__ __forceinline__ void unpack_cols(u32x4 v, float (&x)[16 / sizeof(E)])
 }
 constexpr int kThinEntries = 128;                                  // vocabulary entries whose G is in LDS at a time
 // g[v][t] = G[t][v0 + v] for v < count, t < T; 0 for T <= t < TT
-template <class E, int TT>
-__device__ __forceinline__ void stage_g(float (&g)[kThinEntries][TT], const E* G, int64_t vp, int64_t v0, int count, int T) {
+template <int TT>
+__device__ __forceinline__ void stage_g(float (&g)[kThinEntries][TT], const float* G, int64_t vp, int64_t v0, int count, int T) {
   for (int k = threadIdx.x; k < kThinEntries * TT; k += 256) {
     const int t = k / kThinEntries, v = k % kThinEntries;
-    float x = 0.0f;
-    if (t < T && v < count) {
-      if constexpr (sizeof(E) == 2) x = bf16_bits_to_f32(G[t * vp + v0 + v]);
-      else x = G[t * vp + v0 + v];
-    }
-    g[v][t] = x;
+    g[v][t] = t < T && v < count ? G[t * vp + v0 + v] : 0.0f;
   }
 }
 
 // sum[block][t][d] (+)= sum over the block's entries v of G[t][v] W[v][:]
 template <class E, int TT>
-__global__ __launch_bounds__(256) void ce_dh_thin_kernel(const E* __restrict__ G, int64_t vp, const E* __restrict__ W,
+__global__ __launch_bounds__(256) void ce_dh_thin_kernel(const float* __restrict__ G, int64_t vp, const E* __restrict__ W,
                                                          int64_t ldw, int64_t n, int per_block, int T, int d,
                                                          float* __restrict__ sum, bool add) {
   constexpr int C = cols_of<E>();
@@ -451,7 +446,7 @@ __global__ __launch_bounds__(256) void ce_dh_thin_kernel(const E* __restrict__ G
   for (int64_t vb = v0; vb < v1; vb += kThinEntries) {
     const int count = (int)min((int64_t)kThinEntries, v1 - vb);
     __syncthreads();
-    stage_g<E, TT>(g, G, vp, vb, count, T);
+    stage_g<TT>(g, G, vp, vb, count, T);
     __syncthreads();
     if (c >= d) continue;
     const E* p = W + vb * ldw + c;
@@ -494,7 +489,7 @@ __global__ __launch_bounds__(256) void ce_dh_thin_kernel(const E* __restrict__ G
 
 // dW[v][:] = unit sum_t G[t][v] H[t][:], the counted tokens t
 template <class E, int TT>
-__global__ __launch_bounds__(256) void ce_dw_thin_kernel(const E* __restrict__ G, int64_t vp, const E* __restrict__ H,
+__global__ __launch_bounds__(256) void ce_dw_thin_kernel(const float* __restrict__ G, int64_t vp, const E* __restrict__ H,
                                                          int64_t ldh, const int64_t* __restrict__ targets, int64_t V,
                                                          int64_t n, int per_block, int T, int d,
                                                          const float* __restrict__ unit, E* __restrict__ dW, int64_t lddw) {
@@ -503,7 +498,7 @@ __global__ __launch_bounds__(256) void ce_dw_thin_kernel(const E* __restrict__ G
   const int c = (blockIdx.y * 256 + threadIdx.x) * C;
   const int64_t v0 = (int64_t)blockIdx.x * per_block;               // per_block <= kThinEntries
   const int count = (int)min((int64_t)per_block, n - v0);
-  stage_g<E, TT>(g, G, vp, v0, count, T);
+  stage_g<TT>(g, G, vp, v0, count, T);
   __syncthreads();
   if (c >= d) return;
   const float u = unit ? *unit : 1.0f;
@@ -656,12 +651,14 @@ constexpr int64_t kPieceTile = kShapeTile[kShapes - 1];
 // 820 MiB.
 constexpr int64_t kCeBudget = (int64_t)512 << 20;
 
-// Whether the products run without transposed copies and matrix instructions:
-// for a few tokens and a head of some size, whose copies would cost more than
-// all else (V = 32000, d = 4096, bf16: T = 1 224 us against 356 us, T = 16 273
+// Whether the products run without transposed copies and matrix instructions
+// (and with G in fp32): for up to 4 tokens, and up to 16 with a head of some
+// size, whose copies would cost more than all else (V = 32000, d = 4096, bf16: T = 1 224 us against 356 us, T = 16 295
 // us, T = 17 361 us; V = 5003, d = 512: fp32, 10 MB, T = 16 57 us, T = 17 66
 // us, but bf16, 5 MB, 50 us and 42 us).
-static bool thin_gradient(int64_t T, int64_t V, int d, int es) { return T <= 16 && V * d * es >= (int64_t(8) << 20); }
+static bool thin_gradient(int64_t T, int64_t V, int d, int es) {
+  return T <= kThinTokens || (T <= 16 && V * d * es >= (int64_t(8) << 20));
+}
 
 // Sizes and places of the gradient's workspace.
 struct CeGradPlan {
@@ -695,7 +692,7 @@ static CeGradPlan ce_grad_plan(int64_t T, int64_t V, int d, int es) {
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += round_up(bytes, 256); return o; };
   p.unit = take(sizeof(float));
-  p.g = take((size_t)T * p.vp * es);
+  p.g = take((size_t)T * p.vp * (p.thin ? sizeof(float) : es));
   p.gt = p.wt = p.ht = 0;
   if (!p.thin) {
     p.gt = take((size_t)p.piece * p.tp * es);
@@ -708,12 +705,12 @@ static CeGradPlan ce_grad_plan(int64_t T, int64_t V, int d, int es) {
 }
 size_t ce_grad_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt) { return ce_grad_plan(T, V, d, elem_size(dt)).bytes; }
 
-template <class Op, class Tl>
+template <class Op, class Tl, class E>
 static int softmax_grad_tiled(const Operand& W, const Operand& H, int kchunks, const int64_t* targets, int64_t v0, int64_t V,
-                              const float* lse, const float* dloss, const float* unit, typename Elem<Op>::T* G, int64_t vp,
-                              typename Elem<Op>::T* Gt, int64_t tp, hipStream_t st) {
+                              const float* lse, const float* dloss, const float* unit, E* G, int64_t vp, E* Gt, int64_t tp,
+                              hipStream_t st) {
   const int tm = (int)tiles_of(W.rows, Tl::BM), tn = (int)tiles_of(H.rows, Tl::BN);
-  auto kernel = ce_softmax_grad_kernel<Tl, Op>;
+  auto kernel = ce_softmax_grad_kernel<Tl, Op, E>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, H, kchunks, tm, tn,
                      targets, v0, V, lse, dloss, unit, G, vp, Gt, tp);
   return check_launch("ce_softmax_grad_kernel");
@@ -744,7 +741,7 @@ static int with_tokens(int64_t T, F&& f) {
   return f(std::integral_constant<int, 16>());
 }
 template <class E>
-static int dh_thin(const E* G, int64_t vp, const E* W, int64_t ldw, int64_t n, int blocks, int64_t T, int d, float* sum, bool add,
+static int dh_thin(const float* G, int64_t vp, const E* W, int64_t ldw, int64_t n, int blocks, int64_t T, int d, float* sum, bool add,
                    hipStream_t st) {
   return with_tokens(T, [&](auto tt) {
     auto kernel = ce_dh_thin_kernel<E, decltype(tt)::value>;
@@ -754,7 +751,7 @@ static int dh_thin(const E* G, int64_t vp, const E* W, int64_t ldw, int64_t n, i
   });
 }
 template <class E>
-static int dw_thin(const E* G, int64_t vp, const E* H, int64_t ldh, const int64_t* targets, int64_t V, int64_t n, int64_t T, int d,
+static int dw_thin(const float* G, int64_t vp, const E* H, int64_t ldh, const int64_t* targets, int64_t V, int64_t n, int64_t T, int d,
                    const float* unit, E* dW, int64_t lddw, hipStream_t st) {
   return with_tokens(T, [&](auto tt) {
     auto kernel = ce_dw_thin_kernel<E, decltype(tt)::value>;
@@ -797,15 +794,23 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
     const Operand Wp = {(const char*)W + v0 * ldw * es, ldw * es, n, nullptr, 0};
     const Operand Hp = {(const char*)H, ldh * es, T, nullptr, 0};
     const int kd = d / Op::kElems;
-    rc = with_shape<Op>(logits_shape(T, n, d, es), [&](auto tile) {
-      return softmax_grad_tiled<Op, decltype(tile)>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt_out, p.tp, st);
-    });
-    if (rc) return rc;
-    if (p.thin) {
-      if (dW && (rc = dw_thin<E>(G, p.vp, (const E*)H, ldh, targets, V, n, T, d, unit, (E*)dW + v0 * lddw, lddw, st))) return rc;
-      if (dH && (rc = dh_thin<E>(G, p.vp, (const E*)W + v0 * ldw, ldw, n, p.blocks, T, d, sum, v0 > 0, st))) return rc;
+    const int shape = logits_shape(T, n, d, es);
+    if (p.thin) {                                                   // so few tokens take the smallest tiles
+      float* G32 = (float*)G;
+      auto grad = [&](auto tile) {
+        return softmax_grad_tiled<Op, decltype(tile), float>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G32, p.vp, nullptr, 0, st);
+      };
+      if constexpr (std::is_same<Op, OpF32>::value) rc = grad(typename ShapeTile<Op, 1>::T());
+      else rc = shape ? grad(typename ShapeTile<Op, 1>::T()) : grad(typename ShapeTile<Op, 0>::T());
+      if (rc) return rc;
+      if (dW && (rc = dw_thin<E>(G32, p.vp, (const E*)H, ldh, targets, V, n, T, d, unit, (E*)dW + v0 * lddw, lddw, st))) return rc;
+      if (dH && (rc = dh_thin<E>(G32, p.vp, (const E*)W + v0 * ldw, ldw, n, p.blocks, T, d, sum, v0 > 0, st))) return rc;
       continue;
     }
+    rc = with_shape<Op>(shape, [&](auto tile) {
+      return softmax_grad_tiled<Op, decltype(tile), E>(Wp, Hp, kd, targets, v0, V, lse, dloss, unit, G, p.vp, Gt_out, p.tp, st);
+    });
+    if (rc) return rc;
     if (dW) {
       const Operand a = {(const char*)Ht, p.tp * es, d, nullptr, 0}, b = {(const char*)Gt, p.tp * es, n, nullptr, 0};
       const ProductPlan whole = product_plan(product_type(es), d, n, steps_of(p.tp, es), 1);
