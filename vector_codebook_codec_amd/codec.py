@@ -3,8 +3,13 @@
 Each function has the name of the C entry point it calls and only marshals
 arguments: it checks devices, dtypes and shapes, allocates the outputs and
 workspace with torch when the caller passes none, and hands raw pointers plus
-the current HIP stream to libqamw.so.  Every step of the codec runs in the
-library's kernels.
+the current HIP stream, or the one given as ``stream``, to libqamw.so.  Every
+step of the codec runs in the library's kernels.
+
+With ``stream``, tensors that the call allocates are safe to use on that
+stream and, once it has passed the call, on the current one.  The caller
+orders ``stream`` behind what produces the call's arguments and keeps them
+until the call has run.
 """
 from __future__ import annotations
 
@@ -77,9 +82,27 @@ def _codebook(codebook: torch.Tensor) -> int:
     return codebook.shape[0]
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A tensor of n elements or n x d that a call on `stream` fills.  Its block comes from that stream's own pool: what
+    used it before and what will use it after the call are then in order with the call.  A block of the current stream's
+    pool could still be read or written by work queued there.  The current stream, which the caller may use the result
+    on, is recorded as well."""
+    if stream is not None:
+        handle, current = _stream(stream), torch.cuda.current_stream(device)
+        if handle != current.cuda_stream:
+            own = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+            with torch.cuda.stream(own):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    if type(shape) is tuple:                             # two thirds of torch.empty's time
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     # torch's caching allocator returns 256-byte aligned blocks
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return _empty(max(nbytes, 256), torch.uint8, device, stream)
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -96,11 +119,6 @@ def _matrix(t: torch.Tensor, name: str):
     return n, d, ld if n > 1 else d
 
 
-def _new(n: int, d: int, dtype, like: torch.Tensor) -> torch.Tensor:
-    """An uninitialised n x d matrix on like's device."""
-    return torch.empty_strided((n, d), (d, 1), dtype=dtype, device=like.device)
-
-
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -109,16 +127,6 @@ def _raw_stream(stream) -> int:
     if stream is None and _current_raw_stream is not None:
         return _current_raw_stream(torch.cuda.current_device())
     return _stream(stream)
-
-
-def _temporary(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace that the caller does not see: kept from reuse until `stream`, where that is not the current one,
-    has passed the call."""
-    t = _workspace(nbytes, device)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                        else torch.cuda.ExternalStream(_stream(stream), device=device))
-    return t
 
 
 def load_codebook(K: int) -> np.ndarray:
@@ -158,7 +166,7 @@ def qamw_build_plan(codebook: torch.Tensor, plan: Optional[torch.Tensor] = None,
     if need <= 0:
         raise ValueError(f"unsupported K={K}")
     if plan is None:
-        plan = torch.empty(need, dtype=torch.uint8, device=codebook.device)
+        plan = _empty(need, torch.uint8, codebook.device, stream)
     _dev(plan, "plan")
     if plan.dtype != torch.uint8 or not plan.is_contiguous():
         raise ValueError("plan must be a contiguous uint8 tensor")
@@ -176,14 +184,14 @@ def qamw_calibrate(W: torch.Tensor, chan_rms: torch.Tensor, alpha: float, block:
         raise ValueError("W must be float32 or bfloat16")
     _vec(chan_rms, "chan_rms", d)
     if s_out is None:
-        s_out = torch.empty(d, dtype=torch.float32, device=W.device)
+        s_out = _empty(d, torch.float32, W.device, stream)
     if sigma_out is None:
-        sigma_out = torch.empty(d // 2, dtype=torch.float32, device=W.device)
+        sigma_out = _empty(d // 2, torch.float32, W.device, stream)
     _vec(s_out, "s_out", d)
     _vec(sigma_out, "sigma_out", d // 2)
     need = qamw_calibrate_workspace_bytes(N, d, block)
     if workspace is None:
-        workspace = _workspace(need, W.device)
+        workspace = _workspace(need, W.device, stream)
     _lib.check("qamw_calibrate", _lib.load().qamw_calibrate(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, chan_rms.data_ptr(), float(alpha), int(block),
         int(sign_seed), s_out.data_ptr(), sigma_out.data_ptr(), workspace.data_ptr(),
@@ -213,16 +221,16 @@ def qamw_encode(W: torch.Tensor, s: torch.Tensor, sigma: torch.Tensor, block: in
         if plan.dtype != torch.uint8 or plan.numel() < qamw_plan_bytes(K):
             raise ValueError("plan must be a uint8 tensor from qamw_build_plan for this K")
     if packed is None:
-        packed = torch.empty((N, rw), dtype=torch.int32, device=W.device)
+        packed = _empty((N, rw), torch.int32, W.device, stream)
     if rownorm_f16 is None:
-        rownorm_f16 = torch.empty(N, dtype=torch.int16, device=W.device)
+        rownorm_f16 = _empty(N, torch.int16, W.device, stream)
     _dev(packed, "packed")
     if packed.dtype != torch.int32 or tuple(packed.shape) != (N, rw) or not packed.is_contiguous():
         raise ValueError(f"packed must be a contiguous int32 tensor of shape ({N}, {rw})")
     _vec(rownorm_f16, "rownorm_f16", N, torch.int16)
     need = qamw_encode_workspace_bytes(N, d)
     if workspace is None:
-        workspace = _workspace(need, W.device)
+        workspace = _workspace(need, W.device, stream)
     _lib.check("qamw_encode", _lib.load().qamw_encode(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, s.data_ptr(), sigma.data_ptr(), int(block), int(sign_seed),
         codebook.data_ptr(), K, None if plan is None else plan.data_ptr(), 0 if plan is None else plan.numel(),
@@ -251,9 +259,9 @@ def qamw_encode_noalloc(W: torch.Tensor, s: torch.Tensor, sigma: torch.Tensor, b
         if plan.dtype != torch.uint8 or plan.numel() < qamw_plan_bytes(K):
             raise ValueError("plan must be a uint8 tensor from qamw_build_plan for this K")
     if packed is None:
-        packed = torch.empty((N, rw), dtype=torch.int32, device=W.device)
+        packed = _empty((N, rw), torch.int32, W.device, stream)
     if rownorm_f16 is None:
-        rownorm_f16 = torch.empty(N, dtype=torch.int16, device=W.device)
+        rownorm_f16 = _empty(N, torch.int16, W.device, stream)
     _dev(packed, "packed")
     if packed.dtype != torch.int32 or tuple(packed.shape) != (N, rw) or not packed.is_contiguous():
         raise ValueError(f"packed must be a contiguous int32 tensor of shape ({N}, {rw})")
@@ -280,16 +288,16 @@ def qamw_calibrate_prepare(W: torch.Tensor, chan_rms: torch.Tensor, alpha: float
         raise ValueError("W must be float32 or bfloat16")
     _vec(chan_rms, "chan_rms", d)
     if s_out is None:
-        s_out = torch.empty(d, dtype=torch.float32, device=W.device)
+        s_out = _empty(d, torch.float32, W.device, stream)
     if sigma_out is None:
-        sigma_out = torch.empty(d // 2, dtype=torch.float32, device=W.device)
+        sigma_out = _empty(d // 2, torch.float32, W.device, stream)
     if rownorm_f16 is None:
-        rownorm_f16 = torch.empty(N, dtype=torch.int16, device=W.device)
+        rownorm_f16 = _empty(N, torch.int16, W.device, stream)
     _vec(s_out, "s_out", d)
     _vec(sigma_out, "sigma_out", d // 2)
     _vec(rownorm_f16, "rownorm_f16", N, torch.int16)
     if workspace is None:
-        workspace = _workspace(qamw_calibrate_encode_workspace_bytes(N, d), W.device)
+        workspace = _workspace(qamw_calibrate_encode_workspace_bytes(N, d), W.device, stream)
     _dev(workspace, "workspace")
     _lib.check("qamw_calibrate_prepare", _lib.load().qamw_calibrate_prepare(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, chan_rms.data_ptr(), float(alpha), int(block), int(sign_seed),
@@ -318,13 +326,13 @@ def qamw_calibrate_encode(W: torch.Tensor, chan_rms: torch.Tensor, alpha: float,
         if plan.dtype != torch.uint8 or plan.numel() < qamw_plan_bytes(K):
             raise ValueError("plan must be a uint8 tensor from qamw_build_plan for this K")
     if s_out is None:
-        s_out = torch.empty(d, dtype=torch.float32, device=W.device)
+        s_out = _empty(d, torch.float32, W.device, stream)
     if sigma_out is None:
-        sigma_out = torch.empty(d // 2, dtype=torch.float32, device=W.device)
+        sigma_out = _empty(d // 2, torch.float32, W.device, stream)
     if packed is None:
-        packed = torch.empty((N, rw), dtype=torch.int32, device=W.device)
+        packed = _empty((N, rw), torch.int32, W.device, stream)
     if rownorm_f16 is None:
-        rownorm_f16 = torch.empty(N, dtype=torch.int16, device=W.device)
+        rownorm_f16 = _empty(N, torch.int16, W.device, stream)
     _vec(s_out, "s_out", d)
     _vec(sigma_out, "sigma_out", d // 2)
     _dev(packed, "packed")
@@ -332,7 +340,7 @@ def qamw_calibrate_encode(W: torch.Tensor, chan_rms: torch.Tensor, alpha: float,
         raise ValueError(f"packed must be a contiguous int32 tensor of shape ({N}, {rw})")
     _vec(rownorm_f16, "rownorm_f16", N, torch.int16)
     if workspace is None:
-        workspace = _workspace(qamw_calibrate_encode_workspace_bytes(N, d), W.device)
+        workspace = _workspace(qamw_calibrate_encode_workspace_bytes(N, d), W.device, stream)
     _lib.check("qamw_calibrate_encode", _lib.load().qamw_calibrate_encode(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, chan_rms.data_ptr(), float(alpha), int(block), int(sign_seed),
         codebook.data_ptr(), K, None if plan is None else plan.data_ptr(), 0 if plan is None else plan.numel(),
@@ -352,10 +360,10 @@ def qamw_encode_prepare(W: torch.Tensor, s: torch.Tensor, sigma: torch.Tensor, b
     _vec(s, "s", d)
     _vec(sigma, "sigma", d // 2)
     if rownorm_f16 is None:
-        rownorm_f16 = torch.empty(N, dtype=torch.int16, device=W.device)
+        rownorm_f16 = _empty(N, torch.int16, W.device, stream)
     _vec(rownorm_f16, "rownorm_f16", N, torch.int16)
     if workspace is None:
-        workspace = _workspace(qamw_encode_workspace_bytes(N, d), W.device)
+        workspace = _workspace(qamw_encode_workspace_bytes(N, d), W.device, stream)
     _lib.check("qamw_encode_prepare", _lib.load().qamw_encode_prepare(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, s.data_ptr(), sigma.data_ptr(), int(block), int(sign_seed),
         rownorm_f16.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -378,7 +386,7 @@ def qamw_encode_indices(W: torch.Tensor, block: int, codebook: torch.Tensor, wor
         if plan.dtype != torch.uint8 or plan.numel() < qamw_plan_bytes(K):
             raise ValueError("plan must be a uint8 tensor from qamw_build_plan for this K")
     if packed is None:
-        packed = torch.empty((N, rw), dtype=torch.int32, device=W.device)
+        packed = _empty((N, rw), torch.int32, W.device, stream)
     _dev(packed, "packed")
     if packed.dtype != torch.int32 or tuple(packed.shape) != (N, rw) or not packed.is_contiguous():
         raise ValueError(f"packed must be a contiguous int32 tensor of shape ({N}, {rw})")
@@ -411,11 +419,11 @@ def qamw_lloyd_update(W: torch.Tensor, block: int, packed: torch.Tensor, codeboo
         raise ValueError(f"packed must be a contiguous int32 tensor of shape ({N}, {rw})")
     _dev(enc_workspace, "enc_workspace")
     if out is None:
-        out = torch.empty((K, 2), dtype=torch.float32, device=W.device)
+        out = _empty((K, 2), torch.float32, W.device, stream)
     if distortion is None:
-        distortion = torch.empty(1, dtype=torch.float64, device=W.device)
+        distortion = _empty(1, torch.float64, W.device, stream)
     if workspace is None:
-        workspace = _workspace(qamw_lloyd_workspace_bytes(K), W.device)
+        workspace = _workspace(qamw_lloyd_workspace_bytes(K), W.device, stream)
     _lib.check("qamw_lloyd_update", _lib.load().qamw_lloyd_update(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, int(block), packed.data_ptr(), codebook.data_ptr(), K,
         enc_workspace.data_ptr(), enc_workspace.numel() * enc_workspace.element_size(), out.data_ptr(),
@@ -436,15 +444,15 @@ def qamw_learn_codebook(W: torch.Tensor, block: int, enc_workspace: torch.Tensor
     rw = qamw_packed_row_words(d, K)
     _dev(enc_workspace, "enc_workspace")
     if out is None:
-        out = torch.empty((K, 2), dtype=torch.float32, device=W.device)
+        out = _empty((K, 2), torch.float32, W.device, stream)
     if distortion is None:
-        distortion = torch.empty(int(iters), dtype=torch.float64, device=W.device)
+        distortion = _empty(int(iters), torch.float64, W.device, stream)
     if plan is None:
-        plan = torch.empty(qamw_plan_bytes(K), dtype=torch.uint8, device=W.device)
+        plan = _empty(qamw_plan_bytes(K), torch.uint8, W.device, stream)
     if packed is None:
-        packed = torch.empty((N, rw), dtype=torch.int32, device=W.device)
+        packed = _empty((N, rw), torch.int32, W.device, stream)
     if workspace is None:
-        workspace = _workspace(qamw_lloyd_workspace_bytes(K), W.device)
+        workspace = _workspace(qamw_lloyd_workspace_bytes(K), W.device, stream)
     _lib.check("qamw_learn_codebook", _lib.load().qamw_learn_codebook(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, int(block), enc_workspace.data_ptr(),
         enc_workspace.numel() * enc_workspace.element_size(), codebook_init.data_ptr(), K, int(iters),
@@ -473,15 +481,15 @@ def qamw_encode_polar(W: torch.Tensor, s: torch.Tensor, sigma: torch.Tensor, blo
     if rw < 0:
         raise ValueError(f"unsupported Ka x Kp = {Ka} x {Kp} or d={d}")
     if packed is None:
-        packed = torch.empty((N, rw), dtype=torch.int32, device=W.device)
+        packed = _empty((N, rw), torch.int32, W.device, stream)
     if rownorm_f16 is None:
-        rownorm_f16 = torch.empty(N, dtype=torch.int16, device=W.device)
+        rownorm_f16 = _empty(N, torch.int16, W.device, stream)
     _dev(packed, "packed")
     if packed.dtype != torch.int32 or tuple(packed.shape) != (N, rw) or not packed.is_contiguous():
         raise ValueError(f"packed must be a contiguous int32 tensor of shape ({N}, {rw})")
     _vec(rownorm_f16, "rownorm_f16", N, torch.int16)
     if workspace is None:
-        workspace = _workspace(qamw_encode_workspace_bytes(N, d), W.device)
+        workspace = _workspace(qamw_encode_workspace_bytes(N, d), W.device, stream)
     _lib.check("qamw_encode_polar", _lib.load().qamw_encode_polar(
         W.data_ptr(), _WDT[W.dtype], N, d, ldw, s.data_ptr(), sigma.data_ptr(), int(block), int(sign_seed),
         levels.data_ptr(), Ka, dirs.data_ptr(), Kp, packed.data_ptr(), rownorm_f16.data_ptr(),
@@ -504,10 +512,10 @@ def qamw_channel_rms(X: torch.Tensor, out: Optional[torch.Tensor] = None,
     if X.dtype not in _WDT:
         raise ValueError("X must be float32 or bfloat16")
     if out is None:
-        out = torch.empty(d, dtype=torch.float32, device=X.device)
+        out = _empty(d, torch.float32, X.device, stream)
     _vec(out, "out", d)
     if workspace is None:
-        workspace = _workspace(qamw_channel_rms_workspace_bytes(T, d), X.device)
+        workspace = _workspace(qamw_channel_rms_workspace_bytes(T, d), X.device, stream)
     _lib.check("qamw_channel_rms", _lib.load().qamw_channel_rms(
         X.data_ptr(), _WDT[X.dtype], T, d, ldx, out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream)))
@@ -526,10 +534,10 @@ def qamw_output_error(X: torch.Tensor, W: torch.Tensor, W_hat: torch.Tensor, out
         if t.dtype not in _WDT:
             raise ValueError(f"{name} must be float32 or bfloat16")
     if out is None:
-        out = torch.empty(1, dtype=torch.float64, device=X.device)
+        out = _empty(1, torch.float64, X.device, stream)
     _vec(out, "out", 1, torch.float64)
     if workspace is None:
-        workspace = _workspace(qamw_output_error_workspace_bytes(T, N, d), X.device)
+        workspace = _workspace(qamw_output_error_workspace_bytes(T, N, d), X.device, stream)
     _lib.check("qamw_output_error", _lib.load().qamw_output_error(
         X.data_ptr(), _WDT[X.dtype], T, d, ldx, W.data_ptr(), _WDT[W.dtype], N, ldw, W_hat.data_ptr(),
         _WDT[W_hat.dtype], ldh, out.data_ptr(), workspace.data_ptr(),
@@ -552,7 +560,7 @@ def qamw_decode(packed: torch.Tensor, rownorm_f16: torch.Tensor, d: int, s: Opti
         _vec(s, "s", d)
     _vec(sigma, "sigma", d // 2)
     if out is None:
-        out = torch.empty((N, d), dtype=out_dtype, device=packed.device)
+        out = _empty((N, d), out_dtype, packed.device, stream)
     n2, d2, ldo = _rows(out, "out")
     if (n2, d2) != (N, d) or out.dtype not in _ODT:
         raise ValueError("out must be N x d of float32, bfloat16 or float16")
@@ -572,7 +580,7 @@ def qamw_rotate_activations(X: torch.Tensor, s: Optional[torch.Tensor], block: i
     if s is not None:
         _vec(s, "s", d)
     if out is None:
-        out = torch.empty((T, d), dtype=torch.bfloat16, device=X.device)
+        out = _empty((T, d), torch.bfloat16, X.device, stream)
     t2, d2, ldr = _rows(out, "out")
     if (t2, d2) != (T, d) or out.dtype != torch.bfloat16:
         raise ValueError("out must be a T x d bfloat16 tensor")
@@ -598,7 +606,7 @@ def qamw_decode_matmul(Xr: torch.Tensor, packed: torch.Tensor, rownorm_f16: torc
     _vec(rownorm_f16, "rownorm_f16", N, torch.int16)
     _vec(sigma, "sigma", d // 2)
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=Xr.device)
+        out = _empty((T, N), out_dtype, Xr.device, stream)
     t2, n2, ldy = _rows(out, "out")
     if (t2, n2) != (T, N) or out.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out must be T x N of float32 or bfloat16")

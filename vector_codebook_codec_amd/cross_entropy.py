@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _WDT, _dev, _matrix, _new, _raw_stream, _temporary, _vec
+from .codec import _WDT, _dev, _empty, _matrix, _raw_stream, _vec, _workspace
 
 __all__ = [
     "qamw_cross_entropy",
@@ -42,15 +42,15 @@ def qamw_cross_entropy(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, 
     token whose target is outside [0, V)."""
     T, V, d, ldh, ldw = _head(H, W, targets)
     if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=H.device)
+        loss = _empty(T, torch.float32, H.device, stream)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=H.device)
+        lse = _empty(T, torch.float32, H.device, stream)
     _vec(loss, "loss", T)
     _vec(lse, "lse", T)
     lib = _lib.load()
     dt = _WDT[H.dtype]
     if workspace is None:
-        workspace = _temporary(lib.qamw_cross_entropy_workspace_bytes(T, V, d, dt), H.device, stream)
+        workspace = _workspace(lib.qamw_cross_entropy_workspace_bytes(T, V, d, dt), H.device, stream)
     else:
         _dev(workspace, "workspace")
     _lib.check("qamw_cross_entropy", lib.qamw_cross_entropy(
@@ -69,9 +69,9 @@ def qamw_cross_entropy_grad(H: torch.Tensor, W: torch.Tensor, targets: torch.Ten
     _vec(lse, "lse", T)
     _vec(dloss, "dloss", T)
     if dH is None and need_dH:
-        dH = _new(T, d, H.dtype, H)
+        dH = _empty((T, d), H.dtype, H.device, stream)
     if dW is None and need_dW:
-        dW = _new(V, d, H.dtype, H)
+        dW = _empty((V, d), H.dtype, H.device, stream)
     lddh = lddw = d
     if dH is not None:
         n2, d2, lddh = _matrix(dH, "dH")
@@ -84,7 +84,7 @@ def qamw_cross_entropy_grad(H: torch.Tensor, W: torch.Tensor, targets: torch.Ten
     lib = _lib.load()
     dt = _WDT[H.dtype]
     if workspace is None:
-        workspace = _temporary(lib.qamw_cross_entropy_grad_workspace_bytes(T, V, d, dt), H.device, stream)
+        workspace = _workspace(lib.qamw_cross_entropy_grad_workspace_bytes(T, V, d, dt), H.device, stream)
     _dev(workspace, "workspace")
     _lib.check("qamw_cross_entropy_grad", lib.qamw_cross_entropy_grad(
         H.data_ptr(), dt, T, d, ldh, W.data_ptr(), V, ldw, targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(),

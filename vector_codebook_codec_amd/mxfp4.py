@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _ODT, _WDT, _dev, _matrix, _new, _raw_stream, _temporary
+from .codec import _ODT, _WDT, _dev, _empty, _matrix, _raw_stream, _workspace
 
 __all__ = [
     "qamw_mxfp4_dequantize",
@@ -64,17 +64,17 @@ def qamw_mxfp4_quantize(W: torch.Tensor, values_dtype=None, codes: Optional[torc
         raise ValueError("W must be float32, bfloat16 or float16")
     rb, sb = _sizes(d)
     if codes is None and scales is None:
-        codes = _new(N, rb, torch.uint8, W)
-        scales = _new(N, sb, torch.uint8, W)
+        codes = _empty((N, rb), torch.uint8, W.device, stream)
+        scales = _empty((N, sb), torch.uint8, W.device, stream)
     else:
-        codes = _new(N, rb, torch.uint8, W) if codes is None else codes
-        scales = _new(N, sb, torch.uint8, W) if scales is None else scales
+        codes = _empty((N, rb), torch.uint8, W.device, stream) if codes is None else codes
+        scales = _empty((N, sb), torch.uint8, W.device, stream) if scales is None else scales
         if _quantised(codes, scales, d) != N:
             raise ValueError(f"codes and scales must have {N} rows")
     vptr, vdt, ldv = None, 0, d
     if values is not None or values_dtype is not None:
         if values is None:
-            values = _new(N, d, values_dtype, W)
+            values = _empty((N, d), values_dtype, W.device, stream)
         n2, d2, ldv = _matrix(values, "values")
         vdt = _ODT.get(values.dtype)
         if n2 != N or d2 != d or vdt is None or (values_dtype or values.dtype) != values.dtype:
@@ -92,7 +92,7 @@ def qamw_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, d: int, out
     """The [N][d] values of a quantised matrix in out_dtype (fp32, bf16 or fp16)."""
     N = _quantised(codes, scales, d)
     if out is None:
-        out = _new(N, d, out_dtype, codes)
+        out = _empty((N, d), out_dtype, codes.device, stream)
     n2, d2, ldo = _matrix(out, "out")
     odt = _ODT.get(out.dtype)
     if n2 != N or d2 != d or odt is None:
@@ -115,14 +115,14 @@ def qamw_mxfp4_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
         raise ValueError("X must be float32, bfloat16 or float16")
     N = _quantised(codes, scales, d)
     if out is None:
-        out = _new(T, N, out_dtype, X)
+        out = _empty((T, N), out_dtype, X.device, stream)
     t2, n2, ldy = _matrix(out, "out")
     ydt = _WDT.get(out.dtype)
     if t2 != T or n2 != N or ydt is None:
         raise ValueError("out must be T x N of float32 or bfloat16")
     lib = _lib.load()
     if workspace is None:
-        workspace = _temporary(lib.qamw_mxfp4_matmul_workspace_bytes(T, N, d), X.device, stream)
+        workspace = _workspace(lib.qamw_mxfp4_matmul_workspace_bytes(T, N, d), X.device, stream)
     else:
         _dev(workspace, "workspace")
     status = lib.qamw_mxfp4_matmul(X.data_ptr(), xdt, T, d, ldx, codes.data_ptr(), scales.data_ptr(), N, out.data_ptr(), ydt,
