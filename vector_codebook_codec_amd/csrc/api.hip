@@ -58,7 +58,7 @@ int check_weights(const void* W, int32_t wdt, int64_t d, int64_t ldw) {
   if (!W) return fail(QAMW_EINVAL, "W is NULL");
   if (wdt != QAMW_F32 && wdt != QAMW_BF16) return fail(QAMW_EUNSUPPORTED, "weight dtype %d not supported", wdt);
   if (ldw < d) return fail(QAMW_EINVAL, "ldw=%lld < d=%lld", (long long)ldw, (long long)d);
-  if (!aligned16(W) || (ldw * elem_size(wdt)) % 16)
+  if (!aligned16(W) || !rows_aligned16(ldw, wdt))
     return fail(QAMW_EINVAL, "W must be 16-byte aligned with 16-byte aligned rows");
   return QAMW_OK;
 }
@@ -500,7 +500,7 @@ static int check_rows16(const void* p, int32_t dt, int64_t d, int64_t ld, const 
   if (dt != QAMW_F32 && dt != QAMW_BF16 && !(allow_f16 && dt == QAMW_F16))
     return fail(QAMW_EUNSUPPORTED, "%s dtype %d not supported", name, dt);
   if (ld < d) return fail(QAMW_EINVAL, "%s: leading dimension %lld < d=%lld", name, (long long)ld, (long long)d);
-  if (!aligned16(p) || (ld * elem_size(dt)) % 16)
+  if (!aligned16(p) || !rows_aligned16(ld, dt))
     return fail(QAMW_EINVAL, "%s must be 16-byte aligned with 16-byte aligned rows", name);
   return QAMW_OK;
 }
@@ -557,7 +557,7 @@ int32_t qamw_decode(const uint32_t* packed, const uint16_t* rownorm_f16, int64_t
   if (out_dtype != QAMW_F32 && out_dtype != QAMW_BF16 && out_dtype != QAMW_F16)
     return fail(QAMW_EUNSUPPORTED, "output dtype %d not supported", out_dtype);
   if (ldo < d) return fail(QAMW_EINVAL, "ldo=%lld < d=%lld", (long long)ldo, (long long)d);
-  if (!aligned16(packed) || !aligned16(W_out) || (ldo * elem_size(out_dtype)) % 16 || !aligned16(sigma) ||
+  if (!aligned16(packed) || !aligned16(W_out) || !rows_aligned16(ldo, out_dtype) || !aligned16(sigma) ||
       (s && !aligned16(s)))
     return fail(QAMW_EINVAL, "packed, s, sigma and W_out must be 16-byte aligned with 16-byte aligned rows");
   const int B = qamw_index_bits(K);
@@ -575,7 +575,7 @@ int32_t qamw_rotate_activations(const void* X, int32_t xdtype, int64_t T, int64_
   if (xdtype != QAMW_F32 && xdtype != QAMW_BF16) return fail(QAMW_EUNSUPPORTED, "activation dtype %d not supported", xdtype);
   if (ldx < d || ldr < d) return fail(QAMW_EINVAL, "ldx and ldr must be >= d");
   if (!Xr_bf16) return fail(QAMW_EINVAL, "Xr_bf16 is NULL");
-  if (!aligned16(X) || (ldx * elem_size(xdtype)) % 16 || !aligned16(Xr_bf16) || (ldr * 2) % 16 || (s && !aligned16(s)))
+  if (!aligned16(X) || !rows_aligned16(ldx, xdtype) || !aligned16(Xr_bf16) || ldr % 8 || (s && !aligned16(s)))
     return fail(QAMW_EINVAL, "X, Xr_bf16 and s must be 16-byte aligned with 16-byte aligned rows");
   return launch_rotate_act(L, X, xdtype, (int)T, (int)d, ldx, s, sign_seed, Xr_bf16, ldr, (hipStream_t)stream);
 }
@@ -592,7 +592,7 @@ int32_t qamw_decode_matmul(const uint16_t* Xr_bf16, int64_t T, int64_t d, int64_
     return fail(QAMW_EINVAL, "Xr_bf16, packed, rownorm_f16, sigma and Y must be non-NULL");
   if (ydtype != QAMW_F32 && ydtype != QAMW_BF16) return fail(QAMW_EUNSUPPORTED, "output dtype %d not supported", ydtype);
   if (ldr < d || ldy < N) return fail(QAMW_EINVAL, "ldr must be >= d and ldy >= N");
-  if (!aligned16(Xr_bf16) || (ldr * 2) % 16 || !aligned16(packed) || !aligned16(sigma))
+  if (!aligned16(Xr_bf16) || ldr % 8 || !aligned16(packed) || !aligned16(sigma))
     return fail(QAMW_EINVAL, "Xr_bf16, packed and sigma must be 16-byte aligned, Xr rows too");
   const int B = qamw_index_bits(K);
   const int row_words = (int)qamw_packed_row_words(d, K);
@@ -669,8 +669,8 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
 // ---------------- vocabulary cross entropy ----------------
 // sizes that the kernels' 32-bit offsets inside a tile and their grids can hold
 static bool ce_sizes_fit(int64_t T, int64_t V, int64_t d, int32_t dtype) {
-  const int es = elem_size(dtype);
-  return T <= kMaxDim && V <= kMaxDim && d * es < kMaxRowBytes && T * es < kMaxRowBytes &&
+  const int64_t row = kMaxRowBytes / elem_size(dtype);      // compared before anything is multiplied: sizes may be of any value
+  return V <= kMaxDim && d < row && T < row &&
          ((T + 127) / 128) * ((V + 127) / 128) < kMaxRows;
 }
 static int check_ce(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
@@ -684,7 +684,8 @@ static int check_ce(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t 
   int rc;
   if (T && (rc = check_rows16(H, dtype, d, ldh, "H", false))) return rc;
   if ((rc = check_rows16(W, dtype, d, ldw, "W", false))) return rc;
-  if (ldh * elem_size(dtype) > kMaxRowBytes || ldw * elem_size(dtype) > kMaxRowBytes)
+  const int64_t row = kMaxRowBytes / elem_size(dtype);
+  if (ldh > row || ldw > row)
     return fail(QAMW_EUNSUPPORTED, "leading dimension too large");
   if (T && (!targets || ((uintptr_t)targets & 7u))) return fail(QAMW_EINVAL, "targets must be non-NULL and 8-byte aligned");
   return QAMW_OK;

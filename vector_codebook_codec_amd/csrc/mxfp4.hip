@@ -579,7 +579,7 @@ int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx,
   const Operand w = {(const char*)wcodes, (int64_t)nb * 16, N, wscales, mx4_scale_bytes(d)};
   const Operand x = {(const char*)xcodes, (int64_t)nb * 16, T, xscales, mx4_scale_bytes(d)};
   // the fused form reads X by 16-byte loads with 32-bit offsets
-  if (T <= kFusedTokens && es == 2 && d % 8 == 0 && aligned16(X) && ldx % 8 == 0 && ldx * es <= kMaxRowBytes)
+  if (T <= kFusedTokens && es == 2 && d % 8 == 0 && aligned16(X) && ldx % 8 == 0 && ldx <= kMaxRowBytes / es)
     return ydt == QAMW_F32 ? matmul_fused<MemF32>(xdt, w, x, X, d, ldx, nb, Y, ldy, st)
                            : matmul_fused<MemBf16>(xdt, w, x, X, d, ldx, nb, Y, ldy, st);
   const int rc = launch_mx4_quantize(X, xdt, T, d, ldx, xcodes, xscales, nullptr, QAMW_BF16, 0, st);

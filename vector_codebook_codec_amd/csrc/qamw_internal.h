@@ -27,6 +27,8 @@ int check_launch(const char* what);
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 __host__ __device__ inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int elem_size(int32_t dt) { return dt == QAMW_F32 ? 4 : (dt == QAMW_BF16 || dt == QAMW_F16) ? 2 : 0; }
+// rows of ld elements of a known type start 16 bytes apart (no product: ld may be of any value)
+inline bool rows_aligned16(int64_t ld, int32_t dt) { return ld % (16 / elem_size(dt)) == 0; }
 // Rows per calibration tile (one amplitude partial sum each).  Rows of 5 to
 // 16 windows of 1024 columns are calibrated by one workgroup per CU (one
 // wavefront per window), so more than kCalibTileTarget tiles would run in a
