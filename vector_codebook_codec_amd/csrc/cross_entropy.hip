@@ -5,7 +5,8 @@
 //     G_tv = dloss_t (exp(z_tv - lse_t) - [v = y_t]),   dH = G W,   dW = G^T H
 //
 // A token whose target lies outside [0, V) is not counted: its loss and its
-// gradient are 0, and its hidden state, NaN or not, reaches nothing else.
+// gradient are 0, whatever the head holds, and its hidden state, NaN or not,
+// reaches nothing else.
 //
 // Forward: a workgroup forms one tile of logits in registers (vocabulary
 // entries are the A operand, so a lane holds several logits of one token) and
@@ -47,6 +48,10 @@ template <> struct Elem<OpF32> {
   typedef float T;
   static __device__ __forceinline__ float put(float v) { return v; }
 };
+// whether token t counts (targets NULL: all do)
+__device__ __forceinline__ bool counts(const int64_t* targets, int64_t t, int64_t V) {
+  return !targets || (targets[t] >= 0 && targets[t] < V);
+}
 // four consecutive elements, 4-element aligned
 __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
@@ -331,7 +336,7 @@ __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__
       const int y = k / (64 / kUnit), x = k % (64 / kUnit) * kUnit;
       const int64_t r = r0 + y;
       u32x4 v = {0, 0, 0, 0};
-      if (r < R && c0 + x < C && (!targets || (targets[r] >= 0 && targets[r] < V)))
+      if (r < R && c0 + x < C && counts(targets, r, V))
         v = *reinterpret_cast<const u32x4*>(in + r * pitch + c0 + x);
       *reinterpret_cast<u32x4*>(place(y, x)) = v;
     }
@@ -362,12 +367,15 @@ __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__
 // ---------------------------------------------------------------------------
 // C[n][m] = unit sum_k A[m][k] B[n][k] (unit NULL: 1) over K steps split among
 // gridDim.y workgroups: split s writes (or adds to) C + s * split_stride.
+// Rows n whose target is not counted are written as 0 (targets NULL: all
+// count): their G is 0, but not its product with an infinite or NaN weight.
 // 4096 x 20480 x 4096 bf16: 470 us, 1.46 PFLOP/s.
 // ---------------------------------------------------------------------------
 template <class Tl, class Out>
 __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Operand B, int kchunks, int tiles_m,
                                                                   int tiles_n, int steps_per_split,
                                                                   const float* __restrict__ unit,
+                                                                  const int64_t* __restrict__ targets, int64_t V,
                                                                   Out* __restrict__ C, int64_t ldc,
                                                                   int64_t split_stride, bool add) {
   extern __shared__ __align__(1024) char tile_lds[];
@@ -383,7 +391,9 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
   if constexpr (sizeof(Out) == 2) {
     tile16_put<Tl>(tile_lds, acc, [&](f32x4 v) { return make_uint2(pack_bf16x2(v[0] * u, v[1] * u), pack_bf16x2(v[2] * u, v[3] * u)); });
     tile16_rows<Tl>(tile_lds, [&](int n, int m, u32x4 q) {            // A.rows is a multiple of 8
-      if (n0 + n < B.rows && m0 + m < A.rows) *reinterpret_cast<u32x4*>(out + (n0 + n) * ldc + m0 + m) = q;
+      if (n0 + n >= B.rows || m0 + m >= A.rows) return;
+      if (!counts(targets, n0 + n, V)) q = u32x4{0, 0, 0, 0};
+      *reinterpret_cast<u32x4*>(out + (n0 + n) * ldc + m0 + m) = q;
     });
     return;
   } else {
@@ -391,16 +401,18 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Ope
     const int64_t m = m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4);
     const int64_t n = n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15);
 #pragma unroll
-    for (int j = 0; j < Tl::TN; ++j)
-      if (n + 16 * j < B.rows)
+    for (int j = 0; j < Tl::TN; ++j) {
+      if (n + 16 * j >= B.rows) continue;
+      const bool on = counts(targets, n + 16 * j, V);
 #pragma unroll
-        for (int i = 0; i < Tl::TM; ++i)
-          if (m + 16 * i < A.rows) {
-            Out* p = out + (n + 16 * j) * ldc + m + 16 * i;
-            acc[i][j] *= u;
-            if (add) acc[i][j] += *reinterpret_cast<const f32x4*>(p);
-            store4(p, acc[i][j]);
-          }
+      for (int i = 0; i < Tl::TM; ++i)
+        if (m + 16 * i < A.rows) {
+          Out* p = out + (n + 16 * j) * ldc + m + 16 * i;
+          acc[i][j] = on ? acc[i][j] * u : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if (add) acc[i][j] += *reinterpret_cast<const f32x4*>(p);
+          store4(p, acc[i][j]);
+        }
+    }
   }
 }
 
@@ -531,10 +543,12 @@ __global__ __launch_bounds__(256) void ce_dw_thin_kernel(const float* __restrict
 }
 
 // dH = unit times many fp32 sums, 16 threads an element: thread k adds sums k,
-// k + 16, ..., then the 16 in order; rounded once.
+// k + 16, ..., then the 16 in order; rounded once.  0 for a token that is not
+// counted (its sums are not, where a weight is infinite or NaN).
 template <class E>
 __global__ __launch_bounds__(256) void ce_sum_blocks_kernel(const float* __restrict__ part, int blocks, int64_t stride,
                                                             int64_t T, int d, const float* __restrict__ unit,
+                                                            const int64_t* __restrict__ targets, int64_t V,
                                                             E* __restrict__ out, int64_t ldo) {
   __shared__ f32x4 red[16][16];
   const int i = threadIdx.x & 15, k = threadIdx.x >> 4;
@@ -548,19 +562,23 @@ __global__ __launch_bounds__(256) void ce_sum_blocks_kernel(const float* __restr
   if (k || e >= n) return;
 #pragma unroll
   for (int q = 1; q < 16; ++q) s += red[q][i];
+  if (!counts(targets, e / per, V)) s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   store4(out + e / per * ldo + e % per * 4, unit ? s * *unit : s);
 }
 
-// dH = unit times the fp32 sums of the splits, in order, rounded once
+// dH = unit times the fp32 sums of the splits, in order, rounded once; 0 for a
+// token that is not counted
 template <class E>
 __global__ __launch_bounds__(256) void ce_sum_splits_kernel(const float* __restrict__ part, int splits, int64_t stride,
                                                             int64_t T, int d, const float* __restrict__ unit,
+                                                            const int64_t* __restrict__ targets, int64_t V,
                                                             E* __restrict__ out, int64_t ldo) {
   const float u = unit ? *unit : 1.0f;
   const int64_t per = d / 4, n = T * per;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     f32x4 s = reinterpret_cast<const f32x4*>(part)[i];
     for (int k = 1; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(part + k * stride + 4 * i);
+    if (!counts(targets, i / per, V)) s = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     store4(out + i / per * ldo + i % per * 4, s * u);
   }
 }
@@ -716,20 +734,21 @@ static int softmax_grad_tiled(const Operand& W, const Operand& H, int kchunks, c
   return check_launch("ce_softmax_grad_kernel");
 }
 template <class Tl, class Out>
-static int product_tiled(const Operand& A, const Operand& B, int kchunks, int splits, const float* unit, Out* C, int64_t ldc,
-                         int64_t split_stride, bool add, hipStream_t st) {
+static int product_tiled(const Operand& A, const Operand& B, int kchunks, int splits, const float* unit,
+                         const int64_t* targets, int64_t V, Out* C, int64_t ldc, int64_t split_stride, bool add,
+                         hipStream_t st) {
   const int tm = (int)tiles_of(A.rows, Tl::BM), tn = (int)tiles_of(B.rows, Tl::BN);
   const int steps = (kchunks + kStepChunks - 1) / kStepChunks, per = (steps + splits - 1) / splits;
   auto kernel = ce_product_kernel<Tl, Out>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(tm * tn), (unsigned)splits), dim3(Tl::kThreads), Tl::kLdsBytes, st, A, B,
-                     kchunks, tm, tn, per, unit, C, ldc, split_stride, add);
+                     kchunks, tm, tn, per, unit, targets, V, C, ldc, split_stride, add);
   return check_launch("ce_product_kernel");
 }
 template <class Op, class Out>
-static int product(const Operand& A, const Operand& B, int kchunks, const ProductPlan& p, const float* unit, Out* C,
-                   int64_t ldc, int64_t split_stride, bool add, hipStream_t st) {
+static int product(const Operand& A, const Operand& B, int kchunks, const ProductPlan& p, const float* unit,
+                   const int64_t* targets, int64_t V, Out* C, int64_t ldc, int64_t split_stride, bool add, hipStream_t st) {
   return with_shape<Op>(p.shape, [&](auto tile) {
-    return product_tiled<decltype(tile), Out>(A, B, kchunks, p.splits, unit, C, ldc, split_stride, add, st);
+    return product_tiled<decltype(tile), Out>(A, B, kchunks, p.splits, unit, targets, V, C, ldc, split_stride, add, st);
   });
 }
 
@@ -814,7 +833,8 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
     if (dW) {
       const Operand a = {(const char*)Ht, p.tp * es, d, nullptr, 0}, b = {(const char*)Gt, p.tp * es, n, nullptr, 0};
       const ProductPlan whole = product_plan(product_type(es), d, n, steps_of(p.tp, es), 1);
-      if ((rc = product<Op, E>(a, b, (int)(p.tp / Op::kElems), whole, unit, (E*)dW + v0 * lddw, lddw, 0, false, st))) return rc;
+      if ((rc = product<Op, E>(a, b, (int)(p.tp / Op::kElems), whole, unit, nullptr, V, (E*)dW + v0 * lddw, lddw, 0, false, st)))
+        return rc;
     }
     if (dH) {
       const int64_t np = (n + 7) / 8 * 8;                           // whole chunks; G and Wt hold 0 past n
@@ -824,18 +844,18 @@ static int ce_grad_as(const void* H, int64_t T, int d, int64_t ldh, const void* 
       const Operand a = {(const char*)Wt, p.vp * es, d, nullptr, 0}, b = {(const char*)G, p.vp * es, T, nullptr, 0};
       const int kc = (int)(np / Op::kElems);
       if (n == V && p.dh.splits == 1)                               // one piece, one sum: the result itself
-        return product<Op, E>(a, b, kc, p.dh, unit, (E*)dH, lddh, 0, false, st);
-      if ((rc = product<Op, float>(a, b, kc, p.dh, nullptr, sum, d, split_stride, v0 > 0, st))) return rc;
+        return product<Op, E>(a, b, kc, p.dh, unit, targets, V, (E*)dH, lddh, 0, false, st);
+      if ((rc = product<Op, float>(a, b, kc, p.dh, nullptr, nullptr, V, sum, d, split_stride, v0 > 0, st))) return rc;
     }
   }
   if (!dH) return QAMW_OK;
   if (p.thin) {
     hipLaunchKernelGGL((ce_sum_blocks_kernel<E>), dim3((unsigned)tiles_of(T * (d / 4), 16)), dim3(256), 0, st, sum, p.blocks,
-                       split_stride, T, d, unit, (E*)dH, lddh);
+                       split_stride, T, d, unit, targets, V, (E*)dH, lddh);
     return check_launch("ce_sum_blocks_kernel");
   }
   hipLaunchKernelGGL((ce_sum_splits_kernel<E>), dim3(blocks_for(T * (d / 4), 256)), dim3(256), 0, st, sum, p.dh.splits,
-                     split_stride, T, d, unit, (E*)dH, lddh);
+                     split_stride, T, d, unit, targets, V, (E*)dH, lddh);
   return check_launch("ce_sum_splits_kernel");
 }
 int launch_cross_entropy_grad(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V,
