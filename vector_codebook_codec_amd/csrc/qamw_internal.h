@@ -173,14 +173,16 @@ int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx,
 // keeps four K steps of a 64 x 64 tile in LDS instead of two, for products
 // that wait for memory (64 x 32000 x 4096 in bf16: 63 us against 72 us); only
 // two of its workgroups fit a CU.  fp32 products do not use it: they wait for
-// the matrix instructions.
+// the matrix instructions.  Nor do they use 256 x 256 tiles, whose registers
+// leave no room for a second sum (OpF32::kChainSteps): in one chain these
+// took 7.47 us a step where four 128 x 128 tiles take 7.56.
 enum ProductType { kProductBf16, kProductF32, kProductMx4 };
 constexpr int kCus = 256, kShapes = 4;
 constexpr int kShapeTile[kShapes] = {64, 64, 128, 256};
 constexpr float kNever = 1e9f;
 constexpr float kShapeStepUs[3][kShapes][3] = {
     {{0.43f, 0.45f, kNever}, {0.51f, 0.51f, 0.19f}, {0.74f, 0.98f, 0.49f}, {1.60f, 3.15f, 1.58f}},
-    {{kNever, kNever, kNever}, {0.62f, 1.09f, 0.50f}, {2.02f, 3.79f, 1.89f}, {7.47f, 15.0f, 7.48f}},
+    {{kNever, kNever, kNever}, {0.62f, 1.09f, 0.50f}, {2.02f, 3.79f, 1.89f}, {kNever, kNever, kNever}},
     {{0.38f, 0.55f, kNever}, {0.45f, 0.64f, 0.24f}, {0.92f, 1.27f, 0.60f}, {1.98f, 3.84f, 1.91f}}};
 inline int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 inline double step_us(ProductType t, int shape, int64_t load) {
