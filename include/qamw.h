@@ -469,8 +469,11 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  * cores; statistics in fp32.  For bf16 inputs G, relative to the largest
  * counted |dloss|, is rounded to bf16 before it is multiplied (not for few
  * tokens); dH and dW are summed in fp32 and rounded once.  All sums have
- * a fixed order.  T = 0 is valid (dW is then written as 0).  Rows of H, W and
- * of a T-element row of dtype must be under 4 MiB (T <= 2^20 for fp32).
+ * a fixed order.  The gradient's p_tv = exp(z_tv - lse_t) carries the rounding
+ * of lse_t to fp32: all probabilities of a token are off by the same factor,
+ * by up to |lse_t| 2^-24 (6e-6 at 100), and so is p_ty - 1 in absolute terms.
+ * T = 0 is valid (dW is then written as 0).  Rows of H and W and a row of T
+ * elements of dtype must be under 4 MiB (T < 2^20 for fp32, 2^21 for bf16).
  *   workspace >= qamw_cross_entropy_workspace_bytes(T, V, d, dtype) or
  *             qamw_cross_entropy_grad_workspace_bytes(T, V, d, dtype) bytes,
  *             256-byte aligned
