@@ -33,12 +33,11 @@ def check(q, X, codes, scales, name):
     assert np.array_equal(np.isnan(got), np.isnan(exact))
     ok = ~np.isnan(exact)
     assert (np.abs(got - exact)[ok] <= X.shape[1] * 2.0 ** -23 * S[ok]).all()
-    # a product of one column at a time is exact: the value of the activation itself
     return got
 
 
 def unit_weights(q, d, at, size=1.0):
-    """Weights that pick one column each."""
+    """Weights that pick one column each: its product is the activation's value, exactly."""
     W = torch.zeros(len(at), d, device=DEV)
     for n, j in enumerate(at):
         W[n, j] = size
@@ -53,11 +52,8 @@ def test_every_element(q, T, dt):
     bits = np.arange(T * d, dtype=np.int64) * (29 if dt == "bf16" else 31) % 0x7c00
     bits = (bits | (np.arange(T * d) % 2) << 15).astype(np.uint16).reshape(T, d)
     X = torch.from_numpy(bits.view(np.int16)).view(DT[dt]).to(DEV)
-    if dt == "bf16":                                     # 2^60 weights keep subnormal values inside fp32
-        X = X * 1.0
     at = list(range(0, d, 7))
-    size = 1.0
-    codes, scales = unit_weights(q, d, at, size)
+    codes, scales = unit_weights(q, d, at)
     got = check(q, X, codes, scales, "every element")
     want = M.dequantize(*M.quantize(X.double().cpu().numpy()), d)[:, at]
     normal = (np.abs(want) >= 2.0 ** -126) | (want == 0)
