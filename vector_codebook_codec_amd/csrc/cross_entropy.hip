@@ -40,14 +40,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 template <class Op> struct Elem;
-template <> struct Elem<OpBf16> {
-  typedef uint16_t T;
-  static __device__ __forceinline__ uint16_t put(float v) { return (uint16_t)f32_to_bf16_bits(v); }
-};
-template <> struct Elem<OpF32> {
-  typedef float T;
-  static __device__ __forceinline__ float put(float v) { return v; }
-};
+template <> struct Elem<OpBf16> { typedef uint16_t T; };
+template <> struct Elem<OpF32> { typedef float T; };
 // whether token t counts (targets NULL: all do)
 __device__ __forceinline__ bool counts(const int64_t* targets, int64_t t, int64_t V) {
   return !targets || (targets[t] >= 0 && targets[t] < V);
@@ -140,27 +134,24 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_stats_kernel(Operand W, Opera
   }
 }
 
-// The same for up to 16 TF tokens, a tile of 16 RF vocabulary entries: bound
+// The same for up to 16 tokens, a tile of kThinRows vocabulary entries: bound
 // by reading the head once (T = 1, V = 32000, d = 4096 bf16: 48 us, 5.4 TB/s of
 // the 5.9 that a plain read reaches).
-template <class Op, int RF, int TF, int U>
+constexpr int kThinRows = 16;
+template <class Op, int U>
 __global__ __launch_bounds__(kThinThreads) void ce_stats_thin_kernel(Operand W, Operand H, int kchunks,
                                                                      const int64_t* __restrict__ targets,
                                                                      float2* __restrict__ part, float* __restrict__ zt) {
-  __shared__ __align__(16) char red[thin_lds_bytes<RF, TF>()];
-  const int64_t m0 = (int64_t)blockIdx.x * (16 * RF);
-  f32x4 acc[RF][TF] = {};
-  thin_run<Op, RF, TF, U>(acc, W, m0, H, kchunks);
+  __shared__ __align__(16) char red[thin_lds_bytes<1, 1>()];
+  const int64_t m0 = (int64_t)blockIdx.x * kThinRows;
+  f32x4 acc[1][1] = {};
+  thin_run<Op, U>(acc[0][0], W, m0, H, kchunks);
   thin_sum(acc, red);
   if (threadIdx.x >= kWave) return;
   const int lane = threadIdx.x;
-#pragma unroll
-  for (int j = 0; j < TF; ++j) {
-    const int64_t t = 16 * j + (lane & 15);
-    const int64_t v = m0 + 4 * (lane >> 4);
-    const float2 s = column_stats(acc, j, near32(W.rows - v), t < H.rows ? near32(targets[t] - v) : -1, zt + t);
-    if (lane < 16 && t < H.rows) part[blockIdx.x * H.rows + t] = s;
-  }
+  const int64_t t = lane & 15, v = m0 + 4 * (lane >> 4);
+  const float2 s = column_stats(acc, 0, near32(W.rows - v), t < H.rows ? near32(targets[t] - v) : -1, zt + t);
+  if (lane < 16 && t < H.rows) part[blockIdx.x * H.rows + t] = s;
 }
 
 // Joins the tiles' statistics: TB tokens a workgroup and 256 / TB threads a
@@ -599,7 +590,6 @@ static unsigned blocks_for(int64_t n, int per) { return (unsigned)std::min<int64
 // (V = 32000, d = 4096, bf16: T = 1 56.9 us, T = 4 60.0 us; with 64 entries 62.7
 // us at T = 1, in 64 x 64 tiles 58.2 us at T = 20).
 constexpr int64_t kThinTokens = 4;
-constexpr int kThinRows = 16;
 
 static ProductType product_type(int es) { return es == 4 ? kProductF32 : kProductBf16; }
 static int64_t steps_of(int64_t elements, int es) { return tiles_of(elements * es, kStepBytes); }
@@ -642,7 +632,7 @@ static int ce_thin(const Operand& W, const Operand& H, int kchunks, const int64_
   const int64_t T = H.rows;
   float2* part = (float2*)ws;
   float* zt = (float*)((char*)ws + round_up((size_t)tm * T * sizeof(float2), 256));
-  hipLaunchKernelGGL((ce_stats_thin_kernel<Op, kThinRows / 16, 1, 4>), dim3((unsigned)tm), dim3(kThinThreads), 0, st, W, H, kchunks,
+  hipLaunchKernelGGL((ce_stats_thin_kernel<Op, 4>), dim3((unsigned)tm), dim3(kThinThreads), 0, st, W, H, kchunks,
                      targets, part, zt);
   const int rc = check_launch("ce_stats_thin_kernel");
   return rc ? rc : ce_finish(part, zt, targets, T, W.rows, tm, loss, lse, st);

@@ -55,13 +55,10 @@ struct Operand {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
 }
-// lane l's 16 (4) bytes from offset voff + soff to lds + 16 l (4 l)
+// lane l's 16 bytes from offset voff + soff to lds + 16 l
 typedef __attribute__((address_space(3))) void* LdsPtr;
 __device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voff, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)voff, (int)soff, 0, 0);
-}
-__device__ __forceinline__ void copy4_to_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 4, (int)voff, (int)soff, 0, 0);
 }
 
 // ---- element types: products of one fragment pair over one chunk per lane
@@ -404,41 +401,35 @@ __device__ __forceinline__ void thin_sum(f32x4 (&acc)[RF][TF], char* lds) {
   }
 }
 
-// acc of this wavefront's share of K, unscaled operands: 4 chunks of every row
-// a unit, chunk 4 u + l / 16 in lane l; U units a batch, the next batch in
-// flight while one is multiplied.
-template <class Op, int RF, int TF, int U>
-__device__ __forceinline__ void thin_run(f32x4 (&acc)[RF][TF], const Operand& A, int64_t m0, const Operand& B, int kchunks) {
+// acc of this wavefront's share of K, unscaled operands, 16 rows of each: 4
+// chunks of every row a unit, chunk 4 u + l / 16 in lane l; U units a batch,
+// the next batch in flight while one is multiplied.
+template <class Op, int U>
+__device__ __forceinline__ void thin_run(f32x4& acc, const Operand& A, int64_t m0, const Operand& B, int kchunks) {
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t row_bytes = (uint32_t)kchunks * 16u;
-  const int64_t ra = A.rows - m0 < 16 * RF ? A.rows - m0 : 16 * RF;
+  const int64_t ra = A.rows - m0 < 16 ? A.rows - m0 : 16;
   const __amdgpu_buffer_rsrc_t bufa = buffer_of(A.p + m0 * A.pitch, (uint32_t)((ra - 1) * A.pitch) + row_bytes);
   const __amdgpu_buffer_rsrc_t bufb = buffer_of(B.p, (uint32_t)((B.rows - 1) * B.pitch) + row_bytes);
   const uint32_t va = (uint32_t)l16 * (uint32_t)A.pitch + 16u * g, vb = (uint32_t)l16 * (uint32_t)B.pitch + 16u * g;
   const int units = (kchunks + 3) / 4, per = (units + kThinWaves - 1) / kThinWaves;
   const int u0 = min(wave * per, units), u1 = min(u0 + per, units);
-  i32x4 a[2][U][RF], b[2][U][TF];
+  i32x4 a[2][U], b[2][U];
   auto load = [&](int u, auto set) __attribute__((always_inline)) {
     constexpr int S = decltype(set)::value;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const bool in = u + k < u1 && 4 * (u + k) + g < kchunks;
       const uint32_t soff = u + k < u1 ? (uint32_t)(u + k) * 64u : 0u;      // below every buffer's size
-#pragma unroll
-      for (int i = 0; i < RF; ++i) a[S][k][i] = load16(bufa, in ? va + (uint32_t)(16 * i) * (uint32_t)A.pitch : kPastEnd, soff);
-#pragma unroll
-      for (int j = 0; j < TF; ++j) b[S][k][j] = load16(bufb, in ? vb + (uint32_t)(16 * j) * (uint32_t)B.pitch : kPastEnd, soff);
+      a[S][k] = load16(bufa, in ? va : kPastEnd, soff);
+      b[S][k] = load16(bufb, in ? vb : kPastEnd, soff);
     }
   };
   auto multiply = [&](auto set) __attribute__((always_inline)) {
     constexpr int S = decltype(set)::value;
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-#pragma unroll
-      for (int i = 0; i < RF; ++i)
-#pragma unroll
-        for (int j = 0; j < TF; ++j) acc[i][j] = Op::mma(a[S][k][i], b[S][k][j], acc[i][j], 0, 0, 0);
+    for (int k = 0; k < U; ++k) acc = Op::mma(a[S][k], b[S][k], acc, 0, 0, 0);
   };
   typedef std::integral_constant<int, 0> S0;
   typedef std::integral_constant<int, 1> S1;
