@@ -467,8 +467,9 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  *   lse      (gradient) as qamw_cross_entropy wrote it for these inputs
  * Arithmetic: products of the inputs as they are, summed in fp32 on matrix
  * cores; statistics in fp32.  For bf16 inputs G, relative to the largest
- * counted |dloss|, is rounded to bf16 before it is multiplied (not for few
- * tokens); dH and dW are summed in fp32 and rounded once.  All sums have
+ * counted |dloss|, is rounded to bf16 (2^-9 of each entry) before it is
+ * multiplied, except for up to 4 tokens, or up to 16 and a head of at least 8
+ * MiB; dH and dW are summed in fp32 and rounded once.  All sums have
  * a fixed order.  The gradient's p_tv = exp(z_tv - lse_t) carries the rounding
  * of lse_t to fp32: all probabilities of a token are off by the same factor,
  * by up to |lse_t| 2^-24 (6e-6 at 100), and so is p_ty - 1 in absolute terms.

@@ -56,8 +56,9 @@ __device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f3
 // Tile statistics of the logits: part[tile][t] = (max, sum of exp(z - max)),
 // and the target's logit from the one tile that holds it.  Bound by the
 // matrix instructions, and by the power they draw: T = 2048, V = 32000, d = 4096
-// bf16 takes 425 us, 1.26 PFLOP/s, at 1.8 to 1.9 GHz; a library product of
-// that size runs at 1.20 PFLOP/s.
+// bf16 takes 420 us in a row of calls, 1.28 PFLOP/s, at 1.9 to 2.0 GHz with
+// the matrix instructions busy 60 to 65 % of the time (470 us at the median
+// of a traced run); a library product of that size runs at 1.20 PFLOP/s.
 // ---------------------------------------------------------------------------
 // Of one 16-token column of fragments: lane group l / 16 holds the entries
 // 16 i + r past the lane's first one, `left` of them (or more) inside the
@@ -221,8 +222,9 @@ __global__ __launch_bounds__(1024) void ce_upstream_kernel(const float* __restri
 
 // ---------------------------------------------------------------------------
 // G / unit of one piece, in the logits' tiles (T = 4096, 20480 entries, d =
-// 4096 bf16: 535 us, 1.28 PFLOP/s, 60 us of it writing G twice): vocabulary entries v_first + [0, W.rows).  G [T][vp] and
-// Gt [W.rows][tp]; the columns past W.rows (to vp) and past T (to tp) are 0.
+// 4096 bf16: 580 us, 1.18 PFLOP/s, 60 us of it writing G twice): vocabulary
+// entries v_first + [0, W.rows).  G [T][vp] and Gt [W.rows][tp]; the columns
+// past W.rows (to vp) and past T (to tp) are 0.
 // ---------------------------------------------------------------------------
 template <class Tl, class Op, class E>
 __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
@@ -307,7 +309,7 @@ __global__ __launch_bounds__(Tl::kThreads) void ce_softmax_grad_kernel(
 // ---------------------------------------------------------------------------
 // out[c][r] = in[r][c] for r < R and 0 for R <= r < rp; rows whose target is
 // not counted read as 0 (targets NULL: all rows count).  64 x 64 tiles
-// through LDS, 16 bytes a lane on both sides: 20480 x 4096 bf16 60 us, 5.6 TB/s.
+// through LDS, 16 bytes a lane on both sides: 20480 x 4096 bf16 62 us, 5.4 TB/s.
 // ---------------------------------------------------------------------------
 template <class E>
 __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__ in, int64_t pitch, int64_t R, int64_t C,
@@ -360,7 +362,7 @@ __global__ __launch_bounds__(256) void ce_transpose_kernel(const E* __restrict__
 // gridDim.y workgroups: split s writes (or adds to) C + s * split_stride.
 // Rows n whose target is not counted are written as 0 (targets NULL: all
 // count): their G is 0, but not its product with an infinite or NaN weight.
-// 4096 x 20480 x 4096 bf16: 470 us, 1.46 PFLOP/s.
+// 4096 x 20480 x 4096 bf16: 511 us (dW) and 516 us (dH), 1.34 PFLOP/s.
 // ---------------------------------------------------------------------------
 template <class Tl, class Out>
 __global__ __launch_bounds__(Tl::kThreads) void ce_product_kernel(Operand A, Operand B, int kchunks, int tiles_m,
@@ -661,9 +663,12 @@ constexpr int64_t kCeBudget = (int64_t)512 << 20;
 
 // Whether the products run without transposed copies and matrix instructions
 // (and with G in fp32): for up to 4 tokens, and up to 16 with a head of some
-// size, whose copies would cost more than all else (V = 32000, d = 4096, bf16: T = 1 224 us against 356 us, T = 16 295
-// us, T = 17 361 us; V = 5003, d = 512: fp32, 10 MB, T = 16 57 us, T = 17 66
-// us, but bf16, 5 MB, 50 us and 42 us).
+// size, whose copies would cost more than all else (loss and gradient at V =
+// 32000, d = 4096, bf16: T = 1 214 us against 356 us, T = 16 302 us, T = 17 361
+// us; V = 5003, d = 512: fp32, 10 MB, T = 16 57 us, T = 17 66 us, but bf16, 5
+// MB, 50 us and 42 us).  The limit is one of time: beyond it bf16's G is
+// rounded however few the tokens are, and dH and dW are off by up to 0.0025 of
+// their norm where their own rounding alone gives 0.0017.
 static bool thin_gradient(int64_t T, int64_t V, int d, int es) {
   return T <= kThinTokens || (T <= 16 && V * d * es >= (int64_t(8) << 20));
 }

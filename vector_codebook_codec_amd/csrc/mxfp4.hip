@@ -228,12 +228,16 @@ __global__ __launch_bounds__(kBlockThreads) void mx4_dequantize_kernel(const uin
 // Y[t][n] = sum_k X^[t][k] W^[n][k] on v_mfma_scale_f32_16x16x128: the
 // instruction multiplies 128 four-bit products per result and applies both
 // blocks' scales, so nothing is decoded.  Weights are the A operand: a lane
-// then holds 4 consecutive channels n of one token.  T = 8192, 11008 x 4096: 240
-// us, 3.1 PFLOP/s (255 us with the quantisation of X).  Long rows run at 4.2 to
-// 4.4 PFLOP/s, whatever the order of LDS reads and matrix instructions, at a
-// falling clock: power (the instructions alone, on registers, reach 6.8).  With
-// 16 K steps a tile's first loads and its stores add 4 steps' time, and of the
-// sixth round of tiles 0.4 is used.
+// then holds 4 consecutive channels n of one token.  T = 8192, 11008 x 4096: 231
+// us, 3.2 PFLOP/s, in a row of calls (251 us with the quantisation of X).  The
+// clock stays near its highest (2.27 of 2.4 GHz), so power does not bound it:
+// a K step of a 256 x 256 tile takes about 4300 cycles, in which the matrix
+// instructions are busy for 2050.  Over the whole launch they are busy 32 % of
+// the time and LDS reads 21 %: neither is full, and wavefronts wait for 28 % of
+// their cycles and to issue for 43 %.  With 16 K steps a tile's first loads and its stores add 4 steps' time, and of the
+// sixth round of tiles 0.4 is used.  Rows of 13824: 3.9 PFLOP/s, 46 % busy at
+// 2.04 GHz (the instructions alone, on registers, reach 6.8).  This tile has
+// all 256 registers and one too few: the compiler spills one, 8 bytes a lane.
 // ---------------------------------------------------------------------------
 template <class Out>
 __device__ __forceinline__ void store_y(typename Out::T* Y, int64_t ldy, int64_t t, int64_t n, int64_t N, f32x4 v) {
@@ -344,8 +348,12 @@ __global__ __launch_bounds__(256) void mx4_sum_tail_kernel(const float* __restri
 // unit for instruction s, and the 16 scale codes of the unit.  With kFused
 // the activations are quantised here, a block a lane, in registers: one
 // launch less, and each workgroup reads X itself (16-byte aligned rows).
-// T = 1, 11008 x 4096: 9.7 us for 24 MB; the loads in flight, all issued at
-// once, take about half of it, starting, summing and ending the rest.
+// T = 1, 11008 x 4096: 9.6 us for 24 MB; the loads in flight, all issued at
+// once, take about half of it, starting, summing and ending the rest.  The
+// fused form's registers allow two workgroups a CU, 512 places for 688
+// workgroups: a second round for the last 176.  T = 13, 4096 x 11008: 8.3 us
+// for one workgroup a CU, whose wavefronts take two or three units one after
+// another, loads and products of a unit in turn.
 // ---------------------------------------------------------------------------
 template <int RF, int TF, class In, class Out, bool kFused>
 __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Operand Xq, const typename In::T* __restrict__ X,

@@ -218,8 +218,8 @@ struct Tile {
     };
     // One LDS read between every few matrix instructions (bf16 at 8192 x 8192 x
     // 4096: 392 us against 406 us as the compiler orders them).  The scaled
-    // instructions run faster as the compiler orders them (11008 x 8192 x 4096:
-    // 228 us against 235 us).
+    // instructions run faster as the compiler orders them (T = 11008, 8192 x
+    // 4096: 228 us against 235 us).
     auto interleave = [&]() __attribute__((always_inline)) {
       if constexpr (Op::kScaled) return;
       constexpr int kMma = TM * TN * Op::kMmas, kReads = TM + TN;
@@ -278,7 +278,8 @@ struct Tile {
 
 // The tile shapes (qamw_internal.h says when each is taken).  The larger a
 // tile, the fewer operand bytes go through LDS per product: at 8192 x 8192 x
-// 4096 in bf16, 392 us (1.40 PFLOP/s) and 498 us with 256 and 128.  One
+// 4096 in bf16, 392 us (1.40 PFLOP/s) and 498 us with 256 and 128 (fp32 uses
+// the two smaller ones).  One
 // workgroup of 256 x 256, two of 128 x 128 share a CU, of 64 x 64 five with two
 // K steps in LDS and two with four.
 template <class Op, int kShape> struct ShapeTile;
