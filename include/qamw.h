@@ -434,6 +434,7 @@ int32_t qamw_decode_matmul(const uint16_t* Xr_bf16, int64_t T, int64_t d, int64_
  *   NaN block gives NaN.  To multiply with rotated operands, rotate X with
  *   qamw_rotate_activations and the weight's rows with the same call before
  *   quantising them.
+ *   T N up to about 2^39 results (2^27 rows of W for few tokens).
  *   workspace >= qamw_mxfp4_matmul_workspace_bytes(T, N, d), 256-byte aligned
  */
 int64_t qamw_mxfp4_row_bytes(int64_t d);     /* -1 for d outside [1, 2^20] */
@@ -475,6 +476,8 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  * by up to |lse_t| 2^-24 (6e-6 at 100), and so is p_ty - 1 in absolute terms.
  * T = 0 is valid (dW is then written as 0).  Rows of H and W and a row of T
  * elements of dtype must be under 4 MiB (T < 2^20 for fp32, 2^21 for bf16).
+ * A launch holds fewer than 2^32 threads: V < 2^27 for up to 4 tokens and T V
+ * up to about 2^37 (fp32) or 2^39 (bf16) logits beyond that.
  *   workspace >= qamw_cross_entropy_workspace_bytes(T, V, d, dtype) or
  *             qamw_cross_entropy_grad_workspace_bytes(T, V, d, dtype) bytes,
  *             256-byte aligned

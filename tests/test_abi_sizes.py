@@ -70,3 +70,27 @@ def test_mxfp4_huge_sizes(lib, n):
     assert lib.qamw_mxfp4_matmul(A, BF16, n, 64, 64, A, A, 8, A, F32, 8, WS, 1 << 40, None) == EUNSUPPORTED
     assert lib.qamw_mxfp4_matmul(A, BF16, 4, 64, 64, A, A, n, A, F32, n, WS, 1 << 40, None) == EUNSUPPORTED
     assert lib.qamw_mxfp4_matmul_workspace_bytes(n, 8, 64) == 0 and lib.qamw_mxfp4_matmul_workspace_bytes(8, n, 64) == 0
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_cross_entropy_more_workgroups_than_a_launch_holds(lib, dt):
+    """A launch has fewer than 2^32 threads: heads of 2^27 rows for a few tokens, 2^39 logits for many."""
+    size = lib.qamw_cross_entropy_workspace_bytes
+    for T in (1, 4):
+        assert size(T, 1 << 27, 8, dt) == 0 and size(T, (1 << 27) - 16, 8, dt) > 0
+        assert forward(lib, dt, T=T, V=1 << 27) == EUNSUPPORTED and gradient(lib, dt, T=T, V=1 << 27) == EUNSUPPORTED
+    T = (1 << 20) - 8                                    # 2^13 or 2^12 tiles of tokens
+    V = 1 << (18 if dt == F32 else 19)                   # in fp32 128 x 128 tiles, in bf16 256 x 256
+    assert size(T, V, 512, dt) == 0 and size(T, V // 16, 512, dt) > 0
+    assert forward(lib, dt, T=T, V=V) == EUNSUPPORTED
+
+
+def test_mxfp4_more_workgroups_than_a_launch_holds(lib):
+    def call(T, N):
+        return lib.qamw_mxfp4_matmul(A, BF16, T, 64, 64, A, A, N, A, F32, N, WS, 16, None)
+
+    EWORKSPACE = -4
+    assert call(1, 1 << 27) == EUNSUPPORTED and call(1, (1 << 27) - 16) == EWORKSPACE
+    assert call(16, 1 << 31) == EUNSUPPORTED
+    assert call(1 << 31, 64) == EUNSUPPORTED and call(1 << 29, 64) == EWORKSPACE       # 2^25 and 2^23 tiles of 64 x 64
+    assert call(1 << 20, 1 << 19) == EUNSUPPORTED and call(1 << 20, 1 << 18) == EWORKSPACE

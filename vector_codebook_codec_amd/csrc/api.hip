@@ -655,7 +655,7 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
   int rc = check_mx4(N, d, codes, scales);
   if (rc) return rc;
   if (T < 0) return fail(QAMW_EINVAL, "T must not be negative (T=%lld)", (long long)T);
-  if (T > kMaxRows || ((T + 15) / 16) * ((N + 15) / 16) >= kMaxRows) return fail(QAMW_EUNSUPPORTED, "product too large");
+  if (T > kMaxRows || (T && N && !mx4_grid_fits(T, N, d))) return fail(QAMW_EUNSUPPORTED, "product too large");
   if ((rc = check_plain_rows(X, xdtype, T, d, ldx, "X", true))) return rc;
   if ((rc = check_plain_rows(Y, ydtype, N ? T : 0, N, ldy, "Y", false))) return rc;
   if (T == 0 || N == 0) return QAMW_OK;
@@ -670,8 +670,7 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
 // sizes that the kernels' 32-bit offsets inside a tile and their grids can hold
 static bool ce_sizes_fit(int64_t T, int64_t V, int64_t d, int32_t dtype) {
   const int64_t row = kMaxRowBytes / elem_size(dtype);      // compared before anything is multiplied: sizes may be of any value
-  return V <= kMaxDim && d < row && T < row &&
-         ((T + 127) / 128) * ((V + 127) / 128) < kMaxRows;
+  return V <= kMaxDim && d < row && T < row && (T <= 0 || ce_grid_fits(T, V, (int)d, dtype));
 }
 static int check_ce(const void* H, int32_t dtype, int64_t T, int64_t d, int64_t ldh, const void* W, int64_t V, int64_t ldw,
                     const int64_t* targets) {

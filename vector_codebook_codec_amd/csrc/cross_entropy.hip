@@ -600,6 +600,11 @@ static int logits_shape(int64_t T, int64_t V, int d, int es) { return product_pl
 static int logits_tile(int64_t T, int64_t V, int d, int es) {
   return T <= kThinTokens ? kThinRows : kShapeTile[logits_shape(T, V, d, es)];
 }
+bool ce_grid_fits(int64_t T, int64_t V, int d, int32_t dt) {
+  if (T <= kThinTokens) return grid_holds(tiles_of(V, kThinRows), kThinThreads);
+  const int shape = logits_shape(T, V, d, elem_size(dt));
+  return grid_holds(shape_tiles(shape, V, T), shape_threads(shape));
+}
 size_t ce_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt) {
   return round_up((size_t)tiles_of(V, logits_tile(T, V, d, elem_size(dt))) * T * sizeof(float2), 256) +
          round_up((size_t)T * sizeof(float), 256);

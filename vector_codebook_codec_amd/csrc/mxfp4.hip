@@ -234,10 +234,11 @@ __global__ __launch_bounds__(kBlockThreads) void mx4_dequantize_kernel(const uin
 // a K step of a 256 x 256 tile takes about 4300 cycles, in which the matrix
 // instructions are busy for 2050.  Over the whole launch they are busy 32 % of
 // the time and LDS reads 21 %: neither is full, and wavefronts wait for 28 % of
-// their cycles and to issue for 43 %.  With 16 K steps a tile's first loads and its stores add 4 steps' time, and of the
-// sixth round of tiles 0.4 is used.  Rows of 13824: 3.9 PFLOP/s, 46 % busy at
-// 2.04 GHz (the instructions alone, on registers, reach 6.8).  This tile has
-// all 256 registers and one too few: the compiler spills one, 8 bytes a lane.
+// their cycles and to issue for 43 %.  With 16 K steps a tile's first loads and
+// its stores add 4 steps' time, and of the sixth round of tiles 0.4 is used.
+// Rows of 13824: 3.9 PFLOP/s, 46 % busy at 2.04 GHz (the instructions alone, on
+// registers, reach 6.8).  This tile has all 256 registers and one too few: the
+// compiler spills one, 8 bytes a lane.
 // ---------------------------------------------------------------------------
 template <class Out>
 __device__ __forceinline__ void store_y(typename Out::T* Y, int64_t ldy, int64_t t, int64_t n, int64_t N, f32x4 v) {
@@ -515,6 +516,14 @@ static Mx4Plan mx4_plan(int64_t T, int64_t N, int64_t d) {
     p.bytes += (size_t)(tail * p.tiles.splits * tile * tile) * sizeof(float);
   }
   return p;
+}
+bool mx4_grid_fits(int64_t T, int64_t N, int64_t d) {
+  // below these no shape comes near the limit: less than 2^22 tiles
+  if (T < (int64_t(1) << 26) && N < (int64_t(1) << 26) && T * N < (int64_t(1) << 31)) return true;
+  if (thin_pays(T, N)) return grid_holds(tiles_of(N, 16), kThinThreads);
+  const TailPlan p = mx4_plan(T, N, d).tiles;
+  const int64_t n = shape_tiles(p.shape, N, T);
+  return grid_holds(p.whole + (n - p.whole) * p.splits, shape_threads(p.shape));
 }
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) { return mx4_plan(T, N, d).bytes; }
 

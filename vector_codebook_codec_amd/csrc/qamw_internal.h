@@ -161,6 +161,7 @@ int launch_mx4_quantize(const void* W, int32_t wdt, int64_t N, int d, int64_t ld
                         void* values, int32_t vdt, int64_t ldv, hipStream_t st);
 int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N, int d, void* W, int32_t odt,
                           int64_t ldo, hipStream_t st);
+bool mx4_grid_fits(int64_t T, int64_t N, int64_t d);
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st);
@@ -192,6 +193,9 @@ inline double step_us(ProductType t, int shape, int64_t load) {
 inline int64_t shape_tiles(int shape, int64_t M, int64_t N) {
   return tiles_of(M, kShapeTile[shape]) * tiles_of(N, kShapeTile[shape]);
 }
+inline int shape_threads(int shape) { return kShapeTile[shape] == 64 ? 256 : 512; }
+// a launch is of fewer than 2^32 threads along x
+inline bool grid_holds(int64_t workgroups, int threads) { return workgroups < (int64_t(1) << 32) / threads; }
 // writing and reading fp32 partial results at 4 TB/s, and the launch that adds them
 inline double partials_us(double elements) { return 3.0 + elements * 8e-6 / 4.0; }
 
@@ -243,6 +247,7 @@ inline TailPlan tail_plan(ProductType t, int64_t M, int64_t N, int64_t steps) {
 constexpr int64_t kMaxRowBytes = int64_t(1) << 22;
 
 // ---- vocabulary cross entropy (cross_entropy.hip)
+bool ce_grid_fits(int64_t T, int64_t V, int d, int32_t dt);
 size_t ce_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt);
 size_t ce_grad_workspace_bytes(int64_t T, int64_t V, int d, int32_t dt);
 int launch_cross_entropy(const void* H, int32_t dt, int64_t T, int d, int64_t ldh, const void* W, int64_t V, int64_t ldw,

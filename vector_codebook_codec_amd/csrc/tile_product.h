@@ -111,6 +111,7 @@ struct Tile {
   static constexpr int kRows = BM + BN;
   static constexpr int kDataBytes = kRows * kStepBytes;
   static constexpr int kScaleBytes = Op::kScaled ? kRows * 16 : 0;         // codes of two K steps
+  static_assert(kThreads == (BM == 64 ? 256 : 512), "shape_threads says how many threads a shape has");
   static constexpr int S = S_;                                    // K steps in LDS, a power of two
   static constexpr int kLdsBytes = S * (kDataBytes + kScaleBytes);
   static constexpr int kCopiesA = BM / 8 / kWaves, kCopiesB = BN / 8 / kWaves;   // 8 rows per wavefront copy
