@@ -468,7 +468,7 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  *   lse      (gradient) as qamw_cross_entropy wrote it for these inputs
  * Arithmetic: products of the inputs as they are, summed in fp32 on matrix
  * cores; statistics in fp32.  For bf16 inputs G, relative to the largest
- * counted |dloss|, is rounded to bf16 (2^-9 of each entry) before it is
+ * counted |dloss|, is rounded to bf16 (up to 2^-8 of each entry) before it is
  * multiplied, except for up to 4 tokens, or up to 16 and a head of at least 8
  * MiB; dH and dW are summed in fp32 and rounded once.  All sums have
  * a fixed order.  The gradient's p_tv = exp(z_tv - lse_t) carries the rounding

@@ -10,9 +10,9 @@ leaves:
     1e-5, for Y, dH and dW relative to their norm, for loss and lse relative to
     1 + |lse|.
   * bf16 gradients: one rounding of the result and one of the logits' gradient,
-    each at most 2^-9 of its term and independent: sqrt(2) 2^-9 = 2.8e-3.
-    Bound: 4e-3.
-  * bf16 products: one rounding, at most 2^-9 = 1.95e-3.  Bound: 2e-3.
+    at most 2^-8 of each term, 1.7e-3 in the root mean square over mantissas,
+    independent of each other: 2.4e-3.  Bound: 4e-3.
+  * bf16 products: one rounding, 1.7e-3 over many results.  Bound: 2e-3.
 dW's rows that are no token's target hold the softmax part of the gradient
 alone, which is small beside the target's part elsewhere, and are held to the
 same bounds by themselves.

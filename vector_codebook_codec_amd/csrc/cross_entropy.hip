@@ -18,10 +18,12 @@
 // and once transposed; dW = G^T H is final for the piece, dH = G W is summed
 // over the pieces in fp32.  Every product contracts along the operands' rows,
 // which is why H and each piece of W are also laid out transposed.  G is
-// rounded to bf16 for bf16 inputs, like H and W themselves: its relative
-// error 2^-9 is below that of the rounded gradients it is summed into.  For a
-// few tokens and a large head both products run without matrix instructions
-// and transposed copies.
+// rounded to bf16 for bf16 inputs, like H and W themselves: an entry is off by
+// up to 2^-8, as much as the rounded gradients that it is summed into, which
+// are then off by 0.0019 of their norm (T = 4096, V = 131072) to 0.0025 (few
+// tokens) where their own rounding gives 0.0017.  For a few tokens and a large
+// head both products run without matrix instructions and transposed copies,
+// with G in fp32.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
