@@ -449,6 +449,72 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
                           size_t workspace_bytes, void* stream);
 
 /*
+ * Attention cache in the same format: the keys and values of a model whose
+ * weights are served in 4 bits, in pages that sequences share by a table.
+ *   codes   [2][pages][heads][page][qamw_mxfp4_cache_row_bytes(d)] uint8, keys
+ *           first: a row is one head of one token, quantised by the rule above
+ *   scales  [2][pages][heads][page][qamw_mxfp4_cache_scale_bytes(d)] uint8: a
+ *           code per block, padded with 0 to 2, 4 or 8
+ *   page    tokens of a page, a power of two in [16, 65536]; d in [1, 256];
+ *           codes and scales 16-byte aligned
+ * Rows of K, V, Q and out are [token][head][d] with strides in elements, unit
+ * stride along d and no alignment but their elements'; dtypes QAMW_F32,
+ * QAMW_BF16 or QAMW_F16.
+ *
+ * qamw_mxfp4_cache_write: K and V of T tokens into slots [T] int64; slot s is
+ *   place s % page of page s / page.  A slot outside [0, pages page) is not
+ *   written (a padded token's -1).  The slots of one call must differ: what a
+ *   slot that is given twice holds afterwards is unspecified, of its rows.
+ * qamw_mxfp4_cache_read: the values in slots [T] to K and V of dtype (either
+ *   may be NULL); a slot outside the cache reads as 0.
+ * qamw_mxfp4_cache_attention: attention of T queries over the cache.
+ *   Q        [T][q_heads][d]; query heads h q_heads / heads and the following
+ *            q_heads / heads - 1 use key head h
+ *   starts   [sequences + 1] int32: sequence b's queries are starts[b] to
+ *            starts[b + 1] - 1, at most max_queries of them (rows past those
+ *            are not computed), its latest tokens; NULL: one query each,
+ *            sequences = T, max_queries = 1
+ *   table    [sequences][table_pitch] int32: the page of tokens [j page, (j +
+ *            1) page) in column j < table_cols.  Tokens of a page outside [0,
+ *            pages) are masked.
+ *   lengths  [sequences] int32: cached tokens, those of the queries among
+ *            them (at most table_cols page count; below 0 as 0)
+ *     z_t = scale <q, k_t> over tokens t < length, with causal t <= place =
+ *     length - queries + i for a sequence's query i, with window > 0 also t >
+ *     place - window;   out = sum_t softmax(z)_t v_t,   lse = log sum_t exp z_t
+ *   A row whose masks leave nothing gives 0 and -infinity.  What masked slots
+ *   hold does not matter (NaN blocks too).
+ *   out      [T][q_heads][d] of odtype, lse [T][q_heads] float32 or NULL.  Rows
+ *            of queries that belong to no sequence are left as they were.
+ *   scale    positive and finite
+ * Arithmetic: keys and values as they stand; bf16 queries as they stand, fp16
+ * and fp32 ones as 2 and 3 bf16 numbers (16 and 24 bits).  Products are summed
+ * in fp32, statistics are fp32.  Each weight is rounded once before it
+ * multiplies a value: by up to 2^-8 of itself where Q and out are bf16, 2^-16
+ * where one is fp16, 2^-24 where one is fp32.  out is rounded once.  Sums have
+ * a fixed order for given sizes.
+ *   T q_heads / heads and table_cols page up to 2^30
+ *   workspace >= qamw_mxfp4_cache_attention_workspace_bytes(..., table_cols
+ *             page, ...), 256-byte aligned; may be NULL where that is 0
+ */
+int64_t qamw_mxfp4_cache_row_bytes(int64_t d);     /* -1 for d outside [1, 256] */
+int64_t qamw_mxfp4_cache_scale_bytes(int64_t d);
+int32_t qamw_mxfp4_cache_write(const void* K, const void* V, int32_t dtype, int64_t T, int64_t heads, int64_t d,
+                               int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, const int64_t* slots,
+                               uint8_t* codes, uint8_t* scales, int64_t pages, int64_t page, void* stream);
+int32_t qamw_mxfp4_cache_read(const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page, int64_t heads, int64_t d,
+                              const int64_t* slots, int64_t T, void* K, void* V, int32_t dtype, int64_t k_token,
+                              int64_t k_head, int64_t v_token, int64_t v_head, void* stream);
+size_t qamw_mxfp4_cache_attention_workspace_bytes(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads,
+                                                  int64_t q_heads, int64_t d, int64_t tokens, int32_t qdtype, int32_t odtype);
+int32_t qamw_mxfp4_cache_attention(const void* Q, int32_t qdtype, int64_t T, int64_t q_heads, int64_t d, int64_t q_token,
+                                   int64_t q_head, const int32_t* starts, int64_t sequences, int64_t max_queries,
+                                   const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page, int64_t heads,
+                                   const int32_t* table, int64_t table_cols, int64_t table_pitch, const int32_t* lengths,
+                                   float scale, int32_t causal, int64_t window, void* out, int32_t odtype, int64_t o_token,
+                                   int64_t o_head, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Softmax cross entropy of a language model's last hidden states against its
  * vocabulary head, and the gradient (QAM-W, Experiments: the codec is judged
  * by what it does to the model's loss).  The T x V logits are never stored.

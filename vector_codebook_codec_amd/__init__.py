@@ -4,8 +4,18 @@ The codec's work runs in hand-written HIP kernels behind the C ABI of
 include/qamw.h (libqamw.so, built in-tree by ``_build.build()``).  This
 package binds that ABI for torch device tensors; see ``codec`` for the entry
 points ``qamw_calibrate``, ``qamw_encode`` and ``qamw_decode``, ``mxfp4`` for
-the microscaled 4-bit format, and ``cross_entropy`` for the model's loss.
+the microscaled 4-bit format, ``cache`` for an attention cache in it, and
+``cross_entropy`` for the model's loss.
 """
+from .cache import (  # noqa: F401
+    qamw_mxfp4_cache_attention,
+    qamw_mxfp4_cache_attention_workspace_bytes,
+    qamw_mxfp4_cache_new,
+    qamw_mxfp4_cache_read,
+    qamw_mxfp4_cache_row_bytes,
+    qamw_mxfp4_cache_scale_bytes,
+    qamw_mxfp4_cache_write,
+)
 from .codec import (  # noqa: F401
     load_codebook,
     load_polar,

@@ -57,6 +57,13 @@ SIGNATURES = {
     "qamw_mxfp4_dequantize": (_i32, [_p, _p, _i64, _i64, _p, _i32, _i64, _p]),
     "qamw_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "qamw_mxfp4_matmul": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _i64, _p, _i32, _i64, _p, _sz, _p]),
+    "qamw_mxfp4_cache_row_bytes": (_i64, [_i64]),
+    "qamw_mxfp4_cache_scale_bytes": (_i64, [_i64]),
+    "qamw_mxfp4_cache_write": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _i64, _i64, _p]),
+    "qamw_mxfp4_cache_read": (_i32, [_p, _p, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i32, _i64, _i64, _i64, _i64, _p]),
+    "qamw_mxfp4_cache_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i32, _i32]),
+    "qamw_mxfp4_cache_attention": (_i32, [_p, _i32, _i64, _i64, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _i64, _i64,
+                                          _p, _i64, _i64, _p, _f32, _i32, _i64, _p, _i32, _i64, _i64, _p, _p, _sz, _p]),
     "qamw_cross_entropy_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "qamw_cross_entropy": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _sz, _p]),
     "qamw_cross_entropy_grad_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),

@@ -7,6 +7,7 @@
 #include <stdarg.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cstdio>
 #include <mutex>
 #include <string>
@@ -664,6 +665,144 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
     return fail(QAMW_EWORKSPACE, "the 4-bit product needs %zu bytes of 256-byte aligned workspace (got %zu)", need,
                 workspace_bytes);
   return launch_mx4_matmul(X, xdtype, T, (int)d, ldx, codes, scales, N, Y, ydtype, ldy, workspace, (hipStream_t)stream);
+}
+
+// ---------------- attention cache in 4 bits ----------------
+constexpr int64_t kCacheMaxBytes = int64_t(1) << 45;
+constexpr int64_t kCacheMaxTokens = int64_t(1) << 30;      // of a sequence, and query rows of a call
+
+int64_t qamw_mxfp4_cache_row_bytes(int64_t d) { return d >= 1 && d <= kCacheMaxHeadDim ? mx4_blocks(d) * 16 : -1; }
+int64_t qamw_mxfp4_cache_scale_bytes(int64_t d) { return d >= 1 && d <= kCacheMaxHeadDim ? cache_scale_bytes(d) : -1; }
+
+static int check_cache(const void* codes, const void* scales, int64_t pages, int64_t heads, int64_t page, int64_t d,
+                       CacheShape* c) {
+  if (pages < 0 || heads <= 0 || d <= 0)
+    return fail(QAMW_EINVAL, "heads and d must be positive and pages not negative (pages=%lld heads=%lld d=%lld)",
+                (long long)pages, (long long)heads, (long long)d);
+  const int shift = log2_exact(page);
+  if (shift < 0 || page < kCacheMinPage || page > kCacheMaxPage)
+    return fail(QAMW_EUNSUPPORTED, "a page must hold a power of two in [16, 65536] of tokens (got %lld)", (long long)page);
+  if (d > kCacheMaxHeadDim) return fail(QAMW_EUNSUPPORTED, "head dimension %lld above 256", (long long)d);
+  if (heads > 65536 || pages > kCacheMaxBytes / (heads * page * mx4_blocks(d) * 16) || pages > INT32_MAX)
+    return fail(QAMW_EUNSUPPORTED, "cache too large");
+  if (pages && (!codes || !scales || !aligned16(codes) || !aligned16(scales)))
+    return fail(QAMW_EINVAL, "codes and scales must be non-NULL and 16-byte aligned");
+  *c = {pages, (int)heads, shift, (int)d, (int)mx4_blocks(d), cache_scale_bytes(d)};
+  return QAMW_OK;
+}
+// rows [T][heads][d] of any strides (unit stride along d), aligned to their elements; outputs may not overlap themselves
+static int check_head_rows(const void* p, int32_t dt, int64_t T, int64_t heads, int64_t d, int64_t token, int64_t head,
+                           const char* name, bool written) {
+  if (dt != QAMW_F32 && dt != QAMW_BF16 && dt != QAMW_F16) return fail(QAMW_EUNSUPPORTED, "%s dtype %d not supported", name, dt);
+  if (token < 0 || head < 0) return fail(QAMW_EINVAL, "%s: strides must not be negative", name);
+  if (!T) return QAMW_OK;
+  if (!p || (uintptr_t)p % (uintptr_t)elem_size(dt))
+    return fail(QAMW_EINVAL, "%s must be non-NULL and aligned to its elements", name);
+  if (token > kCacheMaxBytes || head > kCacheMaxBytes) return fail(QAMW_EUNSUPPORTED, "%s: strides too large", name);
+  if (written) {
+    // one stride steps over whole rows, the other over everything that the first spans
+    const int64_t tokens = T - 1, others = heads - 1;
+    const bool apart_h = heads == 1 || head >= d, apart_t = T == 1 || token >= d;
+    const bool heads_in = T == 1 || heads == 1 || others <= (token - d) / (head ? head : 1);
+    const bool tokens_in = T == 1 || heads == 1 || tokens <= (head - d) / (token ? token : 1);
+    if (!apart_h || !apart_t || !(heads_in || tokens_in)) return fail(QAMW_EINVAL, "%s: rows overlap", name);
+  }
+  return QAMW_OK;
+}
+static int check_slots(const int64_t* slots, int64_t T) {
+  if (T < 0) return fail(QAMW_EINVAL, "T must not be negative (T=%lld)", (long long)T);
+  if (T > kMaxRows) return fail(QAMW_EUNSUPPORTED, "too many tokens (T=%lld)", (long long)T);
+  if (T && (!slots || ((uintptr_t)slots & 7u))) return fail(QAMW_EINVAL, "slots must be non-NULL and 8-byte aligned");
+  return QAMW_OK;
+}
+
+int32_t qamw_mxfp4_cache_write(const void* K, const void* V, int32_t dtype, int64_t T, int64_t heads, int64_t d,
+                               int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, const int64_t* slots,
+                               uint8_t* codes, uint8_t* scales, int64_t pages, int64_t page, void* stream) {
+  CacheShape c;
+  int rc = check_cache(codes, scales, pages, heads, page, d, &c);
+  if (rc || (rc = check_slots(slots, T)) || (rc = check_head_rows(K, dtype, T, heads, d, k_token, k_head, "K", false)) ||
+      (rc = check_head_rows(V, dtype, T, heads, d, v_token, v_head, "V", false)))
+    return rc;
+  if (T == 0 || pages == 0) return QAMW_OK;
+  return launch_cache_write(K, V, dtype, T, k_token, k_head, v_token, v_head, c, slots, codes, scales, (hipStream_t)stream);
+}
+
+int32_t qamw_mxfp4_cache_read(const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page, int64_t heads, int64_t d,
+                              const int64_t* slots, int64_t T, void* K, void* V, int32_t dtype, int64_t k_token,
+                              int64_t k_head, int64_t v_token, int64_t v_head, void* stream) {
+  CacheShape c;
+  int rc = check_cache(codes, scales, pages, heads, page, d, &c);
+  if (rc || (rc = check_slots(slots, T)) ||
+      (rc = check_head_rows(K, dtype, K ? T : 0, heads, d, k_token, k_head, "K", true)) ||
+      (rc = check_head_rows(V, dtype, V ? T : 0, heads, d, v_token, v_head, "V", true)))
+    return rc;
+  if (T == 0 || (!K && !V)) return QAMW_OK;
+  return launch_cache_read(K, V, dtype, T, k_token, k_head, v_token, v_head, c, slots, codes, scales, (hipStream_t)stream);
+}
+
+// sizes that a call's launches and 32-bit row indices can hold
+static bool attention_sizes_fit(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads, int64_t q_heads, int64_t tokens) {
+  return T <= kCacheMaxTokens && heads <= 65536 && q_heads <= 65536 && sequences <= (int64_t(1) << 24) / heads &&
+         T * (q_heads / heads) <= kCacheMaxTokens && max_queries >= 1 && tokens <= kCacheMaxTokens;
+}
+static AttentionPlan plan_of(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads, int64_t q_heads, int64_t d,
+                             int64_t tokens, int32_t qdt, int32_t odt) {
+  return attention_plan(T, sequences, std::min(max_queries, T), heads, q_heads / heads, d, tokens, qdt, odt);
+}
+static bool attention_grid_fits(const AttentionPlan& p, int64_t T, int64_t q_heads) {
+  return grid_holds(p.groups, kBlockThreads) && (p.splits == 1 || grid_holds(T * q_heads / 4 + 1, kBlockThreads));
+}
+size_t qamw_mxfp4_cache_attention_workspace_bytes(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads,
+                                                  int64_t q_heads, int64_t d, int64_t tokens, int32_t qdtype, int32_t odtype) {
+  if (T <= 0 || sequences <= 0 || heads <= 0 || q_heads <= 0 || q_heads % heads || d <= 0 || d > kCacheMaxHeadDim || tokens < 0 ||
+      !elem_size(qdtype) || !elem_size(odtype) || !attention_sizes_fit(T, sequences, max_queries, heads, q_heads, tokens))
+    return 0;
+  return plan_of(T, sequences, max_queries, heads, q_heads, d, tokens, qdtype, odtype).bytes;
+}
+
+int32_t qamw_mxfp4_cache_attention(const void* Q, int32_t qdtype, int64_t T, int64_t q_heads, int64_t d, int64_t q_token,
+                                   int64_t q_head, const int32_t* starts, int64_t sequences, int64_t max_queries,
+                                   const uint8_t* codes, const uint8_t* scales, int64_t pages, int64_t page, int64_t heads,
+                                   const int32_t* table, int64_t table_cols, int64_t table_pitch, const int32_t* lengths,
+                                   float scale, int32_t causal, int64_t window, void* out, int32_t odtype, int64_t o_token,
+                                   int64_t o_head, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  AttentionArgs a;
+  int rc = check_cache(codes, scales, pages, heads, page, d, &a.c);
+  if (rc) return rc;
+  if (T < 0 || sequences < 0 || q_heads <= 0 || q_heads % heads)
+    return fail(QAMW_EINVAL, "sizes must not be negative and q_heads a multiple of heads (T=%lld sequences=%lld q_heads=%lld heads=%lld)",
+                (long long)T, (long long)sequences, (long long)q_heads, (long long)heads);
+  if (max_queries < 1 || (!starts && (max_queries != 1 || sequences != T)))
+    return fail(QAMW_EINVAL, "max_queries must be positive; without starts there is one query a sequence");
+  if (table_cols < 0 || table_pitch < table_cols) return fail(QAMW_EINVAL, "table_pitch must be >= table_cols >= 0");
+  if (table_cols > kCacheMaxTokens / page || table_pitch > kCacheMaxBytes ||
+      !attention_sizes_fit(T, sequences, max_queries, heads, q_heads, table_cols * page))
+    return fail(QAMW_EUNSUPPORTED, "attention too large");
+  if (!(scale > 0.0f) || isinf(scale)) return fail(QAMW_EINVAL, "scale must be positive and finite");
+  if (window < 0) return fail(QAMW_EINVAL, "window must not be negative (0: none)");
+  if ((rc = check_head_rows(Q, qdtype, T, q_heads, d, q_token, q_head, "Q", false)) ||
+      (rc = check_head_rows(out, odtype, T, q_heads, d, o_token, o_head, "out", true)))
+    return rc;
+  if (T == 0 || sequences == 0) return QAMW_OK;
+  if (!lengths || ((uintptr_t)lengths & 3u) || ((uintptr_t)starts & 3u) || (table_cols && !table) || ((uintptr_t)table & 3u))
+    return fail(QAMW_EINVAL, "starts, lengths and table must be 4-byte aligned, lengths and table non-NULL");
+  if ((uintptr_t)lse & 3u) return fail(QAMW_EINVAL, "lse must be 4-byte aligned");
+  const int64_t tokens = table_cols * page;
+  const AttentionPlan p = plan_of(T, sequences, max_queries, heads, q_heads, d, tokens, qdtype, odtype);
+  if (!attention_grid_fits(p, T, q_heads)) return fail(QAMW_EUNSUPPORTED, "attention too large");
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes || ((uintptr_t)workspace & 255u)))
+    return fail(QAMW_EWORKSPACE, "the attention needs %zu bytes of 256-byte aligned workspace (got %zu)", p.bytes, workspace_bytes);
+  a.codes = codes, a.scales = scales;
+  a.Q = Q, a.qdt = qdtype, a.q_token = q_token, a.q_head = q_head;
+  a.out = out, a.odt = odtype, a.o_token = o_token, a.o_head = o_head;
+  a.lse = lse;
+  a.starts = starts, a.lengths = lengths, a.table = table, a.table_pitch = table_pitch, a.cols = (int)table_cols;
+  a.T = T, a.max_queries = std::min(max_queries, T);
+  a.sequences = (int)sequences, a.group = (int)(q_heads / heads);
+  a.scale = scale, a.causal = causal != 0;
+  a.window = window >= kCacheMaxTokens ? 0 : (int)window;    // no narrower than any sequence
+  return launch_cache_attention(a, p, workspace, (hipStream_t)stream);
 }
 
 // ---------------- vocabulary cross entropy ----------------

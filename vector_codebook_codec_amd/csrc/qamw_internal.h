@@ -166,6 +166,48 @@ size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st);
 
+// ---- attention cache in microscaled 4 bits (cache.hip, cache_attention.hip)
+struct CacheShape {
+  int64_t pages;
+  int heads, page_shift;           // page = 1 << page_shift tokens
+  int d, nb, sb;                   // blocks of a head, bytes of a row of scales
+};
+constexpr int kCacheMaxHeadDim = 256;
+constexpr int64_t kCacheMinPage = 16, kCacheMaxPage = 65536;
+inline int cache_scale_bytes(int64_t d) { return mx4_blocks(d) <= 2 ? 2 : mx4_blocks(d) <= 4 ? 4 : 8; }
+int launch_cache_write(const void* K, const void* V, int32_t dt, int64_t T, int64_t kt, int64_t kh, int64_t vt, int64_t vh,
+                       const CacheShape& c, const int64_t* slots, uint8_t* codes, uint8_t* scales, hipStream_t st);
+int launch_cache_read(void* K, void* V, int32_t dt, int64_t T, int64_t kt, int64_t kh, int64_t vt, int64_t vh,
+                      const CacheShape& c, const int64_t* slots, const uint8_t* codes, const uint8_t* scales, hipStream_t st);
+
+// Queries, outputs and sequences of an attention call (cache_attention.hip).
+struct AttentionArgs {
+  CacheShape c;
+  const uint8_t *codes, *scales;
+  const void* Q;
+  void* out;
+  float* lse;                                     // [T][group heads], or NULL
+  int32_t qdt, odt;
+  int64_t q_token, q_head, o_token, o_head;       // strides in elements
+  const int32_t *starts, *lengths, *table;        // starts: NULL for one query a sequence
+  int64_t table_pitch;
+  int64_t T, max_queries;
+  int sequences, group, cols;
+  float scale;
+  int causal, window;                             // window 0: none
+};
+// How the work of a call is cut: a workgroup takes `rows` query rows (query
+// by head of a group) of one sequence and key head, and one of `splits` shares
+// of their tokens.
+struct AttentionPlan {
+  int rows, row_tiles, splits;
+  int64_t groups;                                 // workgroups
+  size_t bytes;                                   // partial results
+};
+AttentionPlan attention_plan(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads, int64_t group, int64_t d,
+                             int64_t tokens, int32_t qdt, int32_t odt);
+int launch_cache_attention(const AttentionArgs& a, const AttentionPlan& p, void* ws, hipStream_t st);
+
 // ---- how a product [M][N] is cut into square tiles (tile_product.h).
 // The measured time of one K step (128 bytes of every row), in microseconds,
 // where every CU has L tiles of a shape to work on, for L = 1, 2 and per tile
