@@ -74,3 +74,18 @@ def matmul(X, codes, scales):
     Xq = dequantize(*quantize(X), d)
     W = dequantize(codes, scales, d)
     return Xq @ W.T, np.abs(Xq) @ np.abs(W).T
+
+
+def adapter_matmul(X, codes, scales, A, B, index, factors):
+    """(Y, sum of |products| of the first term, of the second, sum of |U| |B|): the product plus the adapters of the
+    tokens' own, float64."""
+    X = np.asarray(X, dtype=np.float64)
+    Y, S = matmul(X, codes, scales)
+    extra, inner = np.zeros_like(Y), np.zeros_like(Y)
+    for t, i in enumerate(index):
+        if 0 <= i < len(A):
+            u = factors[i] * (A[i] @ X[t])
+            Y[t] += B[i] @ u
+            extra[t] = np.abs(B[i]) @ (abs(factors[i]) * (np.abs(A[i]) @ np.abs(X[t])))
+            inner[t] = np.abs(B[i]) @ np.abs(u)
+    return Y, S, extra, inner

@@ -52,6 +52,8 @@ from .cross_entropy import (  # noqa: F401
     qamw_cross_entropy_workspace_bytes,
 )
 from .mxfp4 import (  # noqa: F401
+    qamw_mxfp4_adapter_matmul,
+    qamw_mxfp4_adapter_matmul_workspace_bytes,
     qamw_mxfp4_dequantize,
     qamw_mxfp4_matmul,
     qamw_mxfp4_matmul_workspace_bytes,

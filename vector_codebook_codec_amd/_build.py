@@ -19,9 +19,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "calibrate.hip", "encode.hip", "plan.hip", "decode.hip", "matmul.hip",
                                                 "metrics.hip", "polar.hip", "learn.hip", "mxfp4.hip",
-                                                "cross_entropy.hip", "cache.hip", "cache_attention.hip")]
+                                                "cross_entropy.hip", "adapter.hip", "cache.hip", "cache_attention.hip")]
 HEADERS = [os.path.join(CSRC, "qamw_device.h"), os.path.join(CSRC, "qamw_internal.h"),
            os.path.join(CSRC, "tile_product.h"), os.path.join(CSRC, "mx4_device.h"),
+           os.path.join(CSRC, "mx4_adapter.h"),
            os.path.join(ROOT, "include", "qamw.h")]
 LIB_PATH = os.path.join(PKG, "libqamw.so")
 ARCH = "gfx950"

@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "qamw.h"
+#include "mx4_adapter.h"
 #include "mx4_device.h"
 #include "qamw_device.h"
 #include "qamw_internal.h"
@@ -144,12 +145,13 @@ __global__ __launch_bounds__(kBlockThreads) void mx4_dequantize_kernel(const uin
 // ---------------------------------------------------------------------------
 // Workgroups below `whole` take one tile each; those after it take a share of
 // K of a tile, `splits` to a tile, and leave fp32 results in
-// part[tile - whole][split][BN][BM] for mx4_sum_tail_kernel.
-template <class Tl, class Out>
+// part[tile - whole][split][BN][BM] for mx4_sum_tail_kernel.  Adapters are
+// added by the workgroup that holds a tile's first share.
+template <class Tl, class Out, class Ad>
 __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Operand X, int kchunks, int tiles_m,
                                                                   int tiles_n, int whole, int splits,
                                                                   typename Out::T* __restrict__ Y, int64_t ldy,
-                                                                  float* __restrict__ part) {
+                                                                  float* __restrict__ part, Adapters ad) {
   extern __shared__ __align__(1024) char tile_lds[];
   const int id = blockIdx.x, steps = (kchunks + kStepChunks - 1) / kStepChunks;
   const bool split = id >= whole;
@@ -166,6 +168,12 @@ __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Ope
   const int64_t m0 = (int64_t)tm * Tl::BM, n0 = (int64_t)tn * Tl::BN;
   f32x4 acc[Tl::TM][Tl::TN] = {};
   if (s0 < s1) Tl::run(acc, W, m0, X, n0, kchunks, s0, s1, tile_lds);
+  if constexpr (Ad::kOn) {
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (s0 == 0)
+      add_adapters<Ad>(acc, ad, m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + (lane & 15),
+                       n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15), X.rows, W.rows, 0, 1);
+  }
   if (!split) {
     store_tile<Tl, Out>(Y, ldy, n0, X.rows, m0, W.rows, acc, tile_lds);
     return;
@@ -209,10 +217,11 @@ __global__ __launch_bounds__(256) void mx4_sum_tail_kernel(const float* __restri
 // for one workgroup a CU, whose wavefronts take two or three units one after
 // another, loads and products of a unit in turn.
 // ---------------------------------------------------------------------------
-template <int RF, int TF, class In, class Out, bool kFused>
+template <int RF, int TF, class In, class Out, bool kFused, class Ad>
 __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Operand Xq, const typename In::T* __restrict__ X,
                                                                 int d, int ldx_bytes, int kchunks,
-                                                                typename Out::T* __restrict__ Y, int64_t ldy) {
+                                                                typename Out::T* __restrict__ Y, int64_t ldy,
+                                                                Adapters ad) {
   __shared__ __align__(16) char red[thin_lds_bytes<RF, TF>()];
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -281,6 +290,8 @@ __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Op
           acc[i][j] = OpMx4::mma(w[s][i], x[s][j], acc[i][j], 0, (int)((uint32_t)sc[i][s] >> (8 * g)),
                                  (int)((uint32_t)sx[j][s] >> (8 * g)));
   }
+  // the wavefronts take the tokens' adapters in turn, and their sums are added anyway
+  if constexpr (Ad::kOn) add_adapters<Ad>(acc, ad, m0 + l16, l16, Xq.rows, W.rows, wave, kThinWaves);
   thin_sum(acc, red);
   if (wave) return;
 #pragma unroll
@@ -380,14 +391,14 @@ bool mx4_grid_fits(int64_t T, int64_t N, int64_t d) {
 }
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) { return mx4_plan(T, N, d).bytes; }
 
-template <class Tl, class Out>
+template <class Tl, class Out, class Ad>
 static int matmul_tiled(const TailPlan& p, const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, float* part,
-                        hipStream_t st) {
+                        const Adapters& ad, hipStream_t st) {
   typedef typename Out::T E;
   const int tm = (int)tiles_of(W.rows, Tl::BM), tn = (int)tiles_of(X.rows, Tl::BN), whole = (int)p.whole, tail = tm * tn - whole;
-  auto kernel = mx4_matmul_kernel<Tl, Out>;
+  auto kernel = mx4_matmul_kernel<Tl, Out, Ad>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(whole + tail * p.splits)), dim3(Tl::kThreads), Tl::kLdsBytes, st, W, X, kchunks,
-                     tm, tn, whole, p.splits, (E*)Y, ldy, part);
+                     tm, tn, whole, p.splits, (E*)Y, ldy, part, ad);
   const int rc = check_launch("mx4_matmul_kernel");
   if (rc || !tail) return rc;
   auto sum = mx4_sum_tail_kernel<Tl, Out>;
@@ -395,10 +406,11 @@ static int matmul_tiled(const TailPlan& p, const Operand& W, const Operand& X, i
                      tn, X.rows, W.rows, (E*)Y, ldy);
   return check_launch("mx4_sum_tail_kernel");
 }
-template <class Out>
+template <class Out, class Ad>
 static int matmul_to(const TailPlan& p, const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, float* part,
-                     hipStream_t st) {
-  return with_shape<OpMx4>(p.shape, [&](auto tile) { return matmul_tiled<decltype(tile), Out>(p, W, X, kchunks, Y, ldy, part, st); });
+                     const Adapters& ad, hipStream_t st) {
+  return with_shape<OpMx4>(
+      p.shape, [&](auto tile) { return matmul_tiled<decltype(tile), Out, Ad>(p, W, X, kchunks, Y, ldy, part, ad, st); });
 }
 
 // A workgroup of the thin product takes 32 channels where that still gives
@@ -406,33 +418,27 @@ static int matmul_to(const TailPlan& p, const Operand& W, const Operand& X, int 
 // 32; T = 16: 11008 x 4096 13.6 us with 32).  The fused form takes 16: its
 // registers allow two workgroups a CU only then (T = 1, 11008 x 4096: 10.9 us
 // against 12.1 us).
-template <int RF, int TF, class In, class Out, bool kFused>
+template <int RF, int TF, class In, class Out, bool kFused, class Ad>
 static int thin_rows(const Operand& W, const Operand& Xq, const void* X, int d, int64_t ldx, int kchunks, void* Y, int64_t ldy,
-                     hipStream_t st) {
-  hipLaunchKernelGGL((mx4_thin_kernel<RF, TF, In, Out, kFused>), dim3((unsigned)tiles_of(W.rows, 16 * RF)), dim3(kThinThreads), 0,
-                     st, W, Xq, (const typename In::T*)X, d, (int)(ldx * sizeof(typename In::T)), kchunks,
-                     (typename Out::T*)Y, ldy);
+                     const Adapters& ad, hipStream_t st) {
+  hipLaunchKernelGGL((mx4_thin_kernel<RF, TF, In, Out, kFused, Ad>), dim3((unsigned)tiles_of(W.rows, 16 * RF)), dim3(kThinThreads),
+                     0, st, W, Xq, (const typename In::T*)X, d, (int)(ldx * sizeof(typename In::T)), kchunks,
+                     (typename Out::T*)Y, ldy, ad);
   return check_launch("mx4_thin_kernel");
 }
-template <int TF, class In, class Out, bool kFused>
+template <int TF, class In, class Out, bool kFused, class Ad>
 static int matmul_thin(const Operand& W, const Operand& Xq, const void* X, int d, int64_t ldx, int kchunks, void* Y, int64_t ldy,
-                       hipStream_t st) {
+                       const Adapters& ad, hipStream_t st) {
   if constexpr (!kFused && TF == 1)
-    if (tiles_of(W.rows, 32) >= kCus) return thin_rows<2, TF, In, Out, kFused>(W, Xq, X, d, ldx, kchunks, Y, ldy, st);
-  return thin_rows<1, TF, In, Out, kFused>(W, Xq, X, d, ldx, kchunks, Y, ldy, st);
+    if (tiles_of(W.rows, 32) >= kCus) return thin_rows<2, TF, In, Out, kFused, Ad>(W, Xq, X, d, ldx, kchunks, Y, ldy, ad, st);
+  return thin_rows<1, TF, In, Out, kFused, Ad>(W, Xq, X, d, ldx, kchunks, Y, ldy, ad, st);
 }
-template <class Out>
-static int matmul_fused(int32_t xdt, const Operand& W, const Operand& Xq, const void* X, int d, int64_t ldx, int kchunks,
-                        void* Y, int64_t ldy, hipStream_t st) {
-  if (xdt == QAMW_F16) return matmul_thin<1, MemF16, Out, true>(W, Xq, X, d, ldx, kchunks, Y, ldy, st);
-  return matmul_thin<1, MemBf16, Out, true>(W, Xq, X, d, ldx, kchunks, Y, ldy, st);
-}
-template <class Out>
+template <class Out, class Ad>
 static int matmul_quantised(const Mx4Plan& p, const Operand& W, const Operand& X, int d, int kchunks, void* Y, int64_t ldy,
-                            float* part, hipStream_t st) {
-  if (X.rows <= 16) return matmul_thin<1, MemBf16, Out, false>(W, X, nullptr, d, 0, kchunks, Y, ldy, st);
-  if (thin_pays(X.rows, W.rows)) return matmul_thin<2, MemBf16, Out, false>(W, X, nullptr, d, 0, kchunks, Y, ldy, st);
-  return matmul_to<Out>(p.tiles, W, X, kchunks, Y, ldy, part, st);
+                            float* part, const Adapters& ad, hipStream_t st) {
+  if (X.rows <= 16) return matmul_thin<1, MemBf16, Out, false, Ad>(W, X, nullptr, d, 0, kchunks, Y, ldy, ad, st);
+  if (thin_pays(X.rows, W.rows)) return matmul_thin<2, MemBf16, Out, false, Ad>(W, X, nullptr, d, 0, kchunks, Y, ldy, ad, st);
+  return matmul_to<Out, Ad>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
 }
 
 // Up to this many tokens of 16 bits the thin product quantises X itself: each
@@ -440,22 +446,33 @@ static int matmul_quantised(const Mx4Plan& p, const Operand& W, const Operand& X
 // T = 1: 5.4 us against 7.0 us with a launch of its own for X).
 constexpr int64_t kFusedTokens = 4;
 
-int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
-                      const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st) {
+template <class Out>
+static int matmul_out(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes, const uint8_t* wscales,
+                      int64_t N, void* Y, int64_t ldy, void* ws, const Adapters* adapters, hipStream_t st) {
   const int nb = (int)mx4_blocks(d), es = elem_size(xdt);
   const Mx4Plan p = mx4_plan(T, N, d);
   uint8_t *xcodes = (uint8_t*)ws, *xscales = xcodes + p.scales;
   float* part = (float*)(xcodes + p.part);
   const Operand w = {(const char*)wcodes, (int64_t)nb * 16, N, wscales, mx4_scale_bytes(d)};
   const Operand x = {(const char*)xcodes, (int64_t)nb * 16, T, xscales, mx4_scale_bytes(d)};
+  const Adapters ad = adapters ? *adapters : Adapters{};
   // the fused form reads X by 16-byte loads with 32-bit offsets
-  if (T <= kFusedTokens && es == 2 && d % 8 == 0 && aligned16(X) && ldx % 8 == 0 && ldx <= kMaxRowBytes / es)
-    return ydt == QAMW_F32 ? matmul_fused<MemF32>(xdt, w, x, X, d, ldx, nb, Y, ldy, st)
-                           : matmul_fused<MemBf16>(xdt, w, x, X, d, ldx, nb, Y, ldy, st);
+  if (T <= kFusedTokens && es == 2 && d % 8 == 0 && aligned16(X) && ldx % 8 == 0 && ldx <= kMaxRowBytes / es) {
+    if (xdt == QAMW_F16) return matmul_thin<1, MemF16, Out, true, NoAdapters>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
+    if (adapters) return matmul_thin<1, MemBf16, Out, true, AdaptersBf16>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
+    return matmul_thin<1, MemBf16, Out, true, NoAdapters>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
+  }
   const int rc = launch_mx4_quantize(X, xdt, T, d, ldx, xcodes, xscales, nullptr, QAMW_BF16, 0, st);
   if (rc) return rc;
-  return ydt == QAMW_F32 ? matmul_quantised<MemF32>(p, w, x, d, nb, Y, ldy, part, st)
-                         : matmul_quantised<MemBf16>(p, w, x, d, nb, Y, ldy, part, st);
+  if (!adapters) return matmul_quantised<Out, NoAdapters>(p, w, x, d, nb, Y, ldy, part, ad, st);
+  if (xdt == QAMW_F32) return matmul_quantised<Out, AdaptersF32>(p, w, x, d, nb, Y, ldy, part, ad, st);
+  return matmul_quantised<Out, AdaptersBf16>(p, w, x, d, nb, Y, ldy, part, ad, st);
+}
+int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
+                      const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws,
+                      const Adapters* adapters, hipStream_t st) {
+  return ydt == QAMW_F32 ? matmul_out<MemF32>(X, xdt, T, d, ldx, wcodes, wscales, N, Y, ldy, ws, adapters, st)
+                         : matmul_out<MemBf16>(X, xdt, T, d, ldx, wcodes, wscales, N, Y, ldy, ws, adapters, st);
 }
 
 }  // namespace qamw

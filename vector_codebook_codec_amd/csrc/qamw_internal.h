@@ -163,8 +163,21 @@ int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N
                           int64_t ldo, hipStream_t st);
 bool mx4_grid_fits(int64_t T, int64_t N, int64_t d);
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
+// Low-rank adapters beside the product (mx4_adapter.h): of U the rows are of
+// `pitch` elements, the rank rounded up to 32; in bf16 two such matrices.
+struct Adapters {
+  const void *B, *U;
+  const int32_t* index;            // [T]; outside [0, n): none
+  int n, rank, pitch;
+};
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
-                      const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws, hipStream_t st);
+                      const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws,
+                      const Adapters* ad, hipStream_t st);       // ad: of X's type, or NULL
+int64_t adapter_pitch(int64_t rank);
+size_t adapter_workspace_bytes(int64_t T, int64_t rank);
+bool adapter_grid_fits(int64_t T, int64_t rank, int64_t n);
+int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t d, int64_t ldx, const void* A, const float* factors,
+                          const Adapters& ad, hipStream_t st);
 
 // ---- attention cache in microscaled 4 bits (cache.hip, cache_attention.hip)
 struct CacheShape {

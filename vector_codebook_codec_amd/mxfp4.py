@@ -1,5 +1,6 @@
 """Microscaled 4-bit floating point over torch device tensors: quantise,
-dequantise and multiply (include/qamw.h states the format).
+dequantise, multiply, and multiply with low-rank adapters of many requests
+beside the shared weights (include/qamw.h states the format).
 
 A quantised matrix is the pair (codes [N][qamw_mxfp4_row_bytes(d)],
 scales [N][qamw_mxfp4_scale_bytes(d)]), both uint8.
@@ -14,6 +15,8 @@ from . import _lib
 from .codec import _ODT, _WDT, _dev, _empty, _matrix, _raw_stream, _workspace
 
 __all__ = [
+    "qamw_mxfp4_adapter_matmul",
+    "qamw_mxfp4_adapter_matmul_workspace_bytes",
     "qamw_mxfp4_dequantize",
     "qamw_mxfp4_matmul",
     "qamw_mxfp4_matmul_workspace_bytes",
@@ -129,4 +132,55 @@ def qamw_mxfp4_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                                    ldy, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream))
     if status:
         _lib.check("qamw_mxfp4_matmul", status)
+    return out
+
+
+def qamw_mxfp4_adapter_matmul_workspace_bytes(T: int, N: int, d: int, rank: int) -> int:
+    return int(_lib.load().qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank))
+
+
+def qamw_mxfp4_adapter_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                              index: torch.Tensor, factors: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Y [T][N] = X^ W^^T + factors[i] (X A_i^T) B_i^T with i = index[t] for token t, in out_dtype (fp32 or bf16): the
+    product of qamw_mxfp4_matmul with every request's own low-rank adapter.
+
+    X [T][d], A [adapters][rank][d] and B [adapters][N][rank] fp32 or bf16 alike, A and B contiguous; index [T] int32,
+    outside [0, adapters) for a token without one; factors [adapters] fp32 (1 if not given)."""
+    T, d, ldx = _matrix(X, "X")
+    xdt = _WDT.get(X.dtype)
+    if xdt is None:
+        raise ValueError("X must be float32 or bfloat16")
+    N = _quantised(codes, scales, d)
+    _dev(A, "A")
+    _dev(B, "B")
+    n, rank = (A.shape[0], A.shape[1]) if A.dim() == 3 else (-1, -1)
+    if A.shape != (n, rank, d) or B.shape != (n, N, rank) or A.dtype is not X.dtype or B.dtype is not X.dtype or \
+            not A.is_contiguous() or not B.is_contiguous():
+        raise ValueError("A must be [adapters][rank][d] and B [adapters][N][rank], contiguous and of X's dtype")
+    _dev(index, "index")
+    if index.dtype is not torch.int32 or index.shape != (T,) or not index.is_contiguous():
+        raise ValueError("index must be a contiguous int32 tensor with an entry per row of X")
+    if factors is not None:
+        _dev(factors, "factors")
+        if factors.dtype is not torch.float32 or factors.shape != (n,) or not factors.is_contiguous():
+            raise ValueError("factors must be a contiguous float32 tensor with an entry per adapter")
+    if out is None:
+        out = _empty((T, N), out_dtype, X.device, stream)
+    t2, n2, ldy = _matrix(out, "out")
+    ydt = _WDT.get(out.dtype)
+    if t2 != T or n2 != N or ydt is None:
+        raise ValueError("out must be T x N of float32 or bfloat16")
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _workspace(lib.qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank), X.device, stream)
+    else:
+        _dev(workspace, "workspace")
+    status = lib.qamw_mxfp4_adapter_matmul(
+        X.data_ptr(), xdt, T, d, ldx, codes.data_ptr(), scales.data_ptr(), N, A.data_ptr(), B.data_ptr(), n, rank,
+        index.data_ptr(), None if factors is None else factors.data_ptr(), out.data_ptr(), ydt, ldy, workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(stream))
+    if status:
+        _lib.check("qamw_mxfp4_adapter_matmul", status)
     return out
