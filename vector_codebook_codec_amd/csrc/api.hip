@@ -726,7 +726,8 @@ static int check_cache(const void* codes, const void* scales, int64_t pages, int
   if (shift < 0 || page < kCacheMinPage || page > kCacheMaxPage)
     return fail(QAMW_EUNSUPPORTED, "a page must hold a power of two in [16, 65536] of tokens (got %lld)", (long long)page);
   if (d > kCacheMaxHeadDim) return fail(QAMW_EUNSUPPORTED, "head dimension %lld above 256", (long long)d);
-  if (heads > 65536 || pages > kCacheMaxBytes / (heads * page * mx4_blocks(d) * 16) || pages > INT32_MAX)
+  // a page of all heads is stepped over by 32 bits
+  if (heads > 65536 || heads * page > (int64_t(1) << 31) / (mx4_blocks(d) * 16) || pages > kCacheMaxBytes / (heads * page * mx4_blocks(d) * 16) || pages > INT32_MAX)
     return fail(QAMW_EUNSUPPORTED, "cache too large");
   if (pages && (!codes || !scales || !aligned16(codes) || !aligned16(scales)))
     return fail(QAMW_EINVAL, "codes and scales must be non-NULL and 16-byte aligned");

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <float.h>
+#include <stdlib.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -16,6 +17,7 @@
 #include "qamw.h"
 #include "qamw_device.h"
 #include "qamw_internal.h"
+#include "tile_product.h"
 
 namespace qamw {
 
@@ -62,7 +64,7 @@ __device__ __forceinline__ TileRange tile_range(const AttentionArgs& a, const Se
   const int lo = span_begin(a, s, r0 / a.group), hi = span_end(a, s, (r1 - 1) / a.group);
   TileRange t;
   t.first = lo / kTileTokens;
-  t.count = hi > lo ? (hi + kTileTokens - 1) / kTileTokens - t.first : 0;
+  t.count = hi > lo && a.c.pages > 0 ? (hi + kTileTokens - 1) / kTileTokens - t.first : 0;
   t.shares = t.count < splits ? (t.count > 1 ? t.count : 1) : splits;
   return t;
 }
@@ -101,7 +103,240 @@ __device__ __forceinline__ f32x4 mfma_bf16(i32x4 a, i32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// Workgroup -> (sequence and key head, row tile, share).  Where the pairs
+// divide among the 8 XCDs, all work of a pair goes to one: its keys and values
+// then pass through one L2.  The last rows, which see most tokens, first.
+struct Place {
+  int pair, b, h, tile, share;
+};
+__device__ __forceinline__ Place place_of(const AttentionArgs& a, int row_tiles, int splits) {
+  const int pairs = a.sequences * a.c.heads, per = row_tiles * splits, id = blockIdx.x;
+  Place p;
+  int inner;
+  if (pairs % 8 == 0) p.pair = id / 8 / per * 8 + id % 8, inner = id / 8 % per;
+  else p.pair = id / per, inner = id % per;
+  p.b = p.pair / a.c.heads, p.h = p.pair - p.b * a.c.heads;
+  p.tile = row_tiles - 1 - inner / splits, p.share = inner % splits;
+  return p;
+}
+// uniform loads of the page table go through the scalar cache
+typedef const __attribute__((address_space(4))) int32_t* ConstantInts;
+
+// One head's rows of a page, keys or values.  For a page outside the cache
+// page 0 is read (there is one: without pages there are no tiles) and nothing
+// of it used.
+struct PageRows {
+  const uint8_t *codes, *scales;                   // of page 0
+  uint32_t code_step, scale_step;                  // from page to page
+  uint32_t code_bytes, scale_bytes;                // of one
+  __device__ __forceinline__ PageRows(const AttentionArgs& a, int kv, int h) {
+    code_bytes = (uint32_t)(16 * a.c.nb) << a.c.page_shift, scale_bytes = (uint32_t)a.c.sb << a.c.page_shift;
+    code_step = code_bytes * (uint32_t)a.c.heads, scale_step = scale_bytes * (uint32_t)a.c.heads;
+    codes = a.codes + kv * a.c.pages * code_step + (int64_t)h * code_bytes;
+    scales = a.scales + kv * a.c.pages * scale_step + (int64_t)h * scale_bytes;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t code_buffer(uint32_t page) const {
+    return buffer_of(codes + (uint64_t)page * code_step, code_bytes);
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_buffer(uint32_t page) const {
+    return buffer_of(scales + (uint64_t)page * scale_step, scale_bytes);
+  }
+};
+
+// A lane's values of 8 tokens, 4 g + (0 .. 3) of either group of 16, as they
+// lie in the cache: elements 2 DB l16 + (0 .. 2 DB - 1) of each, and the scale
+// codes of all their blocks.
+template <int DB>
+struct RawValues {
+  static constexpr int VW = DB == 8 ? 2 : 1;       // words of a token's elements in one lane
+  uint32_t w[2][4][VW], s[2][DB];
+  // a group's page through its two buffers, the group's rows from byte offsets c and sc of them
+  __device__ __forceinline__ void load(int i, __amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, int rb, int c, int sc,
+                                       int l16, int g) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int off = (int)(l16 * DB < rb ? (uint32_t)((4 * g + e) * rb + l16 * DB) : kPastEnd);
+      if constexpr (DB == 2) {
+        w[i][e][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(codes, off, c, 0);
+      } else if constexpr (DB == 4) {
+        w[i][e][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(codes, off, c, 0);
+      } else {
+        const auto x = __builtin_amdgcn_raw_buffer_load_b64(codes, off, c, 0);
+        w[i][e][0] = (uint32_t)x[0], w[i][e][VW - 1] = (uint32_t)x[1];
+      }
+    }
+    if constexpr (DB == 2) {
+      const auto x = __builtin_amdgcn_raw_buffer_load_b64(scales, 8 * g, sc, 0);
+      s[i][0] = (uint32_t)x[0], s[i][1] = (uint32_t)x[1];
+    } else {
+#pragma unroll
+      for (int k = 0; k < DB; k += 4) {
+        const auto x = __builtin_amdgcn_raw_buffer_load_b128(scales, 4 * DB * g + 4 * k, sc, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][k + e] = (uint32_t)x[e];
+      }
+    }
+  }
+  // codes of the 8 tokens and the scale code of this lane's block of each
+  __device__ __forceinline__ void take(uint32_t (&vc)[8], uint32_t (&vw)[8][VW], int l16) const {
+    const int block = l16 * DB / 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (DB == 2) vc[4 * i + e] = s[i][e / 2] >> (16 * (e & 1) + 8 * block) & 255u;
+        if constexpr (DB == 4) vc[4 * i + e] = s[i][e] >> (8 * block) & 255u;
+        if constexpr (DB == 8) vc[4 * i + e] = (block < 4 ? s[i][2 * e] : s[i][2 * e + 1]) >> (8 * (block & 3)) & 255u;
+#pragma unroll
+        for (int n = 0; n < VW; ++n) vw[4 * i + e][n] = w[i][e][n];
+      }
+  }
+};
+// tokens outside [lo, hi) or of no page, which may hold anything, as 0; t: the lane's first token
+template <int DB>
+__device__ __forceinline__ void clear_unseen(uint32_t (&vc)[8], uint32_t (&vw)[8][RawValues<DB>::VW], int t, int lo, int hi,
+                                             const bool (&ok)[2]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (t + 12 * (e / 4) + e < lo || t + 12 * (e / 4) + e >= hi || !ok[e / 4]) {
+      vc[e] = 0;
+#pragma unroll
+      for (int n = 0; n < RawValues<DB>::VW; ++n) vw[e][n] = 0;
+    }
+}
+// NaN blocks as 0, and where they were as 1 in bf16
+template <int DB>
+__device__ __forceinline__ i32x4 take_nan(uint32_t (&vc)[8], uint32_t (&vw)[8][RawValues<DB>::VW]) {
+  i32x4 bad = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (vc[e] == 255u) {
+      bad[e / 2] |= 0x3f80 << (16 * (e & 1));
+      vc[e] = 0;
+#pragma unroll
+      for (int n = 0; n < RawValues<DB>::VW; ++n) vw[e][n] = 0;
+    }
+  return bad;
+}
+__device__ __forceinline__ bool any_nan(const uint32_t (&vc)[8]) {
+  uint32_t most = vc[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) most = max(most, vc[e]);
+  return __ballot(most == 255u) != 0;
+}
+// The operands V^T: put(t, f) for the t-th element of every lane.  Pairs of
+// tokens are put together by byte permutes.
+template <int DB, class Put>
+__device__ __forceinline__ void decode_values(const uint32_t (&vc)[8], const uint32_t (&vw)[8][RawValues<DB>::VW], Put&& put) {
+#pragma unroll
+  for (int n = 0; n < RawValues<DB>::VW; ++n) {
+    uint32_t d[8][4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) decode_bf16(vw[e][n], __uint_as_float(vc[e] << 23), d[e]);
+#pragma unroll
+    for (int x = 0; x < (DB == 2 ? 2 : 4); ++x) {
+      i32x4 even, odd;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        even[e] = (int)__builtin_amdgcn_perm(d[2 * e + 1][x], d[2 * e][x], 0x05040100);
+        odd[e] = (int)__builtin_amdgcn_perm(d[2 * e + 1][x], d[2 * e][x], 0x07060302);
+      }
+      put(8 * n + 2 * x, even);
+      put(8 * n + 2 * x + 1, odd);
+    }
+  }
+}
+
+// The reference of the exponentials follows the maximum only when a score
+// exceeds it by 2^8 (weights are then up to 256, far from any limit): nearly
+// all tiles go without an exchange between lanes and without a pass over the
+// sums.  Scores are those of 8 tokens of one row in every lane.
+template <int RT, int MT>
+__device__ __forceinline__ void follow_maximum(const f32x4 (&s)[RT][2], float c, float (&m)[RT], float (&l)[RT],
+                                               f32x4 (&o)[RT][MT]) {
+  float top[RT];
+  bool above = false;
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    const float x = fmaxf(fmaxf(s[j][0][0], s[j][0][1]), fmaxf(s[j][0][2], s[j][0][3])),
+                y = fmaxf(fmaxf(s[j][1][0], s[j][1][1]), fmaxf(s[j][1][2], s[j][1][3]));
+    top[j] = fmaxf(x, y) * c;
+    above |= top[j] > m[j] + 8.0f;
+  }
+  if (!__ballot(above)) return;
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    float x = fmaxf(top[j], __shfl_xor(top[j], 16));
+    x = fmaxf(m[j], fmaxf(x, __shfl_xor(x, 32)));
+    const float f = __builtin_amdgcn_exp2f(m[j] - x);
+    m[j] = x;
+    l[j] *= f;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) o[j][t] *= f;
+  }
+}
+// the weights 2^(s c - m) as operands P, and their sums
+template <int RT, int kTerms>
+__device__ __forceinline__ void weights(const f32x4 (&s)[RT][2], float c, const float (&m)[RT], float (&l)[RT],
+                                        i32x4 (&p)[RT][kTerms]) {
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i][e], c, -m[j])),
+                    p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i][e + 1], c, -m[j]));
+        l[j] += p0 + p1;
+        uint32_t t[kTerms];
+        split_bf16x2<kTerms>(p0, p1, t);
+#pragma unroll
+        for (int n = 0; n < kTerms; ++n) p[j][n][2 * i + e / 2] = (int)t[n];
+      }
+}
+// Blocks that are NaN must reach the rows that see their token and no others,
+// whose weight of it is 0: the caller takes them as 0, and the elements of a
+// row become NaN where the product of "sees the token" and "is NaN" (bad: 1 or
+// 0 in bf16 for the lane's 8 tokens) counts any.
+template <int RT, int MT, class Sees>
+__device__ __forceinline__ void spread_nan(i32x4 bad, Sees&& sees, f32x4 (&o)[RT][MT]) {
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    i32x4 seen = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (sees(j, e / 4, e & 3)) seen[e / 2] |= 0x3f80 << (16 * (e & 1));
+    const f32x4 count = mfma_bf16(bad, seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (count[e] > 0.0f)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) o[j][t][e] = NAN;
+  }
+}
+// n elements of a row from element j
+template <int n>
+__device__ __forceinline__ void store_elements(int32_t dt, void* row, int j, int d, const float (&x)[n]) {
+  if constexpr (n == 4) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (j + t < d) {
+        if (dt == QAMW_F32) ((float*)row)[j + t] = x[t];
+        else ((uint16_t*)row)[j + t] = dt == QAMW_F16 ? MemF16::put(x[t]) : MemBf16::put(x[t]);
+      }
+  } else {
+#pragma unroll
+    for (int t = 0; t < n; t += 8) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = x[t + e];
+      store8_as(dt, row, j + t, d, y);
+    }
+  }
+}
+
 // floats of a share's partial result: sums, then the reference exponent and the sum of weights of each row
+template <int DB, int RT, int kTerms> constexpr int attn_waves() { return RT == 4 ? 1 : DB == 8 || RT == 2 ? 2 : 3; }
 template <int DB, int RT> constexpr int part_floats() { return 16 * RT * (32 * DB + 2); }
 
 // ---------------------------------------------------------------------------
@@ -116,11 +351,8 @@ template <int DB, int RT> constexpr int part_floats() { return 16 * RT * (32 * D
 //     16) + r: a row's running maximum and sum are one register.
 //   * O^T = V^T P^T: the scores of two groups of 16 tokens are in place as the
 //     operand P.  Lane l decodes elements 2 DB (l % 16) + (0 .. 2 DB - 1) of
-//     the same 8 tokens, pairs of tokens are put together by byte permutes,
-//     and the m-th instruction multiplies the m-th element of every lane.
-// The reference of the exponentials follows the maximum only when a score
-// exceeds it by 2^8 (they are then up to 256, far from any limit): nearly all
-// tiles go without an exchange between lanes and without a pass over the sums.
+//     the same 8 tokens, and the m-th instruction multiplies the m-th element
+//     of every lane.
 //
 // kTerms: q and the weights p are sums of that many bf16 numbers: 1 for bf16
 // in and out (p rounded by at most 2^-8 of itself, each weight on its own; as
@@ -128,32 +360,24 @@ template <int DB, int RT> constexpr int part_floats() { return 16 * RT * (32 * D
 // (p to 2^-16 and 2^-24).  Sums are fp32 throughout.
 // ---------------------------------------------------------------------------
 template <int DB, int RT, int kTerms>
-__global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(AttentionArgs a, int row_tiles, int splits,
+__global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void cache_attention_kernel(AttentionArgs a, int row_tiles, int splits,
                                                                        float* __restrict__ part) {
   constexpr int MT = 2 * DB;                       // matrix instructions along the head
-  constexpr int VW = DB == 8 ? 2 : 1;              // words of a token's elements in one lane
   constexpr int LD = 32 * DB + 4;                  // LDS row, off the banks' period
   __shared__ __align__(16) float joined[kAttnWaves * 16 * LD];
   __shared__ float stats[2][kAttnWaves][16];
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // Workgroup -> (sequence and key head, row tile, share).  Where the pairs
-  // divide among the 8 XCDs, all work of a pair goes to one: its keys and
-  // values then pass through one L2.  The last rows, which see most tokens, first.
-  const int pairs = a.sequences * a.c.heads, per = row_tiles * splits, id = blockIdx.x;
-  int pair, inner;
-  if (pairs % 8 == 0) pair = id / 8 / per * 8 + id % 8, inner = id / 8 % per;
-  else pair = id / per, inner = id % per;
-  const int b = pair / a.c.heads, h = pair - b * a.c.heads;
-  const int tile = row_tiles - 1 - inner / splits, share = inner % splits;
-  const Sequence seq = sequence_of(a, b);
-  const int rows = min((int64_t)seq.n * a.group, (int64_t)INT32_MAX), r0 = tile * 16 * RT, r1 = min(rows, r0 + 16 * RT);
+  const Place at = place_of(a, row_tiles, splits);
+  const int h = at.h;
+  const Sequence seq = sequence_of(a, at.b);
+  const int rows = (int)min((int64_t)seq.n * a.group, (int64_t)INT32_MAX), r0 = at.tile * 16 * RT, r1 = min(rows, r0 + 16 * RT);
   if (r0 >= rows) return;
   const TileRange range = tile_range(a, seq, r0, r1, splits);
-  if (share >= range.shares) return;
-  const int k0 = range.first + (int)((int64_t)range.count * share / range.shares),
-            k1 = range.first + (int)((int64_t)range.count * (share + 1) / range.shares);
+  if (at.share >= range.shares) return;
+  const int k0 = range.first + (int)((int64_t)range.count * at.share / range.shares),
+            k1 = range.first + (int)((int64_t)range.count * (at.share + 1) / range.shares);
   // tokens of any row, and of every row
   const int lo_any = span_begin(a, seq, r0 / a.group), hi_any = span_end(a, seq, (r1 - 1) / a.group);
   const int lo_all = span_begin(a, seq, (r1 - 1) / a.group), hi_all = span_end(a, seq, r0 / a.group);
@@ -189,14 +413,13 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
   // page outside the cache, a group outside every row's span and elements past
   // the head read as 0
   struct Raw {
-    uint32_t k[2][DB], ks[2], v[2][4][VW], vs[2][DB];
+    uint32_t k[2][DB], ks[2];
+    RawValues<DB> v;
     bool page_ok[2];
   };
-  typedef const __attribute__((address_space(4))) int32_t* ConstantInts;
-  const ConstantInts table = (ConstantInts)(uintptr_t)(a.table + b * a.table_pitch);
+  const ConstantInts table = (ConstantInts)(uintptr_t)(a.table + at.b * a.table_pitch);
   const int rb = 16 * a.c.nb, shift = a.c.page_shift, in_page = (1 << shift) - 1;
-  const uint32_t page_codes = (uint32_t)rb << shift, page_scales = (uint32_t)a.c.sb << shift;
-  const int64_t v_codes = a.c.pages * a.c.heads * (int64_t)page_codes, v_scales = a.c.pages * a.c.heads * (int64_t)page_scales;
+  const PageRows key_rows(a, 0, h), value_rows(a, 1, h);
   auto pages_of = [&](int k, int (&page)[2]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -204,21 +427,18 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
       page[i] = k < k1 && t < hi_any && t + 16 > lo_any ? table[t >> shift] : -1;
     }
   };
-  const uint32_t k_at = (uint32_t)(l16 * rb + g * (4 * DB)), v_at = (uint32_t)(4 * g * rb + l16 * DB);
+  const uint32_t k_at = (uint32_t)(l16 * rb + g * (4 * DB));
   const uint32_t ks_at = (uint32_t)(l16 * a.c.sb + (DB == 2 ? g >> 1 : DB == 4 ? g : 2 * g));
   auto load = [&](int k, const int (&page)[2], Raw& r) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool ok = page[i] >= 0 && page[i] < a.c.pages;
       r.page_ok[i] = ok;
-      const int64_t block = (int64_t)(ok ? page[i] : 0) * a.c.heads + h;
-      const uint8_t *pc = a.codes + block * page_codes, *ps = a.scales + block * page_scales;
-      const __amdgpu_buffer_rsrc_t bk = buffer_of(pc, ok ? page_codes : 0), bks = buffer_of(ps, ok ? page_scales : 0),
-                                   bv = buffer_of(pc + v_codes, ok ? page_codes : 0),
-                                   bvs = buffer_of(ps + v_scales, ok ? page_scales : 0);
-      // scalar offsets stay inside the buffer: the range check subtracts them from its size
-      const int at = ok ? k * kTileTokens + wave * kWaveTokens + 16 * i & in_page : 0;
-      const int sc = at * rb, ss = at * a.c.sb;
+      const uint32_t id = ok ? (uint32_t)page[i] : 0u;
+      const __amdgpu_buffer_rsrc_t bk = key_rows.code_buffer(id), bks = key_rows.scale_buffer(id);
+      // offsets stay inside a page: the range check subtracts the scalar one from its size
+      const int in = (k * kTileTokens + wave * kWaveTokens + 16 * i) & in_page;
+      const int sc = in * rb, ss = in * a.c.sb;
 #pragma unroll
       for (int w = 0; w < DB; w += 4) {            // 16 bytes (8 with DB = 2), a whole or no part of a block
         const int off = (int)(g * 4 * DB + 4 * w < rb ? k_at + 4 * w : kPastEnd);
@@ -233,30 +453,7 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
       }
       if constexpr (DB == 8) r.ks[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bks, (int)ks_at, ss, 0);
       else r.ks[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(bks, (int)ks_at, ss, 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int off = (int)(l16 * DB < rb ? v_at + e * rb : kPastEnd);
-        if constexpr (DB == 2) {
-          r.v[i][e][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(bv, off, sc, 0);
-        } else if constexpr (DB == 4) {
-          r.v[i][e][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(bv, off, sc, 0);
-        } else {
-          const auto x = __builtin_amdgcn_raw_buffer_load_b64(bv, off, sc, 0);
-          r.v[i][e][0] = (uint32_t)x[0], r.v[i][e][VW - 1] = (uint32_t)x[1];
-        }
-      }
-      // the scale codes of 4 tokens in a row
-      if constexpr (DB == 2) {
-        const auto x = __builtin_amdgcn_raw_buffer_load_b64(bvs, 8 * g, ss, 0);
-        r.vs[i][0] = (uint32_t)x[0], r.vs[i][1] = (uint32_t)x[1];
-      } else {
-#pragma unroll
-        for (int w = 0; w < DB; w += 4) {
-          const auto x = __builtin_amdgcn_raw_buffer_load_b128(bvs, 4 * DB * g + 4 * w, ss, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) r.vs[i][w + e] = (uint32_t)x[e];
-        }
-      }
+      r.v.load(i, value_rows.code_buffer(id), value_rows.scale_buffer(id), rb, sc, ss, l16, g);
     }
   };
 
@@ -293,125 +490,21 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
           for (int e = 0; e < 4; ++e)
             if (!sees(j, i, e)) s[j][i][e] = -INFINITY;
     }
-    // ---- the reference of the exponentials
-    float top[RT];
-    bool above = false;
-#pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      const float x = fmaxf(fmaxf(s[j][0][0], s[j][0][1]), fmaxf(s[j][0][2], s[j][0][3])),
-                  y = fmaxf(fmaxf(s[j][1][0], s[j][1][1]), fmaxf(s[j][1][2], s[j][1][3]));
-      top[j] = fmaxf(x, y) * c;
-      above |= top[j] > m[j] + 8.0f;
-    }
-    if (__ballot(above)) {
-#pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        float x = fmaxf(top[j], __shfl_xor(top[j], 16));
-        x = fmaxf(m[j], fmaxf(x, __shfl_xor(x, 32)));
-        const float f = __builtin_amdgcn_exp2f(m[j] - x);
-        m[j] = x;
-        l[j] *= f;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) o[j][t] *= f;
-      }
-    }
-    // ---- weights
+    follow_maximum<RT, MT>(s, c, m, l, o);
     i32x4 p[RT][kTerms];
-#pragma unroll
-    for (int j = 0; j < RT; ++j) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i][e], c, -m[j])),
-                      p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i][e + 1], c, -m[j]));
-          l[j] += p0 + p1;
-          uint32_t t[kTerms];
-          split_bf16x2<kTerms>(p0, p1, t);
-#pragma unroll
-          for (int n = 0; n < kTerms; ++n) p[j][n][2 * i + e / 2] = (int)t[n];
-        }
+    weights<RT, kTerms>(s, c, m, l, p);
+    uint32_t vc[8], vw[8][RawValues<DB>::VW];
+    r.v.take(vc, vw, l16);
+    if (!whole) {                                  // rows may see different tokens
+      clear_unseen<DB>(vc, vw, t0 + 4 * g, lo_any, hi_any, r.page_ok);
+      if (any_nan(vc)) spread_nan<RT, MT>(take_nan<DB>(vc, vw), sees, o);
     }
-    // ---- values: scale codes of this lane's block for its 8 tokens
-    uint32_t vc[8], vw[8][VW];
-    const int block = l16 * DB / 16;
+    decode_values<DB>(vc, vw, [&](int t, i32x4 f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (DB == 2) vc[4 * i + e] = r.vs[i][e / 2] >> (16 * (e & 1) + 8 * block) & 255u;
-        if constexpr (DB == 4) vc[4 * i + e] = r.vs[i][e] >> (8 * block) & 255u;
-        if constexpr (DB == 8) vc[4 * i + e] = (block < 4 ? r.vs[i][2 * e] : r.vs[i][2 * e + 1]) >> (8 * (block & 3)) & 255u;
-#pragma unroll
-        for (int n = 0; n < VW; ++n) vw[4 * i + e][n] = r.v[i][e][n];
-      }
-    // tokens that no row sees may hold anything
-    if (!whole) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = t0 + 16 * i + 4 * g + e;
-          if (t < lo_any || t >= hi_any) {
-            vc[4 * i + e] = 0;
-#pragma unroll
-            for (int n = 0; n < VW; ++n) vw[4 * i + e][n] = 0;
-          }
-        }
-    }
-    // Blocks that are NaN must reach the rows that see their token and no
-    // others, whose weight of it is 0: they are taken as 0, and the elements of
-    // a row become NaN where the product of "sees the token" and "is NaN" counts any.
-    uint32_t most = vc[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) most = max(most, vc[e]);
-    if (__ballot(most == 255u)) {
-      i32x4 bad = {0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (vc[e] == 255u) {
-          bad[e / 2] |= 0x3f80 << (16 * (e & 1));
-          vc[e] = 0;
-#pragma unroll
-          for (int n = 0; n < VW; ++n) vw[e][n] = 0;
-        }
-#pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        i32x4 seen = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (sees(j, e / 4, e & 3)) seen[e / 2] |= 0x3f80 << (16 * (e & 1));
-        const f32x4 count = mfma_bf16(bad, seen, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (count[e] > 0.0f)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) o[j][t][e] = NAN;
-      }
-    }
-    // ---- O^T += V^T P^T, two elements of the head at a time from one byte of every token
-#pragma unroll
-    for (int n = 0; n < VW; ++n) {
-      uint32_t d[8][4];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) decode_bf16(vw[e][n], __uint_as_float(vc[e] << 23), d[e]);
-#pragma unroll
-      for (int x = 0; x < (DB == 2 ? 2 : 4); ++x) {
-        i32x4 even, odd;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          even[e] = (int)__builtin_amdgcn_perm(d[2 * e + 1][x], d[2 * e][x], 0x05040100);
-          odd[e] = (int)__builtin_amdgcn_perm(d[2 * e + 1][x], d[2 * e][x], 0x07060302);
-        }
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            o[j][8 * n + 2 * x] = mfma_bf16(even, p[j][t], o[j][8 * n + 2 * x]);
-            o[j][8 * n + 2 * x + 1] = mfma_bf16(odd, p[j][t], o[j][8 * n + 2 * x + 1]);
-          }
-      }
-    }
+        for (int n = 0; n < kTerms; ++n) o[j][t] = mfma_bf16(f, p[j][n], o[j][t]);
+    });
   };
 
   // ---- the tiles, the next one's loads in flight while one is computed, the one after's pages too
@@ -452,7 +545,7 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
       for (int t = 0; t < MT; t += 4)
         *reinterpret_cast<f32x4*>(to + MT * e + t) = f32x4{o[j][t][e], o[j][t + 1][e], o[j][t + 2][e], o[j][t + 3][e]} * f;
     __syncthreads();
-    const int sub = threadIdx.x >> 4, at = (threadIdx.x & 15) * MT, row = r0 + 16 * j + sub;
+    const int sub = threadIdx.x >> 4, col = (threadIdx.x & 15) * MT, row = r0 + 16 * j + sub;
     if (row >= r1) continue;
     float x[MT], sum = 0.0f, ref = stats[0][0][sub];
 #pragma unroll
@@ -463,16 +556,16 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
       ref = fmaxf(ref, stats[0][w][sub]);
 #pragma unroll
       for (int t = 0; t < MT; t += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(joined + (w * 16 + sub) * LD + at + t);
+        const f32x4 v = *reinterpret_cast<const f32x4*>(joined + (w * 16 + sub) * LD + col + t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[t + e] += v[e];
       }
     }
     if (range.shares > 1) {
-      float* to_part = part + (((int64_t)pair * row_tiles + tile) * splits + share) * part_floats<DB, RT>();
+      float* to_part = part + (((int64_t)at.pair * row_tiles + at.tile) * splits + at.share) * part_floats<DB, RT>();
 #pragma unroll
       for (int t = 0; t < MT; t += 4)
-        *reinterpret_cast<f32x4*>(to_part + (16 * j + sub) * 32 * DB + at + t) = f32x4{x[t], x[t + 1], x[t + 2], x[t + 3]};
+        *reinterpret_cast<f32x4*>(to_part + (16 * j + sub) * 32 * DB + col + t) = f32x4{x[t], x[t + 1], x[t + 2], x[t + 3]};
       if ((threadIdx.x & 15) == 0) {
         to_part[16 * RT * 32 * DB + 16 * j + sub] = ref;
         to_part[16 * RT * (32 * DB + 1) + 16 * j + sub] = sum;
@@ -484,25 +577,255 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_kernel(Attention
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;         // NaN stays NaN
 #pragma unroll
     for (int t = 0; t < MT; ++t) x[t] *= inv;
-    void* to_out = row_at(a.out, a.odt, query * a.o_token + head * a.o_head);
-    if constexpr (MT == 4) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (at + t < a.c.d) {
-          if (a.odt == QAMW_F32) ((float*)to_out)[at + t] = x[t];
-          else ((uint16_t*)to_out)[at + t] = a.odt == QAMW_F16 ? MemF16::put(x[t]) : MemBf16::put(x[t]);
-        }
-    } else {
-#pragma unroll
-      for (int t = 0; t < MT; t += 8) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[t + e];
-        store8_as(a.odt, to_out, at + t, a.c.d, y);
-      }
-    }
+    store_elements<MT>(a.odt, row_at(a.out, a.odt, query * a.o_token + head * a.o_head), col, a.c.d, x);
     if (a.lse && (threadIdx.x & 15) == 0)
       a.lse[query * a.c.heads * a.group + head] = sum != 0.0f ? (ref + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many query rows: each of the 4 wavefronts has 32 rows of its own and goes
+// through all tokens of the workgroup's share.  For bf16 queries and output
+// and heads of up to 128 elements.
+//   * Keys are multiplied as they lie in the cache, on the scaled matrix
+//     instructions, 128 elements at once: nothing of them is decoded.  A query
+//     goes as two 8-bit numbers of 4 significant bits each, a row with one
+//     power of two: the row's largest element is in [128, 256), the first
+//     number holds it to within half a step, the second (with a scale 2^-5 of
+//     the first's) the rest: a bf16 number's 8 bits exactly, down to elements
+//     2^-14 of the largest, and below that 2^-22 of the largest.
+//     Such an instruction takes 33 cycles, as long as the two bf16 ones that
+//     it saves (measured, 16 x 16 x 128 against two terms of 16 x 16 x 32).
+//   * Values are decoded once a workgroup, each wavefront 32 tokens, into LDS
+//     in the layout of the matrix operand, two tiles in turn: one barrier a tile.
+// ---------------------------------------------------------------------------
+template <int DB>
+__global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(AttentionArgs a, int row_tiles, int splits,
+                                                                                float* __restrict__ part) {
+  constexpr int RT = 2, MT = 2 * DB, kWaveRows = 16 * RT, kRows = kAttnWaves * kWaveRows;
+  __shared__ __align__(16) i32x4 staged[2][kAttnWaves][MT][kWave];
+  __shared__ __align__(16) i32x4 staged_bad[2][kAttnWaves][kWave];
+  __shared__ int staged_nan[2][kAttnWaves];
+  const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place at = place_of(a, row_tiles, splits);
+  const int h = at.h;
+  const Sequence seq = sequence_of(a, at.b);
+  const int rows = (int)min((int64_t)seq.n * a.group, (int64_t)INT32_MAX), r0 = at.tile * kRows, r1 = min(rows, r0 + kRows);
+  if (r0 >= rows) return;
+  const TileRange range = tile_range(a, seq, r0, r1, splits);
+  if (at.share >= range.shares) return;
+  const int k0 = range.first + (int)((int64_t)range.count * at.share / range.shares),
+            k1 = range.first + (int)((int64_t)range.count * (at.share + 1) / range.shares);
+  // tokens that any row of the workgroup sees; that any and every row of the wavefront sees
+  const int lo_group = span_begin(a, seq, r0 / a.group), hi_group = span_end(a, seq, (r1 - 1) / a.group);
+  const int w0 = r0 + wave * kWaveRows, w1 = min(rows, w0 + kWaveRows), last = max(w1 - 1, 0) / a.group, first = min(w0, rows - 1) / a.group;
+  const int lo_any = span_begin(a, seq, first), hi_any = w0 < rows ? span_end(a, seq, last) : 0;
+  const int lo_all = span_begin(a, seq, last), hi_all = span_end(a, seq, first);
+
+  // ---- queries as 8-bit numbers; the instruction's lane group g holds elements 16 g .. and 64 + 16 g ..
+  i32x8 q[RT][2];
+  int q_scale[RT], row_lo[RT], row_hi[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    const int row = min(w0 + 16 * j + l16, rows - 1), i = row / a.group, head = h * a.group + row % a.group;
+    row_lo[j] = span_begin(a, seq, i), row_hi[j] = span_end(a, seq, i);
+    const void* p = row_at(a.Q, QAMW_BF16, (seq.first + i) * a.q_token + head * a.q_head);
+    float x[4][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      load8<MemBf16>((const uint16_t*)p, (k & 2) * 32 + 16 * g + (k & 1) * 8, a.c.d, x[k]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[k][e]) & 0x7fffffffu);
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    const int exponent = max((int)(top >> 23), 13);           // 255: infinities and NaN, the row becomes NaN
+    q_scale[j] = exponent == 255 ? 255 : exponent - 7;
+    const float unit = __uint_as_float((uint32_t)(127 + 134 - min(exponent, 254)) << 23);        // 2^7 over the largest's binade
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float y0 = x[k][e] * unit, y1 = x[k][e + 1] * unit, y2 = x[k][e + 2] * unit, y3 = x[k][e + 3] * unit;
+        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y0, y1, 0, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, hi, true);
+        const f32x2_t b0 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false), b1 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
+        int lo = __builtin_amdgcn_cvt_pk_fp8_f32((y0 - b0.x) * 32.0f, (y1 - b0.y) * 32.0f, 0, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32((y2 - b1.x) * 32.0f, (y3 - b1.y) * 32.0f, lo, true);
+        q[j][0][2 * k + e / 4] = hi, q[j][1][2 * k + e / 4] = lo;
+      }
+  }
+
+  f32x4 o[RT][MT] = {};
+  float m[RT], l[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) m[j] = -FLT_MAX, l[j] = 0.0f;
+
+  const ConstantInts table = (ConstantInts)(uintptr_t)(a.table + at.b * a.table_pitch);
+  const int rb = 16 * a.c.nb, shift = a.c.page_shift, in_page = (1 << shift) - 1;
+  const PageRows key_rows(a, 0, h), value_rows(a, 1, h);
+
+  // ---- keys, 16 tokens after 16: a lane holds block g of token l % 16.  The
+  // page's buffers change where a page ends; the next one's number is read then.
+  struct Keys {
+    i32x4 c[2];
+    int s[2];
+    bool ok[2];
+  };
+  __amdgpu_buffer_rsrc_t key_codes, key_scales;
+  bool key_ok = false;
+  int next_page = -1;
+  auto turn_page = [&](int t) __attribute__((always_inline)) {
+    key_ok = next_page >= 0 && next_page < a.c.pages;
+    const uint32_t id = key_ok ? (uint32_t)next_page : 0u;
+    key_codes = key_rows.code_buffer(id), key_scales = key_rows.scale_buffer(id);
+    next_page = table[min((t >> shift) + 1, a.cols - 1)];
+  };
+  const int kc_at = g < a.c.nb ? l16 * rb + 16 * g : (int)kPastEnd, ks_at = g < a.c.nb ? l16 * a.c.sb + g : (int)kPastEnd;
+  auto load_keys = [&](int t0, Keys& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int in = (t0 + 16 * i) & in_page;
+      if (in == 0) turn_page(t0 + 16 * i);
+      r.ok[i] = key_ok;
+      r.c[i] = load16(key_codes, (uint32_t)kc_at, (uint32_t)(in * rb));
+      r.s[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(key_scales, ks_at, in * a.c.sb, 0);
+    }
+  };
+
+  // ---- values of this wavefront's 32 tokens of a tile, raw, then as operands in LDS
+  RawValues<DB> raw;
+  bool raw_ok[2];
+  int page[2];
+  auto value_pages = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) page[i] = table[min((k * kTileTokens + wave * kWaveTokens + 16 * i) >> shift, a.cols - 1)];
+  };
+  auto load_values = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      raw_ok[i] = page[i] >= 0 && page[i] < a.c.pages;
+      const uint32_t id = raw_ok[i] ? (uint32_t)page[i] : 0u;
+      const int in = (k * kTileTokens + wave * kWaveTokens + 16 * i) & in_page;
+      raw.load(i, value_rows.code_buffer(id), value_rows.scale_buffer(id), rb, in * rb, in * a.c.sb, l16, g);
+    }
+  };
+  auto stage_values = [&](int k) __attribute__((always_inline)) {
+    const int t0 = k * kTileTokens + wave * kWaveTokens;
+    uint32_t vc[8], vw[8][RawValues<DB>::VW];
+    raw.take(vc, vw, l16);
+    if (t0 < lo_group || t0 + kWaveTokens > hi_group || !raw_ok[0] || !raw_ok[1])
+      clear_unseen<DB>(vc, vw, t0 + 4 * g, lo_group, hi_group, raw_ok);
+    const bool nan = any_nan(vc);
+    if (nan) staged_bad[k & 1][wave][lane] = take_nan<DB>(vc, vw);
+    if (lane == 0) staged_nan[k & 1][wave] = nan;
+    decode_values<DB>(vc, vw, [&](int t, i32x4 f) __attribute__((always_inline)) { staged[k & 1][wave][t][lane] = f; });
+  };
+
+  const float c = a.scale * kLog2e;
+  auto compute = [&](int k, int sub, const Keys& r) __attribute__((always_inline)) {
+    const int t0 = k * kTileTokens + sub * kWaveTokens;
+    if (t0 >= hi_any || t0 + kWaveTokens <= lo_any) return;
+    f32x4 s[RT][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const i32x8 kf = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w, 0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q[j][1], z, 4, 0, 0, r.s[i], 0, q_scale[j] - 5);
+        s[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q[j][0], z, 4, 0, 0, r.s[i], 0, q_scale[j]);
+      }
+    }
+    const bool whole = t0 >= lo_all && t0 + kWaveTokens <= hi_all && r.ok[0] && r.ok[1];
+    auto sees = [&](int j, int i, int e) __attribute__((always_inline)) {
+      const int t = t0 + 16 * i + 4 * g + e;
+      return t >= row_lo[j] && t < row_hi[j] && r.ok[i];
+    };
+    if (!whole) {
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!sees(j, i, e)) s[j][i][e] = -INFINITY;
+    }
+    follow_maximum<RT, MT>(s, c, m, l, o);
+    i32x4 p[RT][1];
+    weights<RT, 1>(s, c, m, l, p);
+    if (__builtin_amdgcn_readfirstlane(staged_nan[k & 1][sub])) spread_nan<RT, MT>(staged_bad[k & 1][sub][lane], sees, o);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const i32x4 v = staged[k & 1][sub][t][lane];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) o[j][t] = mfma_bf16(v, p[j][0], o[j][t]);
+    }
+  };
+
+  if (k0 < k1) {
+    Keys keys[2];
+    value_pages(k0);
+    next_page = table[(k0 * kTileTokens) >> shift];
+    if ((k0 * kTileTokens) & in_page) turn_page(k0 * kTileTokens);       // the share starts inside a page
+    load_keys(k0 * kTileTokens, keys[0]);
+    load_values(k0);
+    value_pages(k0 + 1);
+    stage_values(k0);
+    load_values(k0 + 1);
+    __syncthreads();
+    // Tile k is multiplied from one half of LDS while the other, which nobody reads since the last barrier, is filled.
+    for (int k = k0; k < k1; ++k) {
+#pragma unroll
+      for (int sub = 0; sub < 4; ++sub) {
+        load_keys(k * kTileTokens + (sub + 1) * kWaveTokens, keys[~sub & 1]);
+        if (sub == 0) value_pages(k + 2);
+        compute(k, sub, keys[sub & 1]);
+        if (sub == 1) {
+          stage_values(k + 1);
+          load_values(k + 2);
+        }
+      }
+      __syncthreads();
+    }
+  }
+
+  // ---- results: lane l has row l % 16 and elements MT (4 (l / 16) + e) + t
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    l[j] += __shfl_xor(l[j], 16);
+    l[j] += __shfl_xor(l[j], 32);
+    const int row = w0 + 16 * j + l16;
+    if (row >= rows) continue;
+    if (range.shares > 1) {
+      float* to = part + (((int64_t)at.pair * row_tiles + at.tile) * splits + at.share) * ((int64_t)kRows * (32 * DB + 2));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int t = 0; t < MT; t += 4)
+          *reinterpret_cast<f32x4*>(to + (row - r0) * 32 * DB + MT * (4 * g + e) + t) =
+              f32x4{o[j][t][e], o[j][t + 1][e], o[j][t + 2][e], o[j][t + 3][e]};
+      if (g == 0) {
+        to[kRows * 32 * DB + row - r0] = m[j];
+        to[kRows * (32 * DB + 1) + row - r0] = l[j];
+      }
+      continue;
+    }
+    const int64_t query = seq.first + row / a.group;
+    const int head = h * a.group + row % a.group;
+    const float inv = l[j] != 0.0f ? 1.0f / l[j] : 0.0f;
+    void* to = row_at(a.out, QAMW_BF16, query * a.o_token + head * a.o_head);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) x[t] = o[j][t][e] * inv;
+      store_elements<MT>(QAMW_BF16, to, MT * (4 * g + e), a.c.d, x);
+    }
+    if (a.lse && g == 0)
+      a.lse[query * a.c.heads * a.group + head] = l[j] != 0.0f ? (m[j] + __builtin_amdgcn_logf(l[j])) * kLn2 : -INFINITY;
   }
 }
 
@@ -569,13 +892,20 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_join_kernel(Atte
 static int head_blocks(int64_t d) { return d <= 64 ? 2 : d <= 128 ? 4 : 8; }
 static int dtype_terms(int32_t dt) { return dt == QAMW_F32 ? 3 : dt == QAMW_F16 ? 2 : 1; }
 
+static int row_fragments(int64_t rows, int db, int terms) {
+  const int lim = getenv("RTMIN") ? atoi(getenv("RTMIN")) : 64;
+  const int lim2 = getenv("RT2MIN") ? atoi(getenv("RT2MIN")) : 64;
+  if (terms == 1 && db <= 4 && rows > lim) return 8;
+  if (terms == 1 && db <= 4 && rows > lim2) return 2;
+  return 1;
+}
+
 AttentionPlan attention_plan(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads, int64_t group, int64_t d,
                              int64_t tokens, int32_t qdt, int32_t odt) {
   const int64_t most_rows = std::min(max_queries, T) * group;
   const int terms = std::max(dtype_terms(qdt), dtype_terms(odt)), db = head_blocks(d);
   AttentionPlan p;
-  p.rows = 16;
-  (void)terms;
+  p.rows = 16 * row_fragments(most_rows, db, terms);
   p.row_tiles = (int)std::min<int64_t>(tiles_of(most_rows, p.rows), INT32_MAX);
   const int64_t items = sequences * heads * p.row_tiles, tiles = std::max<int64_t>(tiles_of(tokens, kTileTokens), 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({tiles_of(4 * kCus, std::max<int64_t>(items, 1)), tiles, kMaxSplits}));
@@ -584,19 +914,32 @@ AttentionPlan attention_plan(int64_t T, int64_t sequences, int64_t max_queries, 
   return p;
 }
 
+template <int DB>
+static int join_shares(const AttentionArgs& a, const AttentionPlan& p, const float* part, hipStream_t st) {
+  if (p.splits == 1) return QAMW_OK;
+  hipLaunchKernelGGL((cache_attention_join_kernel<DB>), dim3((unsigned)tiles_of(a.T * a.c.heads * a.group, kAttnWaves)),
+                     dim3(kAttnThreads), 0, st, a, p.rows, p.row_tiles, p.splits, part);
+  return check_launch("cache_attention_join_kernel");
+}
 template <int DB, int RT, int kTerms>
 static int attention_as(const AttentionArgs& a, const AttentionPlan& p, float* part, hipStream_t st) {
   hipLaunchKernelGGL((cache_attention_kernel<DB, RT, kTerms>), dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a,
                      p.row_tiles, p.splits, part);
   const int rc = check_launch("cache_attention_kernel");
-  if (rc || p.splits == 1) return rc;
-  hipLaunchKernelGGL((cache_attention_join_kernel<DB>), dim3((unsigned)tiles_of(a.T * a.c.heads * a.group, kAttnWaves)),
-                     dim3(kAttnThreads), 0, st, a, p.rows, p.row_tiles, p.splits, part);
-  return check_launch("cache_attention_join_kernel");
+  return rc ? rc : join_shares<DB>(a, p, part, st);
+}
+template <int DB>
+static int attention_chunk(const AttentionArgs& a, const AttentionPlan& p, float* part, hipStream_t st) {
+  hipLaunchKernelGGL((cache_attention_chunk_kernel<DB>), dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a, p.row_tiles,
+                     p.splits, part);
+  const int rc = check_launch("cache_attention_chunk_kernel");
+  return rc ? rc : join_shares<DB>(a, p, part, st);
 }
 template <int DB>
 static int attention_of(const AttentionArgs& a, const AttentionPlan& p, float* part, hipStream_t st) {
   const int terms = std::max(dtype_terms(a.qdt), dtype_terms(a.odt));
+  if constexpr (DB <= 4) if (p.rows == 128) return attention_chunk<DB>(a, p, part, st);
+  if (p.rows == 32) return attention_as<DB, 2, 1>(a, p, part, st);
   if (terms == 3) return attention_as<DB, 1, 3>(a, p, part, st);
   if (terms == 2) return attention_as<DB, 1, 2>(a, p, part, st);
   return attention_as<DB, 1, 1>(a, p, part, st);
