@@ -725,24 +725,25 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
   };
 
   const float c = a.scale * kLog2e;
-  auto compute = [&](int k, int sub, const Keys& r) __attribute__((always_inline)) {
+  auto multiply_keys = [&](const Keys& r, f32x4 (&s)[RT][2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 1; n >= 0; --n)                   // the rest of the queries first
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const i32x8 kf = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w, 0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+          s[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q[j][n], n ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : s[j][i], 4,
+                                                                     0, 0, r.s[i], 0, n ? q_scale[j] - 5 : q_scale[j]);
+      }
+  };
+  auto compute = [&](int k, int sub, f32x4 (&s)[RT][2], const bool (&ok)[2]) __attribute__((always_inline)) {
     const int t0 = k * kTileTokens + sub * kWaveTokens;
     if (t0 >= hi_any || t0 + kWaveTokens <= lo_any) return;
-    f32x4 s[RT][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const i32x8 kf = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w, 0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q[j][1], z, 4, 0, 0, r.s[i], 0, q_scale[j] - 5);
-        s[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q[j][0], z, 4, 0, 0, r.s[i], 0, q_scale[j]);
-      }
-    }
-    const bool whole = t0 >= lo_all && t0 + kWaveTokens <= hi_all && r.ok[0] && r.ok[1];
+    const bool whole = t0 >= lo_all && t0 + kWaveTokens <= hi_all && ok[0] && ok[1];
     auto sees = [&](int j, int i, int e) __attribute__((always_inline)) {
       const int t = t0 + 16 * i + 4 * g + e;
-      return t >= row_lo[j] && t < row_hi[j] && r.ok[i];
+      return t >= row_lo[j] && t < row_hi[j] && ok[i];
     };
     if (!whole) {
 #pragma unroll
@@ -754,35 +755,47 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
             if (!sees(j, i, e)) s[j][i][e] = -INFINITY;
     }
     follow_maximum<RT, MT>(s, c, m, l, o);
+    // the values are on their way from LDS while the weights are made
+    i32x4 v[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) v[t] = staged[k & 1][sub][t][lane];
+    __builtin_amdgcn_sched_barrier(0);
     i32x4 p[RT][1];
     weights<RT, 1>(s, c, m, l, p);
     if (__builtin_amdgcn_readfirstlane(staged_nan[k & 1][sub])) spread_nan<RT, MT>(staged_bad[k & 1][sub][lane], sees, o);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const i32x4 v = staged[k & 1][sub][t][lane];
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) o[j][t] = mfma_bf16(v, p[j][0], o[j][t]);
-    }
+      for (int j = 0; j < RT; ++j) o[j][t] = mfma_bf16(v[t], p[j][0], o[j][t]);
   };
 
   if (k0 < k1) {
-    Keys keys[2];
+    Keys keys;
+    f32x4 s[2][RT][2];
+    bool ok[2][2];
     value_pages(k0);
     next_page = table[(k0 * kTileTokens) >> shift];
     if ((k0 * kTileTokens) & in_page) turn_page(k0 * kTileTokens);       // the share starts inside a page
-    load_keys(k0 * kTileTokens, keys[0]);
+    load_keys(k0 * kTileTokens, keys);
     load_values(k0);
     value_pages(k0 + 1);
+    multiply_keys(keys, s[0]);
+    ok[0][0] = keys.ok[0], ok[0][1] = keys.ok[1];
+    load_keys(k0 * kTileTokens + kWaveTokens, keys);
     stage_values(k0);
     load_values(k0 + 1);
     __syncthreads();
-    // Tile k is multiplied from one half of LDS while the other, which nobody reads since the last barrier, is filled.
+    // Tile k is multiplied from one half of LDS while the other, which nobody
+    // reads since the last barrier, is filled.  The scores of the next 32
+    // tokens are under way in the matrix cores while the weights of these are made.
     for (int k = k0; k < k1; ++k) {
 #pragma unroll
       for (int sub = 0; sub < 4; ++sub) {
-        load_keys(k * kTileTokens + (sub + 1) * kWaveTokens, keys[~sub & 1]);
+        multiply_keys(keys, s[~sub & 1]);
+        ok[~sub & 1][0] = keys.ok[0], ok[~sub & 1][1] = keys.ok[1];
+        load_keys(k * kTileTokens + (sub + 2) * kWaveTokens, keys);
         if (sub == 0) value_pages(k + 2);
-        compute(k, sub, keys[sub & 1]);
+        compute(k, sub, s[sub & 1], ok[sub & 1]);
         if (sub == 1) {
           stage_values(k + 1);
           load_values(k + 2);
