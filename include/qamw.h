@@ -454,8 +454,8 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  *     Y[t] = X^[t] W^^T + factors[i] (X[t] A_i^T) B_i^T,   i = index[t]
  * The first term is qamw_mxfp4_matmul's; the second takes X as it is.
  *   X        [T][ldx] of xdtype QAMW_F32 or QAMW_BF16; A and B of the same type
- *   A        [adapters][rank][d], B [adapters][N][rank], contiguous, aligned to
- *            their elements; rank in [1, 1024] (adapters of lower rank are
+ *   A        [adapters][rank][d], B [adapters][N][rank], contiguous, 16-byte
+ *            aligned; rank in [1, 1024] (adapters of lower rank are
  *            filled up with zeros)
  *   index    [T] int32, in any order; outside [0, adapters): no adapter, the
  *            row is qamw_mxfp4_matmul's
@@ -464,10 +464,10 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  * others hold.  X A^T is summed in fp32 and multiplied as two bf16 numbers (16
  * bits) with bf16 B, in fp32 with fp32 B; all of Y is summed in fp32, in a
  * fixed order, and rounded once.
- *   workspace >= qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank),
- *             256-byte aligned
+ *   workspace >= qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank,
+ *             xdtype), 256-byte aligned
  */
-size_t qamw_mxfp4_adapter_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d, int64_t rank);
+size_t qamw_mxfp4_adapter_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d, int64_t rank, int32_t xdtype);
 int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, int64_t ldx, const uint8_t* codes,
                                   const uint8_t* scales, int64_t N, const void* A, const void* B, int64_t adapters,
                                   int64_t rank, const int32_t* index, const float* factors, void* Y, int32_t ydtype,

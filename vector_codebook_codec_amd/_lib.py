@@ -57,7 +57,7 @@ SIGNATURES = {
     "qamw_mxfp4_dequantize": (_i32, [_p, _p, _i64, _i64, _p, _i32, _i64, _p]),
     "qamw_mxfp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "qamw_mxfp4_matmul": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _i64, _p, _i32, _i64, _p, _sz, _p]),
-    "qamw_mxfp4_adapter_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "qamw_mxfp4_adapter_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i32]),
     "qamw_mxfp4_adapter_matmul": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i32,
                                          _i64, _p, _sz, _p]),
     "qamw_mxfp4_cache_row_bytes": (_i64, [_i64]),

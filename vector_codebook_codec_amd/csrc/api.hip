@@ -667,16 +667,17 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
   return launch_mx4_matmul(X, xdtype, T, (int)d, ldx, codes, scales, N, Y, ydtype, ldy, workspace, nullptr, (hipStream_t)stream);
 }
 
-// the product's workspace first, then U
+// the product's workspace first, then the adapters'
 constexpr int64_t kMaxRank = 1024;
 static bool adapter_sizes_fit(int64_t T, int64_t N, int64_t d, int64_t rank, int64_t n) {
-  return n <= INT32_MAX && rank <= kMaxRank && (n <= 0 || (adapter_grid_fits(T, rank, n) && N <= (int64_t(1) << 45) / (n * rank) &&
-                                                          d <= (int64_t(1) << 45) / (n * rank)));
+  return n <= INT32_MAX && rank <= kMaxRank && (n <= 0 || T <= 0 || N <= 0 ||
+                                                (adapter_grid_fits(T, N, rank) && N <= (int64_t(1) << 45) / (n * rank) &&
+                                                 d <= (int64_t(1) << 45) / (n * rank)));
 }
-size_t qamw_mxfp4_adapter_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d, int64_t rank) {
+size_t qamw_mxfp4_adapter_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d, int64_t rank, int32_t xdtype) {
   const size_t product = qamw_mxfp4_matmul_workspace_bytes(T, N, d);
-  if (!product || rank <= 0 || rank > kMaxRank) return 0;
-  return round_up(product, 256) + adapter_workspace_bytes(T, rank);
+  if (!product || rank <= 0 || rank > kMaxRank || (xdtype != QAMW_F32 && xdtype != QAMW_BF16)) return 0;
+  return round_up(product, 256) + adapter_workspace_bytes(T, N, xdtype, rank);
 }
 
 int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, int64_t ldx, const uint8_t* codes,
@@ -694,17 +695,17 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
   if ((rc = check_plain_rows(X, xdtype, T, d, ldx, "X", false))) return rc;
   if ((rc = check_plain_rows(Y, ydtype, N ? T : 0, N, ldy, "Y", false))) return rc;
   if (T == 0 || N == 0) return QAMW_OK;
-  const uintptr_t size = (uintptr_t)elem_size(xdtype);
-  if (adapters && (!A || !B || (uintptr_t)A % size || (uintptr_t)B % size))
-    return fail(QAMW_EINVAL, "A and B must be non-NULL and aligned to their elements");
+  if (adapters && (!A || !B || !aligned16(A) || !aligned16(B)))
+    return fail(QAMW_EINVAL, "A and B must be non-NULL and 16-byte aligned");
   if (adapters && (!index || ((uintptr_t)index & 3u) || ((uintptr_t)factors & 3u)))
     return fail(QAMW_EINVAL, "index must be non-NULL, index and factors 4-byte aligned");
-  const size_t need = qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank);
+  const size_t need = qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank, xdtype);
   if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))
     return fail(QAMW_EWORKSPACE, "the product with adapters needs %zu bytes of 256-byte aligned workspace (got %zu)", need,
                 workspace_bytes);
   char* U = (char*)workspace + round_up(qamw_mxfp4_matmul_workspace_bytes(T, N, d), 256);
-  const Adapters ad = {B, U, index, (int)adapters, (int)rank, (int)adapter_pitch(rank)};
+  const Adapters ad = {B, U, index, (int)adapters, (int)rank, (int)adapter_pitch(rank), (float*)(U + adapter_u_bytes(T, rank)),
+                       adapter_delta_pitch(N)};
   if (adapters && (rc = launch_adapter_shrink(X, xdtype, T, d, ldx, A, factors, ad, (hipStream_t)stream))) return rc;
   return launch_mx4_matmul(X, xdtype, T, (int)d, ldx, codes, scales, N, Y, ydtype, ldy, workspace, adapters ? &ad : nullptr,
                            (hipStream_t)stream);

@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "qamw.h"
 #include "mx4_adapter.h"
@@ -167,13 +168,18 @@ __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Ope
   }
   const int64_t m0 = (int64_t)tm * Tl::BM, n0 = (int64_t)tn * Tl::BN;
   f32x4 acc[Tl::TM][Tl::TN] = {};
+  if constexpr (Ad::kDelta)
+    if (s0 == 0) {
+      const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+      load_delta(acc, ad, m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + 4 * (lane >> 4),
+                 n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15), X.rows);
+    }
   if (s0 < s1) Tl::run(acc, W, m0, X, n0, kchunks, s0, s1, tile_lds);
-  if constexpr (Ad::kOn) {
-    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (s0 == 0)
-      add_adapters<Ad>(acc, ad, m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM) + (lane & 15),
-                       n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN) + (lane & 15), X.rows, W.rows, 0, 1);
-  }
+  if constexpr (Ad::kOn)
+    if (s0 == 0) {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      add_adapters_tile(acc, ad, m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM), n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN), X.rows, W.rows);
+    }
   if (!split) {
     store_tile<Tl, Out>(Y, ldy, n0, X.rows, m0, W.rows, acc, tile_lds);
     return;
@@ -390,6 +396,16 @@ bool mx4_grid_fits(int64_t T, int64_t N, int64_t d) {
   return grid_holds(p.whole + (n - p.whole) * p.splits, shape_threads(p.shape));
 }
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) { return mx4_plan(T, N, d).bytes; }
+// Whether the adapters' part of Y is written as a matrix first, which the
+// product's sums start from.  A tile's workgroup multiplies the adapters of its
+// tokens one after another: nothing where the tokens of a prompt share one,
+// but too much in a batch whose tokens have one each (48 of rank 16 beside 4096
+// x 4096: 31 us in the product's 64 workgroups).  Past 256 tokens the matrix in
+// fp32 costs more than that (4095 x 13824: 226 MB written and read).  The tile's
+// registers leave no room for other ranks than whole chunks, nor for fp32.
+bool adapters_in_delta(int64_t T, int64_t N, int32_t dt, int64_t rank) {
+  return !thin_pays(T, N) && (T <= 256 || dt == QAMW_F32 || rank % 8 != 0);
+}
 
 template <class Tl, class Out, class Ad>
 static int matmul_tiled(const TailPlan& p, const Operand& W, const Operand& X, int kchunks, void* Y, int64_t ldy, float* part,
@@ -438,7 +454,14 @@ static int matmul_quantised(const Mx4Plan& p, const Operand& W, const Operand& X
                             float* part, const Adapters& ad, hipStream_t st) {
   if (X.rows <= 16) return matmul_thin<1, MemBf16, Out, false, Ad>(W, X, nullptr, d, 0, kchunks, Y, ldy, ad, st);
   if (thin_pays(X.rows, W.rows)) return matmul_thin<2, MemBf16, Out, false, Ad>(W, X, nullptr, d, 0, kchunks, Y, ldy, ad, st);
-  return matmul_to<Out, Ad>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
+  if constexpr (Ad::kOn) {
+    if (adapters_in_delta(X.rows, W.rows, std::is_same<Ad, AdaptersF32>::value ? QAMW_F32 : QAMW_BF16, ad.rank)) {
+      const int rc = launch_adapter_expand(std::is_same<Ad, AdaptersF32>::value ? QAMW_F32 : QAMW_BF16, X.rows, W.rows, ad, st);
+      return rc ? rc : matmul_to<Out, AdapterDelta>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
+    }
+  }
+  if constexpr (std::is_same<Ad, AdaptersF32>::value) return QAMW_EINVAL;       // always as a matrix
+  else return matmul_to<Out, Ad>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
 }
 
 // Up to this many tokens of 16 bits the thin product quantises X itself: each

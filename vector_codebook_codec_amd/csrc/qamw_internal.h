@@ -165,17 +165,24 @@ bool mx4_grid_fits(int64_t T, int64_t N, int64_t d);
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
 // Low-rank adapters beside the product (mx4_adapter.h): of U the rows are of
 // `pitch` elements, the rank rounded up to 32; in bf16 two such matrices.
+// B and U rows of whole 16-byte chunks are 16-byte aligned.
 struct Adapters {
   const void *B, *U;
   const int32_t* index;            // [T]; outside [0, n): none
   int n, rank, pitch;
+  const float* delta;              // the adapters' part of Y, rows of delta_pitch (where adapters_in_delta)
+  int64_t delta_pitch;
 };
+bool adapters_in_delta(int64_t T, int64_t N, int32_t dt, int64_t rank);
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws,
                       const Adapters* ad, hipStream_t st);       // ad: of X's type, or NULL
 int64_t adapter_pitch(int64_t rank);
-size_t adapter_workspace_bytes(int64_t T, int64_t rank);
-bool adapter_grid_fits(int64_t T, int64_t rank, int64_t n);
+size_t adapter_workspace_bytes(int64_t T, int64_t N, int32_t dt, int64_t rank);
+inline int64_t adapter_delta_pitch(int64_t N) { return (N + 3) / 4 * 4; }
+inline size_t adapter_u_bytes(int64_t T, int64_t rank) { return round_up((size_t)T * adapter_pitch(rank) * 4, 256); }
+bool adapter_grid_fits(int64_t T, int64_t N, int64_t rank);
+int launch_adapter_expand(int32_t dt, int64_t T, int64_t N, const Adapters& ad, hipStream_t st);
 int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t d, int64_t ldx, const void* A, const float* factors,
                           const Adapters& ad, hipStream_t st);
 

@@ -135,8 +135,8 @@ def qamw_mxfp4_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
     return out
 
 
-def qamw_mxfp4_adapter_matmul_workspace_bytes(T: int, N: int, d: int, rank: int) -> int:
-    return int(_lib.load().qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank))
+def qamw_mxfp4_adapter_matmul_workspace_bytes(T: int, N: int, d: int, rank: int, dtype=torch.bfloat16) -> int:
+    return int(_lib.load().qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank, _WDT[dtype]))
 
 
 def qamw_mxfp4_adapter_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -174,7 +174,7 @@ def qamw_mxfp4_adapter_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torc
         raise ValueError("out must be T x N of float32 or bfloat16")
     lib = _lib.load()
     if workspace is None:
-        workspace = _workspace(lib.qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank), X.device, stream)
+        workspace = _workspace(lib.qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank, xdt), X.device, stream)
     else:
         _dev(workspace, "workspace")
     status = lib.qamw_mxfp4_adapter_matmul(
