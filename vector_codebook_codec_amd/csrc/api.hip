@@ -677,7 +677,7 @@ static bool adapter_sizes_fit(int64_t T, int64_t N, int64_t d, int64_t rank, int
 size_t qamw_mxfp4_adapter_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d, int64_t rank, int32_t xdtype) {
   const size_t product = qamw_mxfp4_matmul_workspace_bytes(T, N, d);
   if (!product || rank <= 0 || rank > kMaxRank || (xdtype != QAMW_F32 && xdtype != QAMW_BF16)) return 0;
-  return round_up(product, 256) + adapter_workspace_bytes(T, N, xdtype, rank);
+  return round_up(product, 256) + adapter_workspace_bytes(T, N, d, xdtype, rank);
 }
 
 int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, int64_t ldx, const uint8_t* codes,
@@ -703,10 +703,10 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
   if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u))
     return fail(QAMW_EWORKSPACE, "the product with adapters needs %zu bytes of 256-byte aligned workspace (got %zu)", need,
                 workspace_bytes);
-  char* U = (char*)workspace + round_up(qamw_mxfp4_matmul_workspace_bytes(T, N, d), 256);
-  const Adapters ad = {B, U, index, (int)adapters, (int)rank, (int)adapter_pitch(rank), (float*)(U + adapter_u_bytes(T, rank)),
-                       adapter_delta_pitch(N)};
-  if (adapters && (rc = launch_adapter_shrink(X, xdtype, T, d, ldx, A, factors, ad, (hipStream_t)stream))) return rc;
+  Adapters ad = {};
+  ad.B = B, ad.index = index, ad.factors = factors, ad.n = (int)adapters, ad.rank = (int)rank;
+  char* own = (char*)workspace + round_up(qamw_mxfp4_matmul_workspace_bytes(T, N, d), 256);
+  if (adapters && (rc = launch_adapter_shrink(X, xdtype, T, N, d, ldx, A, own, &ad, (hipStream_t)stream))) return rc;
   return launch_mx4_matmul(X, xdtype, T, (int)d, ldx, codes, scales, N, Y, ydtype, ldy, workspace, adapters ? &ad : nullptr,
                            (hipStream_t)stream);
 }

@@ -1,7 +1,7 @@
 // Low-rank adapters beside the microscaled 4-bit product: what the product's
 // kernels add to their sums before they are rounded and stored,
 //     Y[t][n] += sum_k U[t][k] B_i[n][k],   i = index[t],
-// with U[t] = f_i A_i X[t] from adapter_shrink_kernel (adapter.hip).  Either
+// with U[t] = f_i A_i X[t] from the kernels of adapter.hip.  Either
 // they multiply U and B themselves or they start from the second term as
 // adapter_expand_kernel left it (launch_mx4_matmul says when).
 #pragma once
@@ -50,26 +50,27 @@ struct AdapterDelta {                              // of either type, multiplied
   static constexpr bool kOn = false, kDelta = true;
 };
 
-// The adapters among the 16 TN tokens whose adapters the lanes hold (lane l:
-// token 16 j + l % 16; INT_MAX: none), one after another in the order of their
-// first token.
-template <int TN>
+// The adapters among the tokens whose adapters the lanes hold (INT_MAX: none),
+// `n` registers of one token a lane in the first kLanes lanes, one after
+// another in the order of their first token.
+template <int n, int kLanes>
 struct AdapterWalk {
-  uint32_t left[TN];                               // tokens of no adapter walked yet
-  __device__ __forceinline__ explicit AdapterWalk(const int (&idx)[TN]) {
+  uint64_t left[n];                                // tokens of no adapter walked yet
+  __device__ __forceinline__ explicit AdapterWalk(const int (&idx)[n]) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) left[j] = (uint32_t)__ballot(idx[j] != INT_MAX) & 0xffffu;
+    for (int j = 0; j < n; ++j) left[j] = __ballot(idx[j] != INT_MAX) & (~0ull >> (64 - kLanes));
   }
-  __device__ __forceinline__ int next(const int (&idx)[TN]) {           // INT_MAX: no more
+  __device__ __forceinline__ int next(const int (&idx)[n]) {            // INT_MAX: no more
     int use = INT_MAX;
 #pragma unroll
-    for (int j = TN - 1; j >= 0; --j)
-      if (left[j]) use = __builtin_amdgcn_readlane(idx[j], __builtin_ctz(left[j]));
+    for (int j = n - 1; j >= 0; --j)
+      if (left[j]) use = __builtin_amdgcn_readlane(idx[j], __builtin_ctzll(left[j]));
 #pragma unroll
-    for (int j = 0; j < TN; ++j) left[j] &= ~(uint32_t)__ballot(idx[j] == use);
+    for (int j = 0; j < n; ++j) left[j] &= ~__ballot(idx[j] == use);
     return use;
   }
 };
+// lane l: the adapters of tokens t + 16 j, t its own
 template <int TN>
 __device__ __forceinline__ void adapters_of(int (&idx)[TN], const int32_t* index, int n, int64_t t, int64_t T) {
 #pragma unroll
@@ -102,44 +103,75 @@ __device__ __forceinline__ f32x4 add_mine(bool mine, i32x4 b, const i32x4 (&u)[A
   for (int e = 0; e < 4; ++e) s[e] = mine ? s[e] : acc[e];
   return s;
 }
+// a lane's chunk of U from its parts, in a fixed order
 template <class Ad>
-__device__ __forceinline__ void load_u(i32x4 (&u)[Ad::kTerms], const Adapters& ad, int64_t t, int64_t T, int k) {
-  typedef typename Ad::E E;
+__device__ __forceinline__ void load_u(i32x4 (&u)[Ad::kTerms], const Adapters& ad, int64_t t, int64_t T, int k, float factor) {
+  constexpr int kQuads = Ad::kTerms == 1 ? 1 : 2;
+  f32x4 part[kMostAdapterParts][kQuads], s[kQuads] = {};
 #pragma unroll
-  for (int n = 0; n < Ad::kTerms; ++n) u[n] = *reinterpret_cast<const i32x4*>((const E*)ad.U + (n * T + (t < T ? t : T - 1)) * ad.pitch + k);
+  for (int p = 0; p < kMostAdapterParts; ++p)      // all at once; those that are not there again the last one
+#pragma unroll
+    for (int n = 0; n < kQuads; ++n)
+      part[p][n] = *reinterpret_cast<const f32x4*>(ad.u_parts + ((p < ad.parts ? p : ad.parts - 1) * T + t) * ad.pitch + k + 4 * n);
+#pragma unroll
+  for (int p = 0; p < kMostAdapterParts; ++p)
+    if (p < ad.parts)
+#pragma unroll
+      for (int n = 0; n < kQuads; ++n) s[n] += part[p][n];
+#pragma unroll
+  for (int n = 0; n < kQuads; ++n) s[n] *= factor;
+  if constexpr (kQuads == 1) {
+    u[0] = __builtin_bit_cast(i32x4, s[0]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float x0 = s[n / 2][2 * (n & 1)], x1 = s[n / 2][2 * (n & 1) + 1];
+      const uint32_t h = pack_bf16x2(x0, x1);
+      u[0][n] = (int)h;
+      u[1][n] = (int)pack_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+    }
+  }
 }
 
+// The adapters and factors of a lane's tokens t + 16 j: read ahead of what
+// needs them.
+template <int TN>
+struct TokenAdapters {
+  int idx[TN];
+  float factor[TN];
+  __device__ __forceinline__ TokenAdapters(const Adapters& ad, int64_t t, int64_t T) {
+    adapters_of(idx, ad.index, ad.n, t, T);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) factor[j] = ad.factors && idx[j] != INT_MAX ? ad.factors[idx[j]] : 1.0f;
+  }
+};
 // acc (fragments of rows m + 16 i by tokens t + 16 j; m and t are this lane's)
 // plus the adapters' part; of the adapters the `part`-th of every `parts`.  For
-// few fragments: the rows of kBatch adapters are in flight at a time.
-template <class Ad, int TM, int TN>
-__device__ __forceinline__ void add_adapters(f32x4 (&acc)[TM][TN], const Adapters& ad, int64_t m, int64_t t, int64_t T, int64_t N,
-                                             int part, int parts) {
+// few fragments: the rows of kBatch adapters are in flight at a time.  Returns
+// whether the lane's (last) token had one of these adapters.
+template <class Ad, int kBatch, int TM, int TN>
+__device__ __forceinline__ bool add_adapters(f32x4 (&acc)[TM][TN], const Adapters& ad, const TokenAdapters<TN>& own, int64_t m,
+                                             int64_t t, int64_t T, int64_t N, int part, int parts) {
   typedef typename Ad::E E;
-  constexpr int kBatch = TM * TN <= 2 ? 8 : 4;
   const int g = (threadIdx.x & (kWave - 1)) >> 4;
-  int idx[TN];
-  adapters_of(idx, ad.index, ad.n, t, T);
+  bool had = false;
   for (int k0 = 0; k0 < ad.pitch; k0 += Ad::kStep) {
     const int k = k0 + 16 / (int)sizeof(E) * g;    // below the pitch, a multiple of both steps
-    AdapterWalk<TN> walk(idx);
     i32x4 u[TN][Ad::kTerms];
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int n = 0; n < Ad::kTerms; ++n) {
-        const int64_t row = t + 16 * j < T ? t + 16 * j : T - 1;
-        u[j][n] = *reinterpret_cast<const i32x4*>((const E*)ad.U + (n * T + row) * ad.pitch + k);
-      }
-    int place = 0;
+    for (int j = 0; j < TN; ++j) load_u<Ad>(u[j], ad, t + 16 * j < T ? t + 16 * j : T - 1, T, k, own.factor[j]);
+    AdapterWalk<TN, 16> walk(own.idx);
+    int place = part;
     for (bool more = true; more;) {
       int use[kBatch];
       i32x4 b[kBatch][TM];
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        do {
-          use[x] = walk.next(idx);
-        } while (use[x] != INT_MAX && place++ % parts != part);
+        for (;; --place) {
+          use[x] = walk.next(own.idx);
+          if (use[x] == INT_MAX || !place) break;
+        }
+        place = parts - 1;
         more = use[x] != INT_MAX;
         if (more)
 #pragma unroll
@@ -150,44 +182,78 @@ __device__ __forceinline__ void add_adapters(f32x4 (&acc)[TM][TN], const Adapter
       for (int x = 0; x < kBatch; ++x)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-          if (use[x] != INT_MAX && __ballot(idx[j] == use[x]))
+          if (use[x] != INT_MAX && __ballot(own.idx[j] == use[x])) {
+            had |= own.idx[j] == use[x];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) acc[i][j] = add_mine<Ad>(idx[j] == use[x], b[x][i], u[j], acc[i][j]);
+            for (int i = 0; i < TM; ++i) acc[i][j] = add_mine<Ad>(own.idx[j] == use[x], b[x][i], u[j], acc[i][j]);
+          }
     }
   }
+  return had;
 }
 
-// The same for the many fragments of a tile, which leave few registers: rows
-// m0 + 16 i and tokens t0 + 16 j of the wavefront, bf16 and ranks of whole
-// 16-byte chunks.  One adapter after another (mostly there is one); addresses
-// are one register each of B and U and scalar offsets, rows past an operand's
-// end are other rows or 0 and are not stored.
-template <int TM, int TN>
-__device__ __forceinline__ void add_adapters_tile(f32x4 (&acc)[TM][TN], const Adapters& ad, int64_t m0, int64_t t0, int64_t T,
-                                                  int64_t N) {
-  if (m0 >= N || t0 >= T) return;
+// The same for a whole tile, bf16 and ranks of whole 16-byte chunks: 64 ranks
+// of U for all its tokens and of B for all its channels are copied to LDS (in
+// the order of tile_product.h's operands), one adapter after another; mostly
+// there is one.  Every thread of the workgroup calls it; lds holds kLdsBytes of the tile.
+template <class Tl>
+__device__ __forceinline__ void add_adapters_tile(f32x4 (&acc)[Tl::TM][Tl::TN], const Adapters& ad, int64_t m0, int64_t t0, int64_t T,
+                                                  int64_t N, char* lds) {
+  static_assert((2 * Tl::BN + Tl::BM) * kStepBytes <= Tl::kLdsBytes, "U and B of 64 ranks");
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
-  int idx[TN];
-  adapters_of(idx, ad.index, ad.n, t0 + l16, T);
-  const int rows = (int)(N - m0 < 16 * TM ? N - m0 : 16 * TM), tokens = (int)(T - t0 < 16 * TN ? T - t0 : 16 * TN);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / Tl::WN, wn = wave % Tl::WN;
+  const int rows = (int)(N - m0 < Tl::BM ? N - m0 : Tl::BM), tokens = (int)(T - t0 < Tl::BN ? T - t0 : Tl::BN);
   const uint32_t pu = 2u * ad.pitch, pb = 2u * ad.rank;
-  const __amdgpu_buffer_rsrc_t u_hi = buffer_of((const uint16_t*)ad.U + t0 * ad.pitch, tokens * pu),
-                               u_lo = buffer_of((const uint16_t*)ad.U + (T + t0) * ad.pitch, tokens * pu);
-  AdapterWalk<TN> walk(idx);
-  for (int use = walk.next(idx); use != INT_MAX; use = walk.next(idx)) {
-    const __amdgpu_buffer_rsrc_t bb = buffer_of((const uint16_t*)ad.B + ((int64_t)use * N + m0) * ad.rank, rows * pb);
-    for (int k0 = 0; k0 < ad.rank; k0 += 32) {
-      const int k = k0 + 8 * g;
-      const uint32_t vb = k < ad.rank ? l16 * pb + 2u * k : kPastEnd, vu = l16 * pu + 2u * k;
-      i32x4 b[TM];
+  // all tokens of the tile, to walk over; this lane's own, to keep sums by
+  int all[Tl::BN / kWave], idx[Tl::TN];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) b[i] = load16(bb, vb, 16 * i < rows ? 16u * i * pb : 0u);
+  for (int j = 0; j < Tl::BN / kWave; ++j) {
+    const int t = lane + kWave * j, i = t < tokens ? ad.index[t0 + t] : -1;
+    all[j] = i >= 0 && i < ad.n ? i : INT_MAX;
+  }
+  adapters_of(idx, ad.index, ad.n, t0 + wn * (Tl::BN / Tl::WN) + l16, T);
+  const __amdgpu_buffer_rsrc_t hi = buffer_of(ad.u16 + t0 * ad.pitch, tokens * pu),
+                               lo = buffer_of(ad.u16 + (T + t0) * ad.pitch, tokens * pu);
+  const int crow = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ ((crow >> 1) & 7);
+  char *const lds_u = lds, *const lds_b = lds + 2 * Tl::BN * kStepBytes;
+  for (int k0 = 0; k0 < ad.rank; k0 += 64) {
+    const int k = k0 + 8 * chunk;
+    __syncthreads();                               // nobody reads what LDS held
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const uint32_t at = 16 * j < tokens ? 16u * j * pu : 0u;
-        const i32x4 u[2] = {load16(u_hi, vu, at), load16(u_lo, vu, at)};
+    for (int i = 0; i < Tl::kCopiesB; ++i) {
+      const uint32_t at = k < ad.pitch ? (uint32_t)(crow + 8 * Tl::kWaves * i) * pu + 2u * k : kPastEnd;
+      copy16_to_lds(hi, lds_u + (wave + Tl::kWaves * i) * 1024, at, 0);
+      copy16_to_lds(lo, lds_u + Tl::BN * kStepBytes + (wave + Tl::kWaves * i) * 1024, at, 0);
+    }
+    AdapterWalk<Tl::BN / kWave, kWave> walk(all);
+    bool first = true;
+    for (int use = walk.next(all); use != INT_MAX; use = walk.next(all), first = false) {
+      if (!first) __syncthreads();                 // nobody reads the last adapter's rows
+      const __amdgpu_buffer_rsrc_t bb = buffer_of((const uint16_t*)ad.B + ((int64_t)use * N + m0) * ad.rank, rows * pb);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) acc[i][j] = add_mine<AdaptersBf16>(idx[j] == use, b[i], u, acc[i][j]);
+      for (int i = 0; i < Tl::kCopiesA; ++i)
+        copy16_to_lds(bb, lds_b + (wave + Tl::kWaves * i) * 1024,
+                      k < ad.rank ? (uint32_t)(crow + 8 * Tl::kWaves * i) * pb + 2u * k : kPastEnd, 0);
+      __builtin_amdgcn_s_waitcnt(0x0f70);          // vmcnt(0): this wavefront's copies are in LDS
+      __syncthreads();
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < Tl::TN; ++j) any |= idx[j] == use;
+      if (!__ballot(any)) continue;
+      for (int s = 0; s < 2 && k0 + 32 * s < ad.rank; ++s) {
+        // chunk 4 s + g of a row; fragments start at multiples of 16 rows
+        const int pos = ((4 * s + g) ^ ((l16 >> 1) & 7)) * 16;
+        i32x4 b[Tl::TM];
+#pragma unroll
+        for (int i = 0; i < Tl::TM; ++i)
+          b[i] = *reinterpret_cast<const i32x4*>(lds_b + (wm * (Tl::BM / Tl::WM) + 16 * i + l16) * kStepBytes + pos);
+#pragma unroll
+        for (int j = 0; j < Tl::TN; ++j) {
+          const char* at = lds_u + (wn * (Tl::BN / Tl::WN) + 16 * j + l16) * kStepBytes + pos;
+          const i32x4 u[2] = {*reinterpret_cast<const i32x4*>(at), *reinterpret_cast<const i32x4*>(at + Tl::BN * kStepBytes)};
+#pragma unroll
+          for (int i = 0; i < Tl::TM; ++i) acc[i][j] = add_mine<AdaptersBf16>(idx[j] == use, b[i], u, acc[i][j]);
+        }
       }
     }
   }

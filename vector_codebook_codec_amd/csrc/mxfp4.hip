@@ -176,10 +176,7 @@ __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Ope
     }
   if (s0 < s1) Tl::run(acc, W, m0, X, n0, kchunks, s0, s1, tile_lds);
   if constexpr (Ad::kOn)
-    if (s0 == 0) {
-      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-      add_adapters_tile(acc, ad, m0 + (wave / Tl::WN) * (Tl::BM / Tl::WM), n0 + (wave % Tl::WN) * (Tl::BN / Tl::WN), X.rows, W.rows);
-    }
+    if (s0 == 0) add_adapters_tile<Tl>(acc, ad, m0, n0, X.rows, W.rows, tile_lds);
   if (!split) {
     store_tile<Tl, Out>(Y, ldy, n0, X.rows, m0, W.rows, acc, tile_lds);
     return;
@@ -223,6 +220,9 @@ __global__ __launch_bounds__(256) void mx4_sum_tail_kernel(const float* __restri
 // for one workgroup a CU, whose wavefronts take two or three units one after
 // another, loads and products of a unit in turn.
 // ---------------------------------------------------------------------------
+struct NoTokens {
+  __device__ __forceinline__ NoTokens(const Adapters&, int64_t, int64_t) {}
+};
 template <int RF, int TF, class In, class Out, bool kFused, class Ad>
 __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Operand Xq, const typename In::T* __restrict__ X,
                                                                 int d, int ldx_bytes, int kchunks,
@@ -242,6 +242,7 @@ __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Op
                                bsx = buffer_of(Xq.scale, kFused ? 0 : (uint32_t)(Xq.rows * Xq.scale_pitch));
   const int units = (kchunks + 15) / 16;
   f32x4 acc[RF][TF] = {};
+  std::conditional_t<Ad::kOn, TokenAdapters<TF>, NoTokens> own(ad, l16, Xq.rows);
   for (int u = wave; u < units; u += kThinWaves) {
     i32x4 w[4][RF], sc[RF], x[4][TF], sx[TF];
     // Loads return in order: the activations first, so that they are quantised
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Op
                                  (int)((uint32_t)sx[j][s] >> (8 * g)));
   }
   // the wavefronts take the tokens' adapters in turn, and their sums are added anyway
-  if constexpr (Ad::kOn) add_adapters<Ad>(acc, ad, m0 + l16, l16, Xq.rows, W.rows, wave, kThinWaves);
+  if constexpr (Ad::kOn) add_adapters<Ad, RF * TF == 1 ? 8 : 4>(acc, ad, own, m0 + l16, l16, Xq.rows, W.rows, wave, kThinWaves);
   thin_sum(acc, red);
   if (wave) return;
 #pragma unroll

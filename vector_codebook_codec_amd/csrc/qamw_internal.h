@@ -163,28 +163,31 @@ int launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t N
                           int64_t ldo, hipStream_t st);
 bool mx4_grid_fits(int64_t T, int64_t N, int64_t d);
 size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
-// Low-rank adapters beside the product (mx4_adapter.h): of U the rows are of
-// `pitch` elements, the rank rounded up to 32; in bf16 two such matrices.
-// B and U rows of whole 16-byte chunks are 16-byte aligned.
+// Low-rank adapters beside the product (mx4_adapter.h).  U = f_i A_i X has rows
+// of `pitch` elements, the rank rounded up to 32, and lies in the workspace as
+// `parts` fp32 matrices to be added (not yet times f_i), and for the product's
+// tiles also as two bf16 ones.  A and B are 16-byte aligned.
+constexpr int kMostAdapterParts = 4;
 struct Adapters {
-  const void *B, *U;
+  const void* B;
   const int32_t* index;            // [T]; outside [0, n): none
-  int n, rank, pitch;
-  const float* delta;              // the adapters' part of Y, rows of delta_pitch (where adapters_in_delta)
+  const float* factors;            // NULL: 1
+  int n, rank, pitch, parts;
+  float* u_parts;
+  uint16_t* u16;                   // where the tiles multiply U and B themselves
+  float* delta;                    // where adapters_in_delta: the adapters' part of Y, rows of delta_pitch
   int64_t delta_pitch;
 };
 bool adapters_in_delta(int64_t T, int64_t N, int32_t dt, int64_t rank);
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws,
                       const Adapters* ad, hipStream_t st);       // ad: of X's type, or NULL
-int64_t adapter_pitch(int64_t rank);
-size_t adapter_workspace_bytes(int64_t T, int64_t N, int32_t dt, int64_t rank);
-inline int64_t adapter_delta_pitch(int64_t N) { return (N + 3) / 4 * 4; }
-inline size_t adapter_u_bytes(int64_t T, int64_t rank) { return round_up((size_t)T * adapter_pitch(rank) * 4, 256); }
+size_t adapter_workspace_bytes(int64_t T, int64_t N, int64_t d, int32_t dt, int64_t rank);
 bool adapter_grid_fits(int64_t T, int64_t N, int64_t rank);
+// U of X into the workspace; completes ad
+int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t N, int64_t d, int64_t ldx, const void* A, void* ws,
+                          Adapters* ad, hipStream_t st);
 int launch_adapter_expand(int32_t dt, int64_t T, int64_t N, const Adapters& ad, hipStream_t st);
-int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t d, int64_t ldx, const void* A, const float* factors,
-                          const Adapters& ad, hipStream_t st);
 
 // ---- attention cache in microscaled 4 bits (cache.hip, cache_attention.hip)
 struct CacheShape {
