@@ -103,35 +103,43 @@ __device__ __forceinline__ f32x4 add_mine(bool mine, i32x4 b, const i32x4 (&u)[A
   for (int e = 0; e < 4; ++e) s[e] = mine ? s[e] : acc[e];
   return s;
 }
-// a lane's chunk of U from its parts, in a fixed order
+// a lane's chunk of U: its parts, read at once (those that are not there are
+// the last one again), then added in a fixed order
 template <class Ad>
-__device__ __forceinline__ void load_u(i32x4 (&u)[Ad::kTerms], const Adapters& ad, int64_t t, int64_t T, int k, float factor) {
-  constexpr int kQuads = Ad::kTerms == 1 ? 1 : 2;
-  f32x4 part[kMostAdapterParts][kQuads], s[kQuads] = {};
+struct ChunkOfU {
+  static constexpr int kQuads = Ad::kTerms == 1 ? 1 : 2;
+  f32x4 part[kMostAdapterParts][kQuads];
+  __device__ __forceinline__ void load(const Adapters& ad, int64_t t, int64_t T, int k) {
 #pragma unroll
-  for (int p = 0; p < kMostAdapterParts; ++p)      // all at once; those that are not there again the last one
+    for (int p = 0; p < kMostAdapterParts; ++p)
 #pragma unroll
-    for (int n = 0; n < kQuads; ++n)
-      part[p][n] = *reinterpret_cast<const f32x4*>(ad.u_parts + ((p < ad.parts ? p : ad.parts - 1) * T + t) * ad.pitch + k + 4 * n);
+      for (int n = 0; n < kQuads; ++n)
+        part[p][n] = *reinterpret_cast<const f32x4*>(ad.u_parts + ((p < ad.parts ? p : ad.parts - 1) * T + t) * ad.pitch + k + 4 * n);
+  }
+  __device__ __forceinline__ void add(i32x4 (&u)[Ad::kTerms], int parts, float factor) const {
+    f32x4 s[kQuads];
 #pragma unroll
-  for (int p = 0; p < kMostAdapterParts; ++p)
-    if (p < ad.parts)
+    for (int n = 0; n < kQuads; ++n) s[n] = part[0][n];
 #pragma unroll
-      for (int n = 0; n < kQuads; ++n) s[n] += part[p][n];
+    for (int p = 1; p < kMostAdapterParts; ++p)
+      if (p < parts)
 #pragma unroll
-  for (int n = 0; n < kQuads; ++n) s[n] *= factor;
-  if constexpr (kQuads == 1) {
-    u[0] = __builtin_bit_cast(i32x4, s[0]);
-  } else {
+        for (int n = 0; n < kQuads; ++n) s[n] += part[p][n];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float x0 = s[n / 2][2 * (n & 1)], x1 = s[n / 2][2 * (n & 1) + 1];
-      const uint32_t h = pack_bf16x2(x0, x1);
-      u[0][n] = (int)h;
-      u[1][n] = (int)pack_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+    for (int n = 0; n < kQuads; ++n) s[n] *= factor;
+    if constexpr (kQuads == 1) {
+      u[0] = __builtin_bit_cast(i32x4, s[0]);
+    } else {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float x0 = s[n / 2][2 * (n & 1)], x1 = s[n / 2][2 * (n & 1) + 1];
+        const uint32_t h = pack_bf16x2(x0, x1);
+        u[0][n] = (int)h;
+        u[1][n] = (int)pack_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+      }
     }
   }
-}
+};
 
 // The adapters and factors of a lane's tokens t + 16 j: read ahead of what
 // needs them.
@@ -157,11 +165,13 @@ __device__ __forceinline__ bool add_adapters(f32x4 (&acc)[TM][TN], const Adapter
   bool had = false;
   for (int k0 = 0; k0 < ad.pitch; k0 += Ad::kStep) {
     const int k = k0 + 16 / (int)sizeof(E) * g;    // below the pitch, a multiple of both steps
+    ChunkOfU<Ad> chunk[TN];
     i32x4 u[TN][Ad::kTerms];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) load_u<Ad>(u[j], ad, t + 16 * j < T ? t + 16 * j : T - 1, T, k, own.factor[j]);
+    for (int j = 0; j < TN; ++j) chunk[j].load(ad, t + 16 * j < T ? t + 16 * j : T - 1, T, k);
     AdapterWalk<TN, 16> walk(own.idx);
     int place = part;
+    bool ready = false;
     for (bool more = true; more;) {
       int use[kBatch];
       i32x4 b[kBatch][TM];
@@ -177,6 +187,11 @@ __device__ __forceinline__ bool add_adapters(f32x4 (&acc)[TM][TN], const Adapter
 #pragma unroll
           for (int i = 0; i < TM; ++i)
             b[x][i] = load_rank_chunk((const E*)ad.B + (int64_t)use[x] * N * ad.rank, m + 16 * i, N, k, ad.rank);
+      }
+      if (!ready) {                                // U's parts and the first rows of B are under way together
+        ready = true;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) chunk[j].add(u[j], ad.parts, own.factor[j]);
       }
 #pragma unroll
       for (int x = 0; x < kBatch; ++x)

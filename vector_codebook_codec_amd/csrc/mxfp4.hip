@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kThinThreads, 4) void mx4_thin_kernel(Operand W, Op
                                  (int)((uint32_t)sx[j][s] >> (8 * g)));
   }
   // the wavefronts take the tokens' adapters in turn, and their sums are added anyway
-  if constexpr (Ad::kOn) add_adapters<Ad, RF * TF == 1 ? 8 : 4>(acc, ad, own, m0 + l16, l16, Xq.rows, W.rows, wave, kThinWaves);
+  if constexpr (Ad::kOn) add_adapters<Ad, kFused ? 1 : 4>(acc, ad, own, m0 + l16, l16, Xq.rows, W.rows, wave, kThinWaves);
   thin_sum(acc, red);
   if (wave) return;
 #pragma unroll
