@@ -93,11 +93,11 @@ def _ints(t: torch.Tensor, name: str, dtype, *shape):
 
 def _one_device(first: torch.Tensor, **others) -> None:
     """Every tensor of a call lies on one device, the current one, whose stream the call goes to."""
-    index = first.device.index
+    index = first.get_device()
     if index != torch.cuda.current_device():
         raise ValueError("tensors must lie on the current device")
     for name, t in others.items():
-        if t is not None and t.device.index != index:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} lies on another device")
 
 

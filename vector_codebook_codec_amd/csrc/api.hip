@@ -754,9 +754,9 @@ static int check_head_rows(const void* p, int32_t dt, int64_t T, int64_t heads, 
   }
   return QAMW_OK;
 }
-static int check_slots(const int64_t* slots, int64_t T) {
+static int check_slots(const int64_t* slots, int64_t T, int64_t heads) {
   if (T < 0) return fail(QAMW_EINVAL, "T must not be negative (T=%lld)", (long long)T);
-  if (T > kMaxRows) return fail(QAMW_EUNSUPPORTED, "too many tokens (T=%lld)", (long long)T);
+  if (T > kMaxRows / 2 / heads) return fail(QAMW_EUNSUPPORTED, "too many tokens (T=%lld)", (long long)T);
   if (T && (!slots || ((uintptr_t)slots & 7u))) return fail(QAMW_EINVAL, "slots must be non-NULL and 8-byte aligned");
   return QAMW_OK;
 }
@@ -766,7 +766,7 @@ int32_t qamw_mxfp4_cache_write(const void* K, const void* V, int32_t dtype, int6
                                uint8_t* codes, uint8_t* scales, int64_t pages, int64_t page, void* stream) {
   CacheShape c;
   int rc = check_cache(codes, scales, pages, heads, page, d, &c);
-  if (rc || (rc = check_slots(slots, T)) || (rc = check_head_rows(K, dtype, T, heads, d, k_token, k_head, "K", false)) ||
+  if (rc || (rc = check_slots(slots, T, heads)) || (rc = check_head_rows(K, dtype, T, heads, d, k_token, k_head, "K", false)) ||
       (rc = check_head_rows(V, dtype, T, heads, d, v_token, v_head, "V", false)))
     return rc;
   if (T == 0 || pages == 0) return QAMW_OK;
@@ -778,7 +778,7 @@ int32_t qamw_mxfp4_cache_read(const uint8_t* codes, const uint8_t* scales, int64
                               int64_t k_head, int64_t v_token, int64_t v_head, void* stream) {
   CacheShape c;
   int rc = check_cache(codes, scales, pages, heads, page, d, &c);
-  if (rc || (rc = check_slots(slots, T)) ||
+  if (rc || (rc = check_slots(slots, T, heads)) ||
       (rc = check_head_rows(K, dtype, K ? T : 0, heads, d, k_token, k_head, "K", true)) ||
       (rc = check_head_rows(V, dtype, V ? T : 0, heads, d, v_token, v_head, "V", true)))
     return rc;

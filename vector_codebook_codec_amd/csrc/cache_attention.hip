@@ -7,7 +7,6 @@
 #include <hip/hip_runtime.h>
 
 #include <float.h>
-#include <stdlib.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -336,7 +335,7 @@ __device__ __forceinline__ void store_elements(int32_t dt, void* row, int j, int
 }
 
 // floats of a share's partial result: sums, then the reference exponent and the sum of weights of each row
-template <int DB, int RT, int kTerms> constexpr int attn_waves() { return RT == 4 ? 1 : DB == 8 || RT == 2 ? 2 : 3; }
+template <int DB, int RT, int kTerms> constexpr int attn_waves() { return DB == 8 || RT == 2 || kTerms == 3 ? 2 : 3; }
 template <int DB, int RT> constexpr int part_floats() { return 16 * RT * (32 * DB + 2); }
 
 // ---------------------------------------------------------------------------
@@ -599,10 +598,9 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 //   * Values are decoded once a workgroup, each wavefront 32 tokens, into LDS
 //     in the layout of the matrix operand, two tiles in turn: one barrier a tile.
 // ---------------------------------------------------------------------------
-template <int DB>
 __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(AttentionArgs a, int row_tiles, int splits,
                                                                                 float* __restrict__ part) {
-  constexpr int RT = 2, MT = 2 * DB, kWaveRows = 16 * RT, kRows = kAttnWaves * kWaveRows;
+  constexpr int DB = 4, RT = 2, MT = 2 * DB, kWaveRows = 16 * RT, kRows = kAttnWaves * kWaveRows;
   __shared__ __align__(16) i32x4 staged[2][kAttnWaves][MT][kWave];
   __shared__ __align__(16) i32x4 staged_bad[2][kAttnWaves][kWave];
   __shared__ int staged_nan[2][kAttnWaves];
@@ -882,10 +880,19 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_join_kernel(Atte
   for (int x = 1; x < kWave; x *= 2) sum += __shfl_xor(sum, x);
   constexpr int E = DB / 2;                        // elements of a lane
   float acc[E] = {};
-  for (int s = 0; s < range.shares; ++s) {
-    const float fs = __shfl(f, s);
+  for (int s0 = 0; s0 < range.shares; s0 += 8) {   // eight shares' rows in flight; past the last one that again, not added
+    float v[8][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += fs * p[s * floats + at * 32 * DB + E * lane + e];
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[s][e] = p[min(s0 + s, range.shares - 1) * floats + at * 32 * DB + E * lane + e];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float fs = __shfl(f, min(s0 + s, range.shares - 1));
+      if (s0 + s < range.shares)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += fs * v[s][e];
+    }
   }
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   void* to = row_at(a.out, a.odt, query * a.o_token + head * a.o_head);
@@ -905,12 +912,35 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_join_kernel(Atte
 static int head_blocks(int64_t d) { return d <= 64 ? 2 : d <= 128 ? 4 : 8; }
 static int dtype_terms(int32_t dt) { return dt == QAMW_F32 ? 3 : dt == QAMW_F16 ? 2 : 1; }
 
+// Fragments of 16 query rows a workgroup takes.  8 is the kernel of many rows:
+// heads of 65 to 128 elements in bf16, from 1024 rows a key head on, where its
+// 128 rows a workgroup leave enough workgroups (8 sequences of 4096 tokens, 32/8
+// heads of 128: 1024 rows 134 us against 152 us with 2 fragments, 512 rows 99 us
+// and 91 us; heads of 64 fill half its instructions: 8192 rows 1080 us and 1050
+// us).  2 fragments share the decoding (256 rows 52 us, with 1 fragment 60 us;
+// 64 rows 28 and 30 us, in one sequence of 8192 tokens 19 and 17 us); their
+// registers allow them for bf16 and heads of up to 128 elements.
 static int row_fragments(int64_t rows, int db, int terms) {
-  const int lim = getenv("RTMIN") ? atoi(getenv("RTMIN")) : 64;
-  const int lim2 = getenv("RT2MIN") ? atoi(getenv("RT2MIN")) : 64;
-  if (terms == 1 && db <= 4 && rows > lim) return 8;
-  if (terms == 1 && db <= 4 && rows > lim2) return 2;
-  return 1;
+  if (terms > 1 || db == 8 || rows <= 128) return 1;
+  return db == 4 && rows > 768 ? 8 : 2;
+}
+
+// Into how many shares the tokens of an item go: rounds of workgroups (two a
+// CU: more of them at a time read no faster) times the tiles of a share, and
+// what joining costs.  Times of a tile of 128 tokens in a round, microseconds;
+// an item of up to 12 tiles in one share takes no longer than two launches (1
+// sequence of 1000 tokens, 32 heads: 11.1 us against 10.7 us in 8 shares).  No
+// share is longer than 96 tiles, however many items there are: they may be uneven.
+static int shares_of(int64_t items, int64_t tiles, int rows) {
+  if (tiles <= 12) return 1;
+  const double tile_us = rows == 16 ? 0.65 : rows == 32 ? 0.9 : 2.7;
+  double best_us = 1e30;
+  int best = 1;
+  for (int64_t s = tiles_of(tiles, 96); s <= kMaxSplits && s <= tiles / 2; ++s) {
+    const double us = (double)tiles_of(items * s, 2 * kCus) * (double)tiles_of(tiles, s) * tile_us + (s > 1 ? 5.0 + 0.1 * (double)s : 0.0);
+    if (us < 0.97 * best_us) best_us = us, best = (int)s;
+  }
+  return tiles_of(tiles, 96) > kMaxSplits ? kMaxSplits : best;
 }
 
 AttentionPlan attention_plan(int64_t T, int64_t sequences, int64_t max_queries, int64_t heads, int64_t group, int64_t d,
@@ -921,7 +951,7 @@ AttentionPlan attention_plan(int64_t T, int64_t sequences, int64_t max_queries, 
   p.rows = 16 * row_fragments(most_rows, db, terms);
   p.row_tiles = (int)std::min<int64_t>(tiles_of(most_rows, p.rows), INT32_MAX);
   const int64_t items = sequences * heads * p.row_tiles, tiles = std::max<int64_t>(tiles_of(tokens, kTileTokens), 1);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({tiles_of(4 * kCus, std::max<int64_t>(items, 1)), tiles, kMaxSplits}));
+  p.splits = shares_of(items, tiles, p.rows);
   p.groups = items * p.splits;
   p.bytes = p.splits > 1 ? (size_t)p.groups * p.rows * (32 * db + 2) * sizeof(float) : 0;
   return p;
@@ -941,18 +971,19 @@ static int attention_as(const AttentionArgs& a, const AttentionPlan& p, float* p
   const int rc = check_launch("cache_attention_kernel");
   return rc ? rc : join_shares<DB>(a, p, part, st);
 }
-template <int DB>
 static int attention_chunk(const AttentionArgs& a, const AttentionPlan& p, float* part, hipStream_t st) {
-  hipLaunchKernelGGL((cache_attention_chunk_kernel<DB>), dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a, p.row_tiles,
+  hipLaunchKernelGGL(cache_attention_chunk_kernel, dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a, p.row_tiles,
                      p.splits, part);
   const int rc = check_launch("cache_attention_chunk_kernel");
-  return rc ? rc : join_shares<DB>(a, p, part, st);
+  return rc ? rc : join_shares<4>(a, p, part, st);
 }
 template <int DB>
 static int attention_of(const AttentionArgs& a, const AttentionPlan& p, float* part, hipStream_t st) {
   const int terms = std::max(dtype_terms(a.qdt), dtype_terms(a.odt));
-  if constexpr (DB <= 4) if (p.rows == 128) return attention_chunk<DB>(a, p, part, st);
-  if (p.rows == 32) return attention_as<DB, 2, 1>(a, p, part, st);
+  if constexpr (DB == 4)
+    if (p.rows == 128) return attention_chunk(a, p, part, st);
+  if constexpr (DB <= 4)
+    if (p.rows == 32) return attention_as<DB, 2, 1>(a, p, part, st);
   if (terms == 3) return attention_as<DB, 1, 3>(a, p, part, st);
   if (terms == 2) return attention_as<DB, 1, 2>(a, p, part, st);
   return attention_as<DB, 1, 1>(a, p, part, st);
