@@ -512,12 +512,14 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
  *   out      [T][q_heads][d] of odtype, lse [T][q_heads] float32 or NULL.  Rows
  *            of queries that belong to no sequence are left as they were.
  *   scale    positive and finite
- * Arithmetic: keys and values as they stand; bf16 queries as they stand, fp16
- * and fp32 ones as 2 and 3 bf16 numbers (16 and 24 bits).  Products are summed
- * in fp32, statistics are fp32.  Each weight is rounded once before it
- * multiplies a value: by up to 2^-8 of itself where Q and out are bf16, 2^-16
- * where one is fp16, 2^-24 where one is fp32.  out is rounded once.  Sums have
- * a fixed order for given sizes.
+ * Arithmetic: keys and values as they stand, queries too (bf16 ones of many
+ * rows and heads of 65 to 128 elements as two 8-bit numbers that hold them to
+ * 2^-22 of a row's largest element, their scores then to 2^-16 of scale sum |q
+ * k|; fp32 ones to 24 bits).  Products are summed in fp32, statistics are fp32.
+ * Each weight is rounded once before it multiplies a value: by up to 2^-16 of
+ * itself, 2^-24 where Q or out is fp32, and for bf16 and many rows 2^-11 of
+ * itself or 2^-25 of the row's largest.  out is rounded once.  Sums have a
+ * fixed order for given sizes.  Scores beyond fp32's range are not supported.
  *   T q_heads / heads and table_cols page up to 2^30
  *   workspace >= qamw_mxfp4_cache_attention_workspace_bytes(..., table_cols
  *             page, ...), 256-byte aligned; may be NULL where that is 0

@@ -51,14 +51,14 @@ def read(codes, scales, slots, d: int):
 
 
 def attention(Q, codes, scales, table, lengths, starts, scale, causal=True, window=0):
-    """(out, lse, weighted) [T][q_heads]...: weighted is sum_t p_t |v_t|, the scale of the errors of out.
-    Rows of no sequence are NaN in all three."""
+    """(out, lse, weighted, plain) [T][q_heads]...: weighted is sum_t p_t |v_t| and plain sum_t |v_t|, the scales of
+    the errors of out.  Rows of no sequence are NaN in all of them."""
     Q = np.asarray(Q, dtype=np.float64)
     T, q_heads, d = Q.shape
     _, pages, heads, page, _ = codes.shape
     group = q_heads // heads
     out, lse = np.full(Q.shape, np.nan), np.full(Q.shape[:2], np.nan)
-    weighted = np.full(Q.shape, np.nan)
+    weighted, plain = np.full(Q.shape, np.nan), np.full(Q.shape, np.nan)
     for b, length in enumerate(lengths):
         n = int(starts[b + 1]) - int(starts[b])
         if n <= 0:
@@ -82,7 +82,7 @@ def attention(Q, codes, scales, table, lengths, starts, scale, causal=True, wind
                 row = starts[b] + i
                 for j in range(h * group, (h + 1) * group):
                     if not sees.any():
-                        out[row, j], lse[row, j], weighted[row, j] = 0.0, -np.inf, 0.0
+                        out[row, j], lse[row, j], weighted[row, j], plain[row, j] = 0.0, -np.inf, 0.0, 0.0
                         continue
                     z = k[sees] @ Q[row, j] * scale
                     m = z.max()
@@ -91,5 +91,5 @@ def attention(Q, codes, scales, table, lengths, starts, scale, causal=True, wind
                     p = p / p.sum()
                     # NaN times a weight, even one that has gone to 0, is NaN
                     out[row, j] = p @ v[sees]
-                    weighted[row, j] = p @ np.abs(v[sees])
-    return out, lse, weighted
+                    weighted[row, j], plain[row, j] = p @ np.abs(v[sees]), np.abs(v[sees]).sum(axis=0)
+    return out, lse, weighted, plain

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mx4_device.h"
 #include "qamw.h"
@@ -82,13 +83,27 @@ __device__ __forceinline__ void* row_at(const void* p, int32_t dt, int64_t eleme
   return (char*)const_cast<void*>(p) + element * (dt == QAMW_F32 ? 4 : 2);
 }
 
-// the 8 four-bit elements of w times the scale, as bf16 (exact)
-__device__ __forceinline__ void decode_bf16(uint32_t w, float s, uint32_t (&o)[4]) {
-  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+// the 8 four-bit elements of w times the scale, as bf16 (exact) or fp16 (exact
+// where f16_holds)
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+template <bool kF16>
+__device__ __forceinline__ void decode_16(uint32_t w, float s, uint32_t (&o)[4]) {
+  if constexpr (kF16) {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
+  } else {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  }
 }
+// Scale codes whose blocks fp16 holds as normal numbers: 2^e / 2 to 6 2^e with e
+// in [-13, 13]; a code of 0 with the zeros that have it.
+__device__ __forceinline__ bool f16_holds(uint32_t code) { return code - 114u <= 26u || code == 0u; }
 // x as a sum of kTerms bf16 numbers: 8, 16 or 24 bits of it
 template <int kTerms>
 __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t (&o)[kTerms]) {
@@ -97,6 +112,9 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t (&o)[k
     o[t] = pack_bf16x2(x0, x1);
     if (t + 1 < kTerms) x0 -= __uint_as_float(o[t] << 16), x1 -= __uint_as_float(o[t] & 0xffff0000u);
   }
+}
+__device__ __forceinline__ f32x4 mfma_f16(i32x4 a, i32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 __device__ __forceinline__ f32x4 mfma_bf16(i32x4 a, i32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -223,15 +241,15 @@ __device__ __forceinline__ bool any_nan(const uint32_t (&vc)[8]) {
   for (int e = 1; e < 8; ++e) most = max(most, vc[e]);
   return __ballot(most == 255u) != 0;
 }
-// The operands V^T: put(t, f) for the t-th element of every lane.  Pairs of
-// tokens are put together by byte permutes.
-template <int DB, class Put>
+// The operands V^T, in fp16 or bf16: put(t, f) for the t-th element of every
+// lane.  Pairs of tokens are put together by byte permutes.
+template <int DB, bool kF16, class Put>
 __device__ __forceinline__ void decode_values(const uint32_t (&vc)[8], const uint32_t (&vw)[8][RawValues<DB>::VW], Put&& put) {
 #pragma unroll
   for (int n = 0; n < RawValues<DB>::VW; ++n) {
     uint32_t d[8][4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) decode_bf16(vw[e][n], __uint_as_float(vc[e] << 23), d[e]);
+    for (int e = 0; e < 8; ++e) decode_16<kF16>(vw[e][n], __uint_as_float(vc[e] << 23), d[e]);
 #pragma unroll
     for (int x = 0; x < (DB == 2 ? 2 : 4); ++x) {
       i32x4 even, odd;
@@ -274,10 +292,9 @@ __device__ __forceinline__ void follow_maximum(const f32x4 (&s)[RT][2], float c,
     for (int t = 0; t < MT; ++t) o[j][t] *= f;
   }
 }
-// the weights 2^(s c - m) as operands P, and their sums
-template <int RT, int kTerms>
-__device__ __forceinline__ void weights(const f32x4 (&s)[RT][2], float c, const float (&m)[RT], float (&l)[RT],
-                                        i32x4 (&p)[RT][kTerms]) {
+// the weights 2^(s c - m), put(row fragment, word of the operand P, two weights), and their sums
+template <int RT, class Put>
+__device__ __forceinline__ void weights(const f32x4 (&s)[RT][2], float c, const float (&m)[RT], float (&l)[RT], Put&& put) {
 #pragma unroll
   for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -287,10 +304,7 @@ __device__ __forceinline__ void weights(const f32x4 (&s)[RT][2], float c, const 
         const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i][e], c, -m[j])),
                     p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i][e + 1], c, -m[j]));
         l[j] += p0 + p1;
-        uint32_t t[kTerms];
-        split_bf16x2<kTerms>(p0, p1, t);
-#pragma unroll
-        for (int n = 0; n < kTerms; ++n) p[j][n][2 * i + e / 2] = (int)t[n];
+        put(j, 2 * i + e / 2, p0, p1);
       }
 }
 // Blocks that are NaN must reach the rows that see their token and no others,
@@ -353,15 +367,17 @@ template <int DB, int RT> constexpr int part_floats() { return 16 * RT * (32 * D
 //     the same 8 tokens, and the m-th instruction multiplies the m-th element
 //     of every lane.
 //
-// kTerms: q and the weights p are sums of that many bf16 numbers: 1 for bf16
-// in and out (p rounded by at most 2^-8 of itself, each weight on its own; as
-// much as the output's own rounding), 2 where fp16 and 3 where fp32 takes part
-// (p to 2^-16 and 2^-24).  Sums are fp32 throughout.
+// kTerms: q is a sum of that many bf16 numbers: 1 for bf16 in and out, 2 where
+// fp16 and 3 where fp32 takes part; the weights are 2, 2 and 3 of them (each
+// rounded by at most 2^-16 or 2^-24 of itself; as one number, by 2^-8, the
+// error of a bf16 output grew from 0.0016 to 0.0024 in the root mean square).
+// Sums are fp32 throughout.
 // ---------------------------------------------------------------------------
 template <int DB, int RT, int kTerms>
 __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void cache_attention_kernel(AttentionArgs a, int row_tiles, int splits,
                                                                        float* __restrict__ part) {
   constexpr int MT = 2 * DB;                       // matrix instructions along the head
+  constexpr int kWeightTerms = kTerms == 3 ? 3 : 2;
   constexpr int LD = 32 * DB + 4;                  // LDS row, off the banks' period
   __shared__ __align__(16) float joined[kAttnWaves * 16 * LD];
   __shared__ float stats[2][kAttnWaves][16];
@@ -466,7 +482,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t kd[4];
-        decode_bf16(r.k[i][w], __uint_as_float((DB == 8 && w < 4 ? r.ks[i] & 255u : DB == 8 ? r.ks[i] >> 8 : r.ks[i]) << 23), kd);
+        decode_16<false>(r.k[i][w], __uint_as_float((DB == 8 && w < 4 ? r.ks[i] & 255u : DB == 8 ? r.ks[i] >> 8 : r.ks[i]) << 23), kd);
         const i32x4 kf = {(int)kd[0], (int)kd[1], (int)kd[2], (int)kd[3]};
 #pragma unroll
         for (int j = 0; j < RT; ++j)
@@ -490,19 +506,24 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
             if (!sees(j, i, e)) s[j][i][e] = -INFINITY;
     }
     follow_maximum<RT, MT>(s, c, m, l, o);
-    i32x4 p[RT][kTerms];
-    weights<RT, kTerms>(s, c, m, l, p);
+    i32x4 p[RT][kWeightTerms];
+    weights<RT>(s, c, m, l, [&](int j, int at, float p0, float p1) __attribute__((always_inline)) {
+      uint32_t t[kWeightTerms];
+      split_bf16x2<kWeightTerms>(p0, p1, t);
+#pragma unroll
+      for (int n = 0; n < kWeightTerms; ++n) p[j][n][at] = (int)t[n];
+    });
     uint32_t vc[8], vw[8][RawValues<DB>::VW];
     r.v.take(vc, vw, l16);
     if (!whole) {                                  // rows may see different tokens
       clear_unseen<DB>(vc, vw, t0 + 4 * g, lo_any, hi_any, r.page_ok);
       if (any_nan(vc)) spread_nan<RT, MT>(take_nan<DB>(vc, vw), sees, o);
     }
-    decode_values<DB>(vc, vw, [&](int t, i32x4 f) __attribute__((always_inline)) {
+    decode_values<DB, false>(vc, vw, [&](int t, i32x4 f) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < RT; ++j)
 #pragma unroll
-        for (int n = 0; n < kTerms; ++n) o[j][t] = mfma_bf16(f, p[j][n], o[j][t]);
+        for (int n = 0; n < kWeightTerms; ++n) o[j][t] = mfma_bf16(f, p[j][n], o[j][t]);
     });
   };
 
@@ -593,19 +614,34 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 //     number holds it to within half a step, the second (with a scale 2^-5 of
 //     the first's) the rest: a bf16 number's 8 bits exactly, down to elements
 //     2^-14 of the largest, and below that 2^-22 of the largest.
-//     Such an instruction takes 33 cycles, as long as the two bf16 ones that
-//     it saves (measured, 16 x 16 x 128 against two terms of 16 x 16 x 32).
+//     Such an instruction takes 33 cycles, half the time of the four bf16 ones
+//     it stands for (measured); two take as long as they.  It sums 128 products cut off
+//     below 24 bits of the largest: scores are within 2^-16 of scale sum |q k|
+//     (lse of rows around 10: off by 6e-6 in the root mean square, 2.6e-4 at
+//     most seen, against 3e-7 from bf16 products).
 //   * Values are decoded once a workgroup, each wavefront 32 tokens, into LDS
-//     in the layout of the matrix operand, two tiles in turn: one barrier a tile.
+//     in the layout of the matrix operand, two tiles in turn: one barrier a
+//     tile.  They and the weights go in fp16, which rounds a weight by at most
+//     2^-11 of itself (2^-25 of the row's reference where it is below 2^-14 of
+//     it); the results of a workgroup that met a value beyond fp16 (or a
+//     NaN block) are dropped, and a second launch does its work with values in
+//     bf16 and the weights as two bf16 numbers.
 // ---------------------------------------------------------------------------
+template <bool kF16>
 __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(AttentionArgs a, int row_tiles, int splits,
-                                                                                float* __restrict__ part) {
+                                                                                float* __restrict__ part, int* __restrict__ redo) {
   constexpr int DB = 4, RT = 2, MT = 2 * DB, kWaveRows = 16 * RT, kRows = kAttnWaves * kWaveRows;
   __shared__ __align__(16) i32x4 staged[2][kAttnWaves][MT][kWave];
   __shared__ __align__(16) i32x4 staged_bad[2][kAttnWaves][kWave];
-  __shared__ int staged_nan[2][kAttnWaves];
+  __shared__ int staged_nan[2][kAttnWaves], unfit;
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if constexpr (kF16) {
+    if (threadIdx.x == 0) redo[blockIdx.x] = 0, unfit = 0;
+    __syncthreads();
+  } else if (!redo[blockIdx.x]) {
+    return;
+  }
   const Place at = place_of(a, row_tiles, splits);
   const int h = at.h;
   const Sequence seq = sequence_of(a, at.b);
@@ -716,10 +752,17 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
     raw.take(vc, vw, l16);
     if (t0 < lo_group || t0 + kWaveTokens > hi_group || !raw_ok[0] || !raw_ok[1])
       clear_unseen<DB>(vc, vw, t0 + 4 * g, lo_group, hi_group, raw_ok);
-    const bool nan = any_nan(vc);
-    if (nan) staged_bad[k & 1][wave][lane] = take_nan<DB>(vc, vw);
-    if (lane == 0) staged_nan[k & 1][wave] = nan;
-    decode_values<DB>(vc, vw, [&](int t, i32x4 f) __attribute__((always_inline)) { staged[k & 1][wave][t][lane] = f; });
+    if constexpr (kF16) {
+      bool fits = true;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) fits &= f16_holds(vc[e]);
+      if (!fits) unfit = 1;
+    } else {
+      const bool nan = any_nan(vc);
+      if (nan) staged_bad[k & 1][wave][lane] = take_nan<DB>(vc, vw);
+      if (lane == 0) staged_nan[k & 1][wave] = nan;
+    }
+    decode_values<DB, kF16>(vc, vw, [&](int t, i32x4 f) __attribute__((always_inline)) { staged[k & 1][wave][t][lane] = f; });
   };
 
   const float c = a.scale * kLog2e;
@@ -754,17 +797,30 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
     }
     follow_maximum<RT, MT>(s, c, m, l, o);
     // the values are on their way from LDS while the weights are made
-    i32x4 v[MT];
+    constexpr int kWeightTerms = kF16 ? 1 : 2;
+    i32x4 v[MT], p[RT][kWeightTerms];
 #pragma unroll
     for (int t = 0; t < MT; ++t) v[t] = staged[k & 1][sub][t][lane];
     __builtin_amdgcn_sched_barrier(0);
-    i32x4 p[RT][1];
-    weights<RT, 1>(s, c, m, l, p);
-    if (__builtin_amdgcn_readfirstlane(staged_nan[k & 1][sub])) spread_nan<RT, MT>(staged_bad[k & 1][sub][lane], sees, o);
+    weights<RT>(s, c, m, l, [&](int j, int at, float p0, float p1) __attribute__((always_inline)) {
+      if constexpr (kF16) {
+        const f32x2_t both = {p0, p1};
+        p[j][0][at] = __builtin_bit_cast(int, __builtin_convertvector(both, f16x2_t));
+      } else {
+        uint32_t t[2];
+        split_bf16x2<2>(p0, p1, t);
+        p[j][0][at] = (int)t[0], p[j][kWeightTerms - 1][at] = (int)t[1];
+      }
+    });
+    if constexpr (!kF16)
+      if (__builtin_amdgcn_readfirstlane(staged_nan[k & 1][sub])) spread_nan<RT, MT>(staged_bad[k & 1][sub][lane], sees, o);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) o[j][t] = mfma_bf16(v[t], p[j][0], o[j][t]);
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int n = 0; n < kWeightTerms; ++n)
+          o[j][t] = kF16 ? mfma_f16(v[t], p[j][n], o[j][t]) : mfma_bf16(v[t], p[j][n], o[j][t]);
   };
 
   if (k0 < k1) {
@@ -802,6 +858,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
       __syncthreads();
     }
   }
+
+  // The last barrier has passed, nobody sets the flag any more.  (Looked at
+  // inside the loop it makes the compiler spill: 620 us became 850.)
+  if constexpr (kF16)
+    if (unfit) {
+      if (threadIdx.x == 0) redo[blockIdx.x] = 1;
+      return;
+    }
 
   // ---- results: lane l has row l % 16 and elements MT (4 (l / 16) + e) + t
 #pragma unroll
@@ -954,6 +1018,7 @@ AttentionPlan attention_plan(int64_t T, int64_t sequences, int64_t max_queries, 
   p.splits = shares_of(items, tiles, p.rows);
   p.groups = items * p.splits;
   p.bytes = p.splits > 1 ? (size_t)p.groups * p.rows * (32 * db + 2) * sizeof(float) : 0;
+  if (p.rows == 128) p.bytes += (size_t)p.groups * sizeof(int);        // which workgroups gave fp16 up
   return p;
 }
 
@@ -972,9 +1037,14 @@ static int attention_as(const AttentionArgs& a, const AttentionPlan& p, float* p
   return rc ? rc : join_shares<DB>(a, p, part, st);
 }
 static int attention_chunk(const AttentionArgs& a, const AttentionPlan& p, float* part, hipStream_t st) {
-  hipLaunchKernelGGL(cache_attention_chunk_kernel, dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a, p.row_tiles,
-                     p.splits, part);
-  const int rc = check_launch("cache_attention_chunk_kernel");
+  int* redo = (int*)((char*)part + p.bytes) - p.groups;
+  hipLaunchKernelGGL(cache_attention_chunk_kernel<true>, dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a, p.row_tiles,
+                     p.splits, part, redo);
+  int rc = check_launch("cache_attention_chunk_kernel");
+  if (rc) return rc;
+  hipLaunchKernelGGL(cache_attention_chunk_kernel<false>, dim3((unsigned)p.groups), dim3(kAttnThreads), 0, st, a, p.row_tiles,
+                     p.splits, part, redo);
+  rc = check_launch("cache_attention_chunk_kernel");
   return rc ? rc : join_shares<4>(a, p, part, st);
 }
 template <int DB>
