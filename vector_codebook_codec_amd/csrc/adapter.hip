@@ -155,6 +155,18 @@ __global__ __launch_bounds__(kBlockThreads) void adapter_round_kernel(Adapters a
   }
 }
 
+// B with rows of `pitch` elements, filled up with 0: ranks that are not whole
+// 16-byte chunks, for the product's tiles.  8 elements a lane.
+__global__ __launch_bounds__(kBlockThreads) void adapter_pad_kernel(const uint16_t* __restrict__ B, int64_t rows, int rank, int pitch,
+                                                                    uint16_t* __restrict__ padded) {
+  const int chunks = pitch / 8;
+  for (int64_t i = (int64_t)blockIdx.x * kBlockThreads + threadIdx.x; i < rows * chunks; i += (int64_t)gridDim.x * kBlockThreads) {
+    const int64_t row = i / chunks;
+    const int k = (int)(i - row * chunks) * 8;
+    *reinterpret_cast<i32x4*>(padded + 8 * i) = load_chunk(B + row * rank, k, rank);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // The adapters' part of Y in fp32: a workgroup takes 16 tokens by 32 channels,
 // its wavefronts every fourth adapter of these tokens each.  A token has one
@@ -191,16 +203,17 @@ static int adapter_parts(int64_t T, int64_t d, int64_t rank) {
   const int64_t items = T <= 256 ? tiles_of(T, 16) * 16 : tiles_of(T, 64) * tiles_of(rank, 64);
   return (int)std::max<int64_t>(1, std::min<int64_t>({kMostAdapterParts, steps / 16, tiles_of(2 * kCus, items)}));
 }
-// U's parts, then U in bf16 or the adapters' part of Y
+// U's parts, U in bf16, the adapters' part of Y or B filled up
 struct AdapterLayout {
   int parts;
-  size_t second, bytes;
+  size_t second, third, bytes;
 };
 static AdapterLayout adapter_layout(int64_t T, int64_t N, int64_t d, int32_t dt, int64_t rank) {
   AdapterLayout p;
   p.parts = adapter_parts(T, d, rank);
   p.second = round_up((size_t)p.parts * T * adapter_pitch(rank) * sizeof(float), 256);
-  p.bytes = p.second + (adapters_in_delta(T, N, dt, rank) ? (size_t)T * adapter_delta_pitch(N) : (size_t)T * adapter_pitch(rank)) * 4;
+  p.third = p.second + round_up((size_t)T * adapter_pitch(rank) * 4, 256);
+  p.bytes = adapters_in_delta(T, N, dt, rank) ? p.third + (size_t)T * adapter_delta_pitch(N) * 4 : p.third;
   return p;
 }
 size_t adapter_workspace_bytes(int64_t T, int64_t N, int64_t d, int32_t dt, int64_t rank) {
@@ -237,7 +250,7 @@ int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t N, int6
   ad->parts = p.parts;
   ad->u_parts = (float*)ws;
   ad->u16 = (uint16_t*)((char*)ws + p.second);
-  ad->delta = (float*)((char*)ws + p.second);
+  ad->delta = (float*)((char*)ws + p.third);
   ad->delta_pitch = adapter_delta_pitch(N);
   int rc;
   if (xdt == QAMW_F32) {
@@ -250,9 +263,19 @@ int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t N, int6
   } else {
     rc = shrink_of<AdaptersBf16>(X, T, d, ldx, A, *ad, st);
   }
-  if (rc || in_delta || T <= 256) return rc;
+  // Many tokens and a rank of no whole chunks: where B filled up is smaller than the adapters' part of Y would be, it
+  // takes that one's place and the tiles multiply it (4000 x 11008 x 4096, 4 adapters of rank 20).
+  const bool pad = in_delta && xdt == QAMW_BF16 && T > 256 && (int64_t)ad->n * ad->pitch <= 2 * T;
+  if (!rc && pad) {
+    const int64_t rows = (int64_t)ad->n * N;
+    hipLaunchKernelGGL(adapter_pad_kernel, dim3((unsigned)std::min<int64_t>(tiles_of(rows * (ad->pitch / 8), kBlockThreads), 1 << 16)),
+                       dim3(kBlockThreads), 0, st, (const uint16_t*)ad->B, rows, ad->rank, ad->pitch, (uint16_t*)ad->delta);
+    rc = check_launch("adapter_pad_kernel");
+  }
+  if (rc || (in_delta && !pad) || T <= 256) return rc;
   hipLaunchKernelGGL(adapter_round_kernel, dim3((unsigned)std::min<int64_t>(tiles_of(T * ad->pitch / 4, kBlockThreads), 1 << 16)),
                      dim3(kBlockThreads), 0, st, *ad, T);
+  if (pad) ad->B = ad->delta, ad->rank = ad->pitch;            // from here on a rank of whole chunks
   return check_launch("adapter_round_kernel");
 }
 
