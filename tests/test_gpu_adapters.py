@@ -230,3 +230,20 @@ def test_serving_step(q):
     assert np.linalg.norm(host(out) - o) <= 1e-5 * np.linalg.norm(o)
     y, _ = M.matmul(host(out).reshape(T, -1), *h[1])
     assert np.linalg.norm(host(Y) - y) <= 1e-5 * np.linalg.norm(y)
+
+
+@pytest.mark.parametrize("T", [3, 60, 400])
+def test_on_another_stream(q, T):
+    """Results and workspaces of calls on a stream that is not the current one, which is busy."""
+    say(f"case stream T={T}")
+    rng, X, codes, scales, A, B, f = make(q, T, 520, 256, 16, 6, "bf16", T)
+    index = torch.from_numpy(choose(rng, T, 6, "each")).to(DEV)
+    want = q.qamw_mxfp4_adapter_matmul(X, codes, scales, A, B, index, f).clone()
+    a = torch.ones(4096, 4096, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a @ a
+    got = [q.qamw_mxfp4_adapter_matmul(X, codes, scales, A, B, index, f, stream=s) for s in (side, side.cuda_stream)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)

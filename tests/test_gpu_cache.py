@@ -484,3 +484,25 @@ def test_on_another_stream(q, n):
     torch.cuda.synchronize()
     for r in (got, again):
         assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1])
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_offsets_past_32_bits(q, n):
+    """Pages more than 4 GiB from the start of either half of the cache."""
+    say(f"case large cache n={n}")
+    heads, d, page, length = 8, 128, 64, 500
+    Q, codes, scales, table, lengths, starts = simple(q, n=n, length=length, heads=heads, group=4, d=d, page=page, seqs=1)
+    want = q.qamw_mxfp4_cache_attention(Q, codes, scales, table, lengths, starts, n)
+    t = torch.arange(length, device=DEV)
+    old = table[0, t // page].long() * page + t % page
+    pages = 140000
+    far = torch.tensor([pages - 1 - 17 * i if i % 2 else 3 * i for i in range(table.shape[1])], dtype=torch.int32, device=DEV).view(1, -1)
+    K, V = q.qamw_mxfp4_cache_read(codes, scales, old, d)
+    big = q.qamw_mxfp4_cache_new(pages, heads, page, d)
+    new = far[0, t // page].long() * page + t % page
+    q.qamw_mxfp4_cache_write(K, V, new, *big)
+    again = q.qamw_mxfp4_cache_read(*big, new, d)
+    got = q.qamw_mxfp4_cache_attention(Q, *big, far, lengths, starts, n)
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], K) and torch.equal(again[1], V)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -843,7 +843,7 @@ int32_t qamw_mxfp4_cache_attention(const void* Q, int32_t qdtype, int64_t T, int
   a.out = out, a.odt = odtype, a.o_token = o_token, a.o_head = o_head;
   a.lse = lse;
   a.starts = starts, a.lengths = lengths, a.table = table, a.table_pitch = table_pitch, a.cols = (int)table_cols;
-  a.T = T, a.max_queries = std::min(max_queries, T);
+  a.T = T;
   a.sequences = (int)sequences, a.group = (int)(q_heads / heads);
   a.scale = scale, a.causal = causal != 0;
   a.window = window >= kCacheMaxTokens ? 0 : (int)window;    // no narrower than any sequence

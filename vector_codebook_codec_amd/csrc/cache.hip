@@ -58,7 +58,9 @@ struct CacheRows {
   }
 };
 
-// 8191 tokens of 8 heads of 128 in bf16: 42.7 MB.
+// Bound by memory where there is enough of it: 65536 tokens of 8 heads of 128
+// read to bf16 take 76 us, 4.5 TB/s (99 us with one row a lane: a slot, then
+// the codes, then the store wait for each other).
 template <class In, int kRows>
 __global__ __launch_bounds__(kBlockThreads) void cache_write_kernel(TwoRows in, uint32_t rows, CacheShape c,
                                                                     const int64_t* __restrict__ slots,
@@ -119,8 +121,8 @@ __global__ __launch_bounds__(kBlockThreads) void cache_read_kernel(TwoRows out, 
 // ===========================================================================
 // launchers
 // ===========================================================================
-// 4 rows a lane where that still gives every CU 8 workgroups, keys and values together
-static bool four_rows(const CacheShape& c, int64_t T) { return T * c.heads >= 16ll * kCus * (kBlockThreads / (4 * c.nb)); }
+// 4 rows a lane where that still gives every CU 4 workgroups, keys and values together
+static bool four_rows(const CacheShape& c, int64_t T) { return T * c.heads >= 8ll * kCus * (kBlockThreads / (4 * c.nb)); }
 static dim3 cache_grid(const CacheShape& c, int64_t T) {
   const int64_t per_block = kBlockThreads / (4 * c.nb) * (four_rows(c, T) ? 4 : 1);
   return dim3((unsigned)std::min<int64_t>(tiles_of(T * c.heads, per_block), 1 << 20), 2);

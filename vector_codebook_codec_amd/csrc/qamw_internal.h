@@ -214,7 +214,7 @@ struct AttentionArgs {
   int64_t q_token, q_head, o_token, o_head;       // strides in elements
   const int32_t *starts, *lengths, *table;        // starts: NULL for one query a sequence
   int64_t table_pitch;
-  int64_t T, max_queries;
+  int64_t T;
   int sequences, group, cols;
   float scale;
   int causal, window;                             // window 0: none
