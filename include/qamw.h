@@ -461,8 +461,8 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  *            row is qamw_mxfp4_matmul's
  *   factors  [adapters] float32 or NULL (1)
  * A token's result depends on its own row and adapter alone, whatever the
- * others hold.  X A^T is summed in fp32 and multiplied as two bf16 numbers (16
- * bits) with bf16 B, in fp32 with fp32 B; all of Y is summed in fp32, in a
+ * others hold.  X A^T is summed in fp32 and multiplied with bf16 B as two bf16
+ * numbers (16 bits) for a bf16 Y and three (24 bits) for fp32, in fp32 with fp32 B; all of Y is summed in fp32, in a
  * fixed order, and rounded once.
  *   workspace >= qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank,
  *             xdtype), 256-byte aligned

@@ -134,7 +134,7 @@ __global__ __launch_bounds__(ShrinkTile::kThreads) void adapter_shrink_tile_kern
   }
 }
 
-// U from its parts as two bf16 numbers, 4 elements a lane
+// U from its parts as three bf16 numbers, 4 elements a lane
 __global__ __launch_bounds__(kBlockThreads) void adapter_round_kernel(Adapters ad, int64_t T) {
   const int quads = ad.pitch / 4;
   for (int64_t i = (int64_t)blockIdx.x * kBlockThreads + threadIdx.x; i < T * quads; i += (int64_t)gridDim.x * kBlockThreads) {
@@ -146,12 +146,14 @@ __global__ __launch_bounds__(kBlockThreads) void adapter_round_kernel(Adapters a
     if (ad.factors) u *= ad.factors[use];
 #pragma unroll
     for (int e = 0; e < 4; ++e) u[e] = k + e < ad.rank ? u[e] : 0.0f;
-    const uint32_t h0 = pack_bf16x2(u[0], u[1]), h1 = pack_bf16x2(u[2], u[3]);
     uint16_t* to = ad.u16 + t * ad.pitch + k;
-    *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2*>(to + T * ad.pitch) =
-        make_uint2(pack_bf16x2(u[0] - __uint_as_float(h0 << 16), u[1] - __uint_as_float(h0 & 0xffff0000u)),
-                   pack_bf16x2(u[2] - __uint_as_float(h1 << 16), u[3] - __uint_as_float(h1 & 0xffff0000u)));
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const uint32_t h0 = pack_bf16x2(u[0], u[1]), h1 = pack_bf16x2(u[2], u[3]);
+      *reinterpret_cast<uint2*>(to + n * T * ad.pitch) = make_uint2(h0, h1);
+      u[0] -= __uint_as_float(h0 << 16), u[1] -= __uint_as_float(h0 & 0xffff0000u);
+      u[2] -= __uint_as_float(h1 << 16), u[3] -= __uint_as_float(h1 & 0xffff0000u);
+    }
   }
 }
 
@@ -212,7 +214,7 @@ static AdapterLayout adapter_layout(int64_t T, int64_t N, int64_t d, int32_t dt,
   AdapterLayout p;
   p.parts = adapter_parts(T, d, rank);
   p.second = round_up((size_t)p.parts * T * adapter_pitch(rank) * sizeof(float), 256);
-  p.third = p.second + round_up((size_t)T * adapter_pitch(rank) * 4, 256);
+  p.third = p.second + round_up((size_t)T * adapter_pitch(rank) * 6, 256);
   p.bytes = adapters_in_delta(T, N, dt, rank) ? p.third + (size_t)T * adapter_delta_pitch(N) * 4 : p.third;
   return p;
 }
@@ -281,7 +283,7 @@ int launch_adapter_shrink(const void* X, int32_t xdt, int64_t T, int64_t N, int6
 
 int launch_adapter_expand(int32_t dt, int64_t T, int64_t N, const Adapters& ad, hipStream_t st) {
   const dim3 grid((unsigned)tiles_of(N, kExpandRows), (unsigned)std::min<int64_t>(tiles_of(T, 16), 65535));
-  auto kernel = dt == QAMW_F32 ? adapter_expand_kernel<AdaptersF32> : adapter_expand_kernel<AdaptersBf16>;
+  auto kernel = dt == QAMW_F32 ? adapter_expand_kernel<AdaptersF32> : adapter_expand_kernel<AdaptersBf16x3>;
   hipLaunchKernelGGL(kernel, grid, dim3(kExpandThreads), 0, st, ad, T, N);
   return check_launch("adapter_expand_kernel");
 }

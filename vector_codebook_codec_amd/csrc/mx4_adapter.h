@@ -28,9 +28,9 @@ __device__ __forceinline__ i32x4 load_chunk(const E* row, int64_t j, int64_t d) 
   return __builtin_bit_cast(i32x4, e);
 }
 
-// The adapters' types.  U in bf16 goes as two numbers, so that only the
-// adapters' own rounding is in the result; a step is what one load of 16 bytes
-// a lane covers.
+// The adapters' types.  U in bf16 goes as two numbers (2^-16 of it) where the
+// result is bf16 and as three (2^-24) where it is fp32; a step is what one load
+// of 16 bytes a lane covers.
 struct NoAdapters {
   static constexpr bool kOn = false, kDelta = false;
 };
@@ -39,6 +39,9 @@ struct AdaptersBf16 {
   typedef uint16_t E;
   typedef OpBf16 Op;
   static constexpr int kStep = 32, kTerms = 2;
+};
+struct AdaptersBf16x3 : AdaptersBf16 {
+  static constexpr int kTerms = 3;
 };
 struct AdaptersF32 {
   static constexpr bool kOn = true, kDelta = false;
@@ -107,7 +110,7 @@ __device__ __forceinline__ f32x4 add_mine(bool mine, i32x4 b, const i32x4 (&u)[A
 // the last one again), then added in a fixed order
 template <class Ad>
 struct ChunkOfU {
-  static constexpr int kQuads = Ad::kTerms == 1 ? 1 : 2;
+  static constexpr int kQuads = sizeof(typename Ad::E) == 4 ? 1 : 2;
   f32x4 part[kMostAdapterParts][kQuads];
   __device__ __forceinline__ void load(const Adapters& ad, int64_t t, int64_t T, int k) {
 #pragma unroll
@@ -132,10 +135,13 @@ struct ChunkOfU {
     } else {
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const float x0 = s[n / 2][2 * (n & 1)], x1 = s[n / 2][2 * (n & 1) + 1];
-        const uint32_t h = pack_bf16x2(x0, x1);
-        u[0][n] = (int)h;
-        u[1][n] = (int)pack_bf16x2(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xffff0000u));
+        float x0 = s[n / 2][2 * (n & 1)], x1 = s[n / 2][2 * (n & 1) + 1];
+#pragma unroll
+        for (int i = 0; i < Ad::kTerms; ++i) {
+          const uint32_t h = pack_bf16x2(x0, x1);
+          u[i][n] = (int)h;
+          x0 -= __uint_as_float(h << 16), x1 -= __uint_as_float(h & 0xffff0000u);
+        }
       }
     }
   }
@@ -211,10 +217,10 @@ __device__ __forceinline__ bool add_adapters(f32x4 (&acc)[TM][TN], const Adapter
 // of U for all its tokens and of B for all its channels are copied to LDS (in
 // the order of tile_product.h's operands), one adapter after another; mostly
 // there is one.  Every thread of the workgroup calls it; lds holds kLdsBytes of the tile.
-template <class Tl>
+template <class Ad, class Tl>
 __device__ __forceinline__ void add_adapters_tile(f32x4 (&acc)[Tl::TM][Tl::TN], const Adapters& ad, int64_t m0, int64_t t0, int64_t T,
                                                   int64_t N, char* lds) {
-  static_assert((2 * Tl::BN + Tl::BM) * kStepBytes <= Tl::kLdsBytes, "U and B of 64 ranks");
+  static_assert((Ad::kTerms * Tl::BN + Tl::BM) * kStepBytes <= Tl::kLdsBytes, "U and B of 64 ranks");
   const int lane = threadIdx.x & (kWave - 1), l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave / Tl::WN, wn = wave % Tl::WN;
   const int rows = (int)(N - m0 < Tl::BM ? N - m0 : Tl::BM), tokens = (int)(T - t0 < Tl::BN ? T - t0 : Tl::BN);
@@ -227,18 +233,18 @@ __device__ __forceinline__ void add_adapters_tile(f32x4 (&acc)[Tl::TM][Tl::TN], 
     all[j] = i >= 0 && i < ad.n ? i : INT_MAX;
   }
   adapters_of(idx, ad.index, ad.n, t0 + wn * (Tl::BN / Tl::WN) + l16, T);
-  const __amdgpu_buffer_rsrc_t hi = buffer_of(ad.u16 + t0 * ad.pitch, tokens * pu),
-                               lo = buffer_of(ad.u16 + (T + t0) * ad.pitch, tokens * pu);
   const int crow = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ ((crow >> 1) & 7);
-  char *const lds_u = lds, *const lds_b = lds + 2 * Tl::BN * kStepBytes;
+  char *const lds_u = lds, *const lds_b = lds + Ad::kTerms * Tl::BN * kStepBytes;
   for (int k0 = 0; k0 < ad.rank; k0 += 64) {
     const int k = k0 + 8 * chunk;
     __syncthreads();                               // nobody reads what LDS held
 #pragma unroll
     for (int i = 0; i < Tl::kCopiesB; ++i) {
       const uint32_t at = k < ad.pitch ? (uint32_t)(crow + 8 * Tl::kWaves * i) * pu + 2u * k : kPastEnd;
-      copy16_to_lds(hi, lds_u + (wave + Tl::kWaves * i) * 1024, at, 0);
-      copy16_to_lds(lo, lds_u + Tl::BN * kStepBytes + (wave + Tl::kWaves * i) * 1024, at, 0);
+#pragma unroll
+      for (int n = 0; n < Ad::kTerms; ++n)
+        copy16_to_lds(buffer_of(ad.u16 + (n * T + t0) * ad.pitch, tokens * pu),
+                      lds_u + n * Tl::BN * kStepBytes + (wave + Tl::kWaves * i) * 1024, at, 0);
     }
     AdapterWalk<Tl::BN / kWave, kWave> walk(all);
     bool first = true;
@@ -265,9 +271,11 @@ __device__ __forceinline__ void add_adapters_tile(f32x4 (&acc)[Tl::TM][Tl::TN], 
 #pragma unroll
         for (int j = 0; j < Tl::TN; ++j) {
           const char* at = lds_u + (wn * (Tl::BN / Tl::WN) + 16 * j + l16) * kStepBytes + pos;
-          const i32x4 u[2] = {*reinterpret_cast<const i32x4*>(at), *reinterpret_cast<const i32x4*>(at + Tl::BN * kStepBytes)};
+          i32x4 u[Ad::kTerms];
 #pragma unroll
-          for (int i = 0; i < Tl::TM; ++i) acc[i][j] = add_mine<AdaptersBf16>(idx[j] == use, b[i], u, acc[i][j]);
+          for (int n = 0; n < Ad::kTerms; ++n) u[n] = *reinterpret_cast<const i32x4*>(at + n * Tl::BN * kStepBytes);
+#pragma unroll
+          for (int i = 0; i < Tl::TM; ++i) acc[i][j] = add_mine<Ad>(idx[j] == use, b[i], u, acc[i][j]);
         }
       }
     }

@@ -176,7 +176,7 @@ __global__ __launch_bounds__(Tl::kThreads) void mx4_matmul_kernel(Operand W, Ope
     }
   if (s0 < s1) Tl::run(acc, W, m0, X, n0, kchunks, s0, s1, tile_lds);
   if constexpr (Ad::kOn)
-    if (s0 == 0) add_adapters_tile<Tl>(acc, ad, m0, n0, X.rows, W.rows, tile_lds);
+    if (s0 == 0) add_adapters_tile<Ad, Tl>(acc, ad, m0, n0, X.rows, W.rows, tile_lds);
   if (!split) {
     store_tile<Tl, Out>(Y, ldy, n0, X.rows, m0, W.rows, acc, tile_lds);
     return;
@@ -481,17 +481,18 @@ static int matmul_out(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx,
   const Operand w = {(const char*)wcodes, (int64_t)nb * 16, N, wscales, mx4_scale_bytes(d)};
   const Operand x = {(const char*)xcodes, (int64_t)nb * 16, T, xscales, mx4_scale_bytes(d)};
   const Adapters ad = adapters ? *adapters : Adapters{};
+  typedef std::conditional_t<sizeof(typename Out::T) == 4, AdaptersBf16x3, AdaptersBf16> AdBf16;
   // the fused form reads X by 16-byte loads with 32-bit offsets
   if (T <= kFusedTokens && es == 2 && d % 8 == 0 && aligned16(X) && ldx % 8 == 0 && ldx <= kMaxRowBytes / es) {
     if (xdt == QAMW_F16) return matmul_thin<1, MemF16, Out, true, NoAdapters>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
-    if (adapters) return matmul_thin<1, MemBf16, Out, true, AdaptersBf16>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
+    if (adapters) return matmul_thin<1, MemBf16, Out, true, AdBf16>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
     return matmul_thin<1, MemBf16, Out, true, NoAdapters>(w, x, X, d, ldx, nb, Y, ldy, ad, st);
   }
   const int rc = launch_mx4_quantize(X, xdt, T, d, ldx, xcodes, xscales, nullptr, QAMW_BF16, 0, st);
   if (rc) return rc;
   if (!adapters) return matmul_quantised<Out, NoAdapters>(p, w, x, d, nb, Y, ldy, part, ad, st);
   if (xdt == QAMW_F32) return matmul_quantised<Out, AdaptersF32>(p, w, x, d, nb, Y, ldy, part, ad, st);
-  return matmul_quantised<Out, AdaptersBf16>(p, w, x, d, nb, Y, ldy, part, ad, st);
+  return matmul_quantised<Out, AdBf16>(p, w, x, d, nb, Y, ldy, part, ad, st);
 }
 int launch_mx4_matmul(const void* X, int32_t xdt, int64_t T, int d, int64_t ldx, const uint8_t* wcodes,
                       const uint8_t* wscales, int64_t N, void* Y, int32_t ydt, int64_t ldy, void* ws,

@@ -166,7 +166,7 @@ size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d);
 // Low-rank adapters beside the product (mx4_adapter.h).  U = f_i A_i X has rows
 // of `pitch` elements, the rank rounded up to 32, and lies in the workspace as
 // `parts` fp32 matrices to be added (not yet times f_i), and for the product's
-// tiles also as two bf16 ones.  A and B are 16-byte aligned.
+// tiles also as three bf16 ones.  A and B are 16-byte aligned.
 constexpr int kMostAdapterParts = 4;
 struct Adapters {
   const void* B;
