@@ -1,0 +1,46 @@
+"""GPU tests of the attention cache at the limits of what its header allows:
+more queries than a call names, blocks that the library never writes, weights
+and scores beyond a type's ordinary range.  Needs an MI355X; criteria as in
+test_gpu_cache.py where no other is stated.
+"""
+import numpy as np
+import pytest
+
+from oracle import mxfp4_cache as C
+from test_gpu_cache import DEV, check, host, make, poisoned, q, say, simple  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def on_gpu(*arrays):
+    return [torch.from_numpy(a).to(DEV) for a in arrays]
+
+
+def exact(Q, codes, scales, table, lengths, starts, causal=True, window=0):
+    back = lambda x: x if isinstance(x, np.ndarray) else x.cpu().numpy()  # noqa: E731
+    return C.attention(host(Q), back(codes), back(scales), back(table), back(lengths), back(starts),
+                       float(np.float32(Q.shape[2] ** -0.5)), causal, window)
+
+
+@pytest.mark.parametrize("n", [1, 7, 300])
+@pytest.mark.parametrize("length", [400, 6000])
+def test_starts_of_any_value(q, n, length):
+    """Entries at the ends of 32 bits: the sequences that lie inside are computed, of the buffers around out and lse no
+    other row is written."""
+    say(f"case starts n={n} length={length}")
+    Q, codes, scales, table, lengths, starts = simple(q, n=n, length=length)
+    want = q.qamw_mxfp4_cache_attention(Q, codes, scales, table, lengths, starts, n)
+    low, high = -2 ** 31, 2 ** 31 - 1
+    out, lse = torch.empty(3 * n + 8, *Q.shape[1:], dtype=Q.dtype, device=DEV), torch.empty(3 * n + 8, Q.shape[1], device=DEV)
+    for entries, whole in (([0, n, low, low], 1), ([0, n, 2 * n, low], 2), ([0, n, n + low, low], 1), ([0, low, low + 5, low], 0),
+                           ([high, low, low, low], 0), ([high, high, low, low], 0)):
+        out.fill_(7.0), lse.fill_(9.0)
+        wild = torch.tensor(entries, dtype=torch.int32, device=DEV)
+        q.qamw_mxfp4_cache_attention(Q, codes, scales, table, lengths, wild, n, out=out[4:-4], lse=lse[4:-4])
+        torch.cuda.synchronize()
+        end = 4 + whole * n
+        # [low, low + 5) and the like hold no query; [n, low) and [n + low, low) neither
+        assert torch.equal(out[4:end], want[0][:whole * n]) and torch.equal(lse[4:end], want[1][:whole * n]), entries
+        for rows in (slice(0, 4), slice(end, None)):
+            assert (out[rows] == 7).all() and (lse[rows] == 9).all(), entries

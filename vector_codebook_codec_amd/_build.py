@@ -22,7 +22,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "calibrate.hip", "encode.h
                                                 "cross_entropy.hip", "adapter.hip", "cache.hip", "cache_attention.hip")]
 HEADERS = [os.path.join(CSRC, "qamw_device.h"), os.path.join(CSRC, "qamw_internal.h"),
            os.path.join(CSRC, "tile_product.h"), os.path.join(CSRC, "mx4_device.h"),
-           os.path.join(CSRC, "mx4_adapter.h"),
+           os.path.join(CSRC, "mx4_adapter.h"), os.path.join(CSRC, "cache_spans.h"),
            os.path.join(ROOT, "include", "qamw.h")]
 LIB_PATH = os.path.join(PKG, "libqamw.so")
 ARCH = "gfx950"

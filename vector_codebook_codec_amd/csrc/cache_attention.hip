@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "cache_spans.h"
 #include "mx4_device.h"
 #include "qamw.h"
 #include "qamw_device.h"
@@ -26,26 +27,10 @@ constexpr int kWaveTokens = 32, kTileTokens = kAttnWaves * kWaveTokens;
 constexpr int kMaxSplits = 64;                     // a wavefront joins them, one a lane
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
-// A sequence's queries and cached tokens, whatever the arrays hold: queries
-// stay inside [0, T), tokens inside the page table.
-struct Sequence {
-  int64_t first;                                   // its first query
-  int n, length;
-};
 __device__ __forceinline__ Sequence sequence_of(const AttentionArgs& a, int b) {
-  Sequence s;
-  if (a.starts) {
-    const int64_t s0 = a.starts[b], s1 = a.starts[b + 1];
-    s.first = s0 < 0 ? 0 : s0 > a.T ? a.T : s0;
-    s.n = (int)((s1 > a.T ? a.T : s1) - s.first);
-  } else {
-    s.first = b;
-    s.n = b < a.T ? 1 : 0;
-  }
-  s.n = s.n > 0 ? s.n : 0;
-  const int64_t most = (int64_t)a.cols << a.c.page_shift, len = a.lengths[b];
-  s.length = (int)(len < 0 ? 0 : len > most ? most : len);
-  return s;
+  const int64_t most = (int64_t)a.cols << a.c.page_shift;
+  return a.starts ? clamped_sequence(a.starts[b], a.starts[b + 1], a.T, a.lengths[b], most)
+                  : clamped_sequence(b, b + 1, a.T, a.lengths[b], most);
 }
 // the tokens [lo, hi) that query i of a sequence attends to (hi below lo: none)
 __device__ __forceinline__ int span_end(const AttentionArgs& a, const Sequence& s, int i) {
