@@ -496,8 +496,9 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
  *   Q        [T][q_heads][d]; query heads h q_heads / heads and the following
  *            q_heads / heads - 1 use key head h
  *   starts   [sequences + 1] int32: sequence b's queries are starts[b] to
- *            starts[b + 1] - 1, at most max_queries of them (rows past those
- *            are not computed), its latest tokens; NULL: one query each,
+ *            starts[b + 1] - 1, its latest tokens; of more than max_queries the
+ *            first max_queries are computed, at their own places, and the
+ *            other rows left as they were; NULL: one query each,
  *            sequences = T, max_queries = 1
  *   table    [sequences][table_pitch] int32: the page of tokens [j page, (j +
  *            1) page) in column j < table_cols.  Tokens of a page outside [0,

@@ -44,3 +44,20 @@ def test_starts_of_any_value(q, n, length):
         assert torch.equal(out[4:end], want[0][:whole * n]) and torch.equal(lse[4:end], want[1][:whole * n]), entries
         for rows in (slice(0, 4), slice(end, None)):
             assert (out[rows] == 7).all() and (lse[rows] == 9).all(), entries
+
+
+# 16, 32 and 128 rows a workgroup, in one share of the tokens and in several; the last row asked for is inside a workgroup's
+@pytest.mark.parametrize("n,most,group,d", [(40, 7, 4, 128), (60, 33, 4, 128), (300, 197, 4, 128), (30, 5, 5, 64), (12, 3, 3, 256)])
+@pytest.mark.parametrize("length", [500, 6000])
+def test_queries_past_max_queries_are_left(q, n, most, group, d, length):
+    """Of a sequence with more than max_queries queries the first max_queries are computed, at their own places, and no
+    other row is written."""
+    say(f"case most n={n} most={most} group={group} d={d} length={length}")
+    Q, codes, scales, table, lengths, starts = simple(q, n=n, length=length, group=group, d=d, seqs=2)
+    out, lse = torch.full_like(Q, 7.0), torch.full(Q.shape[:2], 9.0, device=DEV)
+    q.qamw_mxfp4_cache_attention(Q, codes, scales, table, lengths, starts, most, out=out, lse=lse)
+    torch.cuda.synchronize()
+    asked = torch.arange(2 * n) % n < most
+    assert (out.cpu()[~asked] == 7).all() and (lse.cpu()[~asked] == 9).all()
+    want = [x[asked.numpy()] for x in exact(Q, codes, scales, table, lengths, starts)]
+    check(out.cpu()[asked], lse.cpu()[asked], *want, "bf16", "bf16", d, length)

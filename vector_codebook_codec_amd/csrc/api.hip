@@ -845,6 +845,7 @@ int32_t qamw_mxfp4_cache_attention(const void* Q, int32_t qdtype, int64_t T, int
   a.starts = starts, a.lengths = lengths, a.table = table, a.table_pitch = table_pitch, a.cols = (int)table_cols;
   a.T = T;
   a.sequences = (int)sequences, a.group = (int)(q_heads / heads);
+  a.most = (int)std::min(max_queries, T);
   a.scale = scale, a.causal = causal != 0;
   a.window = window >= kCacheMaxTokens ? 0 : (int)window;    // no narrower than any sequence
   return launch_cache_attention(a, p, workspace, (hipStream_t)stream);

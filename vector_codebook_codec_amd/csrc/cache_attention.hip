@@ -32,6 +32,8 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionArgs& a, int b) {
   return a.starts ? clamped_sequence(a.starts[b], a.starts[b + 1], a.T, a.lengths[b], most)
                   : clamped_sequence(b, b + 1, a.T, a.lengths[b], most);
 }
+// query rows of a key head that are computed: those of at most max_queries queries (T group is at most 2^30)
+__device__ __forceinline__ int rows_of(const AttentionArgs& a, const Sequence& s) { return min(s.n, a.most) * a.group; }
 // the tokens [lo, hi) that query i of a sequence attends to (hi below lo: none)
 __device__ __forceinline__ int span_end(const AttentionArgs& a, const Sequence& s, int i) {
   const int end = s.length - s.n + i + 1;
@@ -382,7 +384,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
   const Place at = place_of(a, row_tiles, splits);
   const int h = at.h;
   const Sequence seq = sequence_of(a, at.b);
-  const int rows = (int)min((int64_t)seq.n * a.group, (int64_t)INT32_MAX), r0 = at.tile * 16 * RT, r1 = min(rows, r0 + 16 * RT);
+  const int rows = rows_of(a, seq), r0 = at.tile * 16 * RT, r1 = min(rows, r0 + 16 * RT);
   if (r0 >= rows) return;
   const TileRange range = tile_range(a, seq, r0, r1, splits);
   if (at.share >= range.shares) return;
@@ -644,7 +646,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
   const Place at = place_of(a, row_tiles, splits);
   const int h = at.h;
   const Sequence seq = sequence_of(a, at.b);
-  const int rows = (int)min((int64_t)seq.n * a.group, (int64_t)INT32_MAX), r0 = at.tile * kRows, r1 = min(rows, r0 + kRows);
+  const int rows = rows_of(a, seq), r0 = at.tile * kRows, r1 = min(rows, r0 + kRows);
   if (r0 >= rows) return;
   const TileRange range = tile_range(a, seq, r0, r1, splits);
   if (at.share >= range.shares) return;
@@ -924,11 +926,9 @@ __global__ __launch_bounds__(kAttnThreads) void cache_attention_join_kernel(Atte
   }
   if (b < 0 || b >= a.sequences) return;
   const Sequence seq = sequence_of(a, b);
-  if (query < seq.first || query >= seq.first + seq.n) return;
   const int64_t row = (query - seq.first) * a.group + (head - h * a.group);
-  const int tile = (int)(row / tile_rows), r0 = tile * tile_rows;
-  if (tile >= row_tiles) return;
-  const int r1 = (int)min((int64_t)seq.n * a.group, (int64_t)r0 + tile_rows);
+  if (query < seq.first || row >= rows_of(a, seq)) return;
+  const int tile = (int)(row / tile_rows), r0 = tile * tile_rows, r1 = min(rows_of(a, seq), r0 + tile_rows);
   const TileRange range = tile_range(a, seq, r0, r1, splits);
   if (range.shares <= 1) return;                   // written already
   const int64_t floats = (int64_t)tile_rows * (32 * DB + 2);

@@ -215,7 +215,7 @@ struct AttentionArgs {
   const int32_t *starts, *lengths, *table;        // starts: NULL for one query a sequence
   int64_t table_pitch;
   int64_t T;
-  int sequences, group, cols;
+  int sequences, group, cols, most;               // most: queries of a sequence that are computed
   float scale;
   int causal, window;                             // window 0: none
 };
