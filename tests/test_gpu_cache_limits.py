@@ -61,3 +61,14 @@ def test_queries_past_max_queries_are_left(q, n, most, group, d, length):
     assert (out.cpu()[~asked] == 7).all() and (lse.cpu()[~asked] == 9).all()
     want = [x[asked.numpy()] for x in exact(Q, codes, scales, table, lengths, starts)]
     check(out.cpu()[asked], lse.cpu()[asked], *want, "bf16", "bf16", d, length)
+
+
+@pytest.mark.parametrize("n", [1, 7, 300])
+def test_starts_without_max_queries(q, n):
+    """All of the sequences' queries are computed where the caller names no limit."""
+    say(f"case no limit n={n}")
+    Q, codes, scales, table, lengths, starts = simple(q, n=n, length=400)
+    out, lse = torch.full_like(Q, 7.0), torch.full(Q.shape[:2], 9.0, device=DEV)
+    q.qamw_mxfp4_cache_attention(Q, codes, scales, table, lengths, starts, out=out, lse=lse)
+    torch.cuda.synchronize()
+    check(out, lse, *exact(Q, codes, scales, table, lengths, starts), "bf16", "bf16", 128, 400)

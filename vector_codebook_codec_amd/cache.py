@@ -153,7 +153,7 @@ def qamw_mxfp4_cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torc
 
 
 def qamw_mxfp4_cache_attention(Q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, table: torch.Tensor,
-                               lengths: torch.Tensor, starts: Optional[torch.Tensor] = None, max_queries: int = 1,
+                               lengths: torch.Tensor, starts: Optional[torch.Tensor] = None, max_queries: Optional[int] = None,
                                scale: Optional[float] = None, causal: bool = True, window: int = 0, out_dtype=None,
                                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                                workspace: Optional[torch.Tensor] = None, stream=None):
@@ -161,7 +161,9 @@ def qamw_mxfp4_cache_attention(Q: torch.Tensor, codes: torch.Tensor, scales: tor
 
     table [sequences][columns] int32 names the pages of each sequence, lengths [sequences] int32 its cached tokens, those
     of the queries among them.  Without starts every sequence has one query; with starts [sequences + 1] int32 sequence b
-    has the queries starts[b] to starts[b + 1] - 1, its latest tokens, at most max_queries.  causal: a query sees no token
+    has the queries starts[b] to starts[b + 1] - 1, its latest tokens.  max_queries: as many as any sequence has, which
+    sizes the launch; of a sequence with more the first max_queries are computed.  T if not given (all of them in any
+    case, in a larger launch where there are several sequences).  causal: a query sees no token
     after its own; window > 0: only the latest `window` tokens up to its own.  scale: 1 / sqrt(d) if not given.
     out [T][q_heads][d] of out_dtype (that of Q if not given), lse [T][q_heads] fp32: 0 and -inf for a row that no token
     is left to; rows of queries that belong to no sequence stay as they were (in tensors made here: unset)."""
@@ -176,6 +178,8 @@ def qamw_mxfp4_cache_attention(Q: torch.Tensor, codes: torch.Tensor, scales: tor
     _ints(lengths, "lengths", torch.int32, sequences)
     if starts is not None:
         _ints(starts, "starts", torch.int32, sequences + 1)
+    if max_queries is None:
+        max_queries = 1 if starts is None else max(T, 1)
     if out is None:
         out = _empty_heads(T, q_heads, d, Q.dtype if out_dtype is None else out_dtype, Q.device, stream)
     odt, oT, oheads, od, ot, oh = _head_rows(out, "out")
