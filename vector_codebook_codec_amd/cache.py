@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _ODT, _dev, _empty, _raw_stream, _workspace
+from .codec import _ODT, _dev, _empty, _one_device, _raw_stream, _workspace
 
 __all__ = [
     "qamw_mxfp4_cache_attention",
@@ -89,16 +89,6 @@ def _ints(t: torch.Tensor, name: str, dtype, *shape):
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}")
-
-
-def _one_device(first: torch.Tensor, **others) -> None:
-    """Every tensor of a call lies on one device, the current one, whose stream the call goes to."""
-    index = first.get_device()
-    if index != torch.cuda.current_device():
-        raise ValueError("tensors must lie on the current device")
-    for name, t in others.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} lies on another device")
 
 
 def _empty_heads(T: int, heads: int, d: int, dtype, device, stream) -> torch.Tensor:

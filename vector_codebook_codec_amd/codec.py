@@ -35,7 +35,7 @@ def _stream(stream) -> int:
 
 
 def _dev(t: torch.Tensor, name: str) -> None:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
 
 
@@ -80,6 +80,16 @@ def _codebook(codebook: torch.Tensor) -> int:
     if codebook.dtype != torch.float32 or codebook.dim() != 2 or codebook.shape[1] != 2 or not codebook.is_contiguous():
         raise ValueError("codebook must be a contiguous K x 2 float32 tensor")
     return codebook.shape[0]
+
+
+def _one_device(first: torch.Tensor, **others) -> None:
+    """Every tensor of a call lies on one device, the current one, whose stream the call goes to."""
+    index = first.get_device()
+    if index != torch.cuda.current_device():
+        raise ValueError("tensors must lie on the current device")
+    for name, t in others.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} lies on another device")
 
 
 def _empty(shape, dtype, device, stream=None) -> torch.Tensor:

@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .codec import _ODT, _WDT, _dev, _empty, _matrix, _raw_stream, _workspace
+from .codec import _ODT, _WDT, _dev, _empty, _matrix, _one_device, _raw_stream, _workspace
 
 __all__ = [
     "qamw_mxfp4_adapter_matmul",
@@ -177,6 +177,7 @@ def qamw_mxfp4_adapter_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torc
         workspace = _workspace(lib.qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank, xdt), X.device, stream)
     else:
         _dev(workspace, "workspace")
+    _one_device(X, codes=codes, scales=scales, A=A, B=B, index=index, factors=factors, out=out, workspace=workspace)
     status = lib.qamw_mxfp4_adapter_matmul(
         X.data_ptr(), xdt, T, d, ldx, codes.data_ptr(), scales.data_ptr(), N, A.data_ptr(), B.data_ptr(), n, rank,
         index.data_ptr(), None if factors is None else factors.data_ptr(), out.data_ptr(), ydt, ldy, workspace.data_ptr(),
