@@ -513,10 +513,8 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
  *   out      [T][q_heads][d] of odtype, lse [T][q_heads] float32 or NULL.  Rows
  *            of queries that belong to no sequence are left as they were.
  *   scale    positive and finite
- * Arithmetic: keys and values as they stand, queries too (bf16 ones of many
- * rows and heads of 65 to 128 elements as two 8-bit numbers that hold them to
- * 2^-22 of a row's largest element, their scores then to 2^-16 of scale sum |q
- * k|; fp32 ones to 24 bits).  Products are summed in fp32, statistics are fp32.
+ * Arithmetic: keys and values as they stand, queries too (fp32 ones to 24
+ * bits).  Products are summed in fp32, statistics are fp32.
  * Each weight is rounded once before it multiplies a value: by up to 2^-16 of
  * itself, 2^-24 where Q or out is fp32, and for bf16 and many rows 2^-11 of
  * itself or 2^-25 of the row's largest.  out is rounded once.  Sums have a

@@ -72,3 +72,22 @@ def test_starts_without_max_queries(q, n):
     q.qamw_mxfp4_cache_attention(Q, codes, scales, table, lengths, starts, out=out, lse=lse)
     torch.cuda.synchronize()
     check(out, lse, *exact(Q, codes, scales, table, lengths, starts), "bf16", "bf16", 128, 400)
+
+
+@pytest.mark.parametrize("d,spread", [(128, 1.0), (128, 4.0), (96, 2.0), (72, 1.0)])
+def test_lse_does_not_depend_on_how_many_queries(q, d, spread):
+    """The same queries in a call of few rows a key head and in one of many.  Both sum exact products of bf16 queries and
+    4-bit keys in fp32, so in the root mean square either's lse is as far from 64 bits as the other's: within twice, and
+    half a step of fp32 at the result's size."""
+    say(f"case lse d={d} spread={spread}")
+    n, few, group, length, page = 300, 90, 4, 900, 32
+    rng, codes, scales, table, lengths, starts = make(q, 91, [(n, length)], 2, d, page, spread=spread)
+    Q = torch.from_numpy(rng.standard_normal((n, 2 * group, d)).astype(np.float32)).to(torch.bfloat16)
+    want = exact(Q, codes, scales, table, lengths, starts)
+    many = q.qamw_mxfp4_cache_attention(Q.to(DEV), codes, scales, *on_gpu(table, lengths, starts), n)
+    late = q.qamw_mxfp4_cache_attention(Q[-few:].to(DEV), codes, scales, *on_gpu(table, lengths, np.array([0, few], dtype=np.int32)), few)
+    torch.cuda.synchronize()
+    rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
+    off_many, off_few = rms(host(many[1])[-few:] - want[1][-few:]), rms(host(late[1]) - want[1][-few:])
+    say(f"  lse off by {off_many:.3g} in a call of many rows, {off_few:.3g} in one of few")
+    assert off_many <= 2 * off_few + 2.0 ** -24 * rms(want[1][-few:])

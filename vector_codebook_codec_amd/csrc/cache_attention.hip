@@ -604,18 +604,14 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 // Many query rows: each of the 4 wavefronts has 32 rows of its own and goes
 // through all tokens of the workgroup's share.  For bf16 queries and output
 // and heads of up to 128 elements.
-//   * Keys are multiplied as they lie in the cache, on the scaled matrix
-//     instructions, 128 elements at once: nothing of them is decoded.  A query
-//     goes as two 8-bit numbers of 4 significant bits each, a row with one
-//     power of two: the row's largest element is in [128, 256), the first
-//     number holds it to within half a step, the second (with a scale 2^-5 of
-//     the first's) the rest: a bf16 number's 8 bits exactly, down to elements
-//     2^-14 of the largest, and below that 2^-22 of the largest.
-//     Such an instruction takes 33 cycles, half the time of the four bf16 ones
-//     it stands for (measured); two take as long as they.  It sums 128 products cut off
-//     below 24 bits of the largest: scores are within 2^-16 of scale sum |q k|
-//     (lse of rows around 10: off by 6e-6 in the root mean square, 2.6e-4 at
-//     most seen, against 3e-7 from bf16 products).
+//   * Keys are decoded to bf16 in every wavefront, straight into the registers
+//     of the product, for its 32 rows: scores are sums in fp32 of exact
+//     products, the same as in the kernel above, whichever of the two takes a
+//     call.  (As they lie in the cache, on the scaled matrix instructions with
+//     a query as two 8-bit numbers, they took 596 us of the case below and now
+//     648, but such an instruction sums 128 products cut off below 24 bits of
+//     the largest: lse was off by 4e-5 in the root mean square where scores go
+//     to 25, now 9e-7.)
 //   * Values are decoded once a workgroup, each wavefront 32 tokens, into LDS
 //     in the layout of the matrix operand, two tiles in turn: one barrier a
 //     tile.  They and the weights go in fp16, which rounds a weight by at most
@@ -623,10 +619,10 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 //     it); the results of a workgroup that met a value beyond fp16 (or a
 //     NaN block) are dropped, and a second launch does its work with values in
 //     bf16 and the weights as two bf16 numbers.
-// 4 chunks of 2048 queries behind up to 8192 tokens, 32/8 heads of 128: 595 us, 1.0
-// PFLOP/s.  Matrix instructions are 40 % busy; the other vector instructions
-// of 32 x 32 scores, 130 with 16 exponentials, take about as long as the 24
-// matrix ones, two wavefronts a SIMD overlap them in part.
+// 4 chunks of 2048 queries behind up to 8192 tokens, 32/8 heads of 128: 648 us, 918
+// TFLOP/s.  The other vector instructions of 32 x 32 scores, 16 exponentials
+// and the decoding of the keys among them, take about as long as the 32 matrix
+// ones; two wavefronts a SIMD overlap them in part.
 // ---------------------------------------------------------------------------
 template <bool kF16>
 __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(AttentionArgs a, int row_tiles, int splits,
@@ -659,39 +655,21 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
   const int lo_any = span_begin(a, seq, first), hi_any = w0 < rows ? span_end(a, seq, last) : 0;
   const int lo_all = span_begin(a, seq, last), hi_all = span_end(a, seq, first);
 
-  // ---- queries as 8-bit numbers; the instruction's lane group g holds elements 16 g .. and 64 + 16 g ..
-  i32x8 q[RT][2];
-  int q_scale[RT], row_lo[RT], row_hi[RT];
+  // ---- queries: lane group g holds block g of a row's elements, as it does of the keys
+  i32x4 q[RT][DB];
+  int row_lo[RT], row_hi[RT];
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int row = min(w0 + 16 * j + l16, rows - 1), i = row / a.group, head = h * a.group + row % a.group;
     row_lo[j] = span_begin(a, seq, i), row_hi[j] = span_end(a, seq, i);
     const void* p = row_at(a.Q, QAMW_BF16, (seq.first + i) * a.q_token + head * a.q_head);
-    float x[4][8];
-    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      load8<MemBf16>((const uint16_t*)p, (k & 2) * 32 + 16 * g + (k & 1) * 8, a.c.d, x[k]);
+    for (int w = 0; w < DB; ++w) {
+      float x[8];
+      load8<MemBf16>((const uint16_t*)p, 8 * (g * DB + w), a.c.d, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[k][e]) & 0x7fffffffu);
+      for (int e = 0; e < 4; ++e) q[j][w][e] = (int)pack_bf16x2(x[2 * e], x[2 * e + 1]);
     }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-    const int exponent = max((int)(top >> 23), 13);           // 255: infinities and NaN, the row becomes NaN
-    q_scale[j] = exponent == 255 ? 255 : exponent - 7;
-    const float unit = __uint_as_float((uint32_t)(127 + 134 - min(exponent, 254)) << 23);        // 2^7 over the largest's binade
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float y0 = x[k][e] * unit, y1 = x[k][e + 1] * unit, y2 = x[k][e + 2] * unit, y3 = x[k][e + 3] * unit;
-        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y0, y1, 0, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, hi, true);
-        const f32x2_t b0 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, false), b1 = __builtin_amdgcn_cvt_pk_f32_fp8(hi, true);
-        int lo = __builtin_amdgcn_cvt_pk_fp8_f32((y0 - b0.x) * 32.0f, (y1 - b0.y) * 32.0f, 0, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32((y2 - b1.x) * 32.0f, (y3 - b1.y) * 32.0f, lo, true);
-        q[j][0][2 * k + e / 4] = hi, q[j][1][2 * k + e / 4] = lo;
-      }
   }
 
   f32x4 o[RT][MT] = {};
@@ -770,14 +748,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
   const float c = a.scale * kLog2e;
   auto multiply_keys = [&](const Keys& r, f32x4 (&s)[RT][2]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 1; n >= 0; --n)                   // the rest of the queries first
+    for (int w = 0; w < DB; ++w)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const i32x8 kf = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w, 0, 0, 0, 0};
+        uint32_t kd[4];
+        decode_16<false>((uint32_t)r.c[i][w], __uint_as_float((uint32_t)r.s[i] << 23), kd);
+        const i32x4 kf = {(int)kd[0], (int)kd[1], (int)kd[2], (int)kd[3]};
 #pragma unroll
-        for (int j = 0; j < RT; ++j)
-          s[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(kf, q[j][n], n ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : s[j][i], 4,
-                                                                     0, 0, r.s[i], 0, n ? q_scale[j] - 5 : q_scale[j]);
+        for (int j = 0; j < RT; ++j) s[j][i] = mfma_bf16(kf, q[j][w], w ? s[j][i] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
       }
   };
   auto compute = [&](int k, int sub, f32x4 (&s)[RT][2], const bool (&ok)[2]) __attribute__((always_inline)) {
@@ -978,10 +956,10 @@ static int dtype_terms(int32_t dt) { return dt == QAMW_F32 ? 3 : dt == QAMW_F16 
 
 // Fragments of 16 query rows a workgroup takes.  8 is the kernel of many rows:
 // heads of 65 to 128 elements in bf16, from 1024 rows a key head on, where its
-// 128 rows a workgroup leave enough workgroups (8 sequences of 4096 tokens, 32/8
-// heads of 128: 1024 rows 134 us against 152 us with 2 fragments, 512 rows 99 us
-// and 91 us; heads of 64 fill half its instructions: 8192 rows 1080 us and 1050
-// us).  2 fragments share the decoding (256 rows 52 us, with 1 fragment 60 us;
+// 128 rows a workgroup leave enough workgroups (8 sequences of up to 4096 tokens,
+// 32/8 heads of 128: 1024 rows 145 us against 168 us with 2 fragments, 512 rows
+// 104 us and 100 us; heads of 64 would fill half its
+// instructions).  2 fragments share the decoding (256 rows 52 us, with 1 fragment 60 us;
 // 64 rows 28 and 30 us, in one sequence of 8192 tokens 19 and 17 us); their
 // registers allow them for bf16 and heads of up to 128 elements.
 static int row_fragments(int64_t rows, int db, int terms) {
