@@ -517,7 +517,7 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
  * bits).  Products are summed in fp32, statistics are fp32.
  * Each weight is rounded once before it multiplies a value: by up to 2^-16 of
  * itself, 2^-24 where Q or out is fp32, and for bf16 and many rows 2^-11 of
- * itself or 2^-25 of the row's largest.  out is rounded once.  Sums have a
+ * itself or 2^-32 of the row's largest.  out is rounded once.  Sums have a
  * fixed order for given sizes.  Scores beyond fp32's range are not supported.
  *   T q_heads / heads and table_cols page up to 2^30
  *   workspace >= qamw_mxfp4_cache_attention_workspace_bytes(..., table_cols

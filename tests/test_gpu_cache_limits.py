@@ -91,3 +91,29 @@ def test_lse_does_not_depend_on_how_many_queries(q, d, spread):
     off_many, off_few = rms(host(many[1])[-few:] - want[1][-few:]), rms(host(late[1]) - want[1][-few:])
     say(f"  lse off by {off_many:.3g} in a call of many rows, {off_few:.3g} in one of few")
     assert off_many <= 2 * off_few + 2.0 ** -24 * rms(want[1][-few:])
+
+
+@pytest.mark.parametrize("n", [4, 60, 200])
+@pytest.mark.parametrize("score", [14.0, 16.0, 17.625])
+def test_weights_far_below_the_largest(q, n, score):
+    """Of every 128 tokens one, whose value is 0, has a score that far above the others': out is what they add up to.
+    Their weights, exp(-score) of the largest, are 2^-20.2 to 2^-25.5 and round to within 2^-16 of themselves, or with
+    many rows in bf16 to 2^-32 of the largest; then comes the output's half step.  The scores are exact, the sums of
+    1024 terms within 1032 2^-24."""
+    say(f"case weights n={n} score={score}")
+    group, d, page, length = 4, 128, 64, 1024
+    K, V = torch.zeros(length, 1, d), torch.ones(length, 1, d)
+    K[::128, 0, 0], V[::128] = 1.0, 0.0
+    table = torch.arange(length // page, dtype=torch.int32).view(1, -1)
+    codes, scales = q.qamw_mxfp4_cache_new(length // page, 1, page, d)
+    q.qamw_mxfp4_cache_write(K.to(DEV), V.to(DEV), torch.arange(length, device=DEV), codes, scales)
+    Q = torch.zeros(n, group, d, dtype=torch.bfloat16)
+    Q[:, :, 0] = score
+    dev = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([length], [0, n])]
+    got, lse = q.qamw_mxfp4_cache_attention(Q.to(DEV), codes, scales, table.to(DEV), dev[0], dev[1], n, scale=1.0, causal=False)
+    torch.cuda.synchronize()
+    weight = np.exp(-score)
+    want = 127 * weight / (1 + 127 * weight)
+    off = np.abs(host(got) / want - 1).max()
+    assert off <= max(2.0 ** -16, 2.0 ** -32 / weight if n * group > 768 else 0) + 2.0 ** -8 + 2 * 1032 * 2.0 ** -24 + 1e-6, off
+    assert np.abs(host(lse) - (score + np.log(8) + np.log1p(127 * weight))).max() <= 1032 * 2.0 ** -24 + 17 * 2.0 ** -23

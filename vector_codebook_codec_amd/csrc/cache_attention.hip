@@ -252,10 +252,11 @@ __device__ __forceinline__ void decode_values(const uint32_t (&vc)[8], const uin
 }
 
 // The reference of the exponentials follows the maximum only when a score
-// exceeds it by 2^8 (weights are then up to 256, far from any limit): nearly
-// all tiles go without an exchange between lanes and without a pass over the
-// sums.  Scores are those of 8 tokens of one row in every lane.
-template <int RT, int MT>
+// exceeds it by 2^8 more than it is meant to (weights are then up to 256 times
+// as large): nearly all tiles go without an exchange between lanes and without
+// a pass over the sums.  It is put kLift powers of two below the maximum.
+// Scores are those of 8 tokens of one row in every lane.
+template <int kLift, int RT, int MT>
 __device__ __forceinline__ void follow_maximum(const f32x4 (&s)[RT][2], float c, float (&m)[RT], float (&l)[RT],
                                                f32x4 (&o)[RT][MT]) {
   float top[RT];
@@ -265,13 +266,13 @@ __device__ __forceinline__ void follow_maximum(const f32x4 (&s)[RT][2], float c,
     const float x = fmaxf(fmaxf(s[j][0][0], s[j][0][1]), fmaxf(s[j][0][2], s[j][0][3])),
                 y = fmaxf(fmaxf(s[j][1][0], s[j][1][1]), fmaxf(s[j][1][2], s[j][1][3]));
     top[j] = fmaxf(x, y) * c;
-    above |= top[j] > m[j] + 8.0f;
+    above |= top[j] > m[j] + (8.0f + kLift);
   }
   if (!__ballot(above)) return;
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     float x = fmaxf(top[j], __shfl_xor(top[j], 16));
-    x = fmaxf(m[j], fmaxf(x, __shfl_xor(x, 32)));
+    x = fmaxf(m[j], fmaxf(x, __shfl_xor(x, 32)) - kLift);
     const float f = __builtin_amdgcn_exp2f(m[j] - x);
     m[j] = x;
     l[j] *= f;
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
           for (int e = 0; e < 4; ++e)
             if (!sees(j, i, e)) s[j][i][e] = -INFINITY;
     }
-    follow_maximum<RT, MT>(s, c, m, l, o);
+    follow_maximum<0, RT, MT>(s, c, m, l, o);
     i32x4 p[RT][kWeightTerms];
     weights<RT>(s, c, m, l, [&](int j, int at, float p0, float p1) __attribute__((always_inline)) {
       uint32_t t[kWeightTerms];
@@ -615,10 +616,13 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 //   * Values are decoded once a workgroup, each wavefront 32 tokens, into LDS
 //     in the layout of the matrix operand, two tiles in turn: one barrier a
 //     tile.  They and the weights go in fp16, which rounds a weight by at most
-//     2^-11 of itself (2^-25 of the row's reference where it is below 2^-14 of
-//     it); the results of a workgroup that met a value beyond fp16 (or a
-//     NaN block) are dropped, and a second launch does its work with values in
-//     bf16 and the weights as two bf16 numbers.
+//     2^-11 of itself.  Its range is used whole: weights are up to 2^15 and a
+//     row's largest at least 2^7, so that small ones are held to within 2^-25,
+//     2^-32 of the largest, and 2^17 tokens that far down lose 2^-15 of the row
+//     (with a largest weight of 1, those below 2^-25 of it vanished).  The
+//     results of a workgroup that met a value beyond fp16 (or a NaN block) are
+//     dropped, and a second launch does its work with values in bf16 and the
+//     weights as two bf16 numbers.
 // 4 chunks of 2048 queries behind up to 8192 tokens, 32/8 heads of 128: 648 us, 918
 // TFLOP/s.  The other vector instructions of 32 x 32 scores, 16 exponentials
 // and the decoding of the keys among them, take about as long as the 32 matrix
@@ -775,7 +779,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(
           for (int e = 0; e < 4; ++e)
             if (!sees(j, i, e)) s[j][i][e] = -INFINITY;
     }
-    follow_maximum<RT, MT>(s, c, m, l, o);
+    follow_maximum<kF16 ? 7 : 0, RT, MT>(s, c, m, l, o);
     // the values are on their way from LDS while the weights are made
     constexpr int kWeightTerms = kF16 ? 1 : 2;
     i32x4 v[MT], p[RT][kWeightTerms];
