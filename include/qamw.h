@@ -509,7 +509,9 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
  *     length - queries + i for a sequence's query i, with window > 0 also t >
  *     place - window;   out = sum_t softmax(z)_t v_t,   lse = log sum_t exp z_t
  *   A row whose masks leave nothing gives 0 and -infinity.  What masked slots
- *   hold does not matter (NaN blocks too).
+ *   hold does not matter (NaN blocks too).  Values with scale codes 253 and
+ *   254, which qamw_mxfp4_cache_write never makes, may be beyond fp32's range:
+ *   rows that see their token hold infinities or NaN there, others do not.
  *   out      [T][q_heads][d] of odtype, lse [T][q_heads] float32 or NULL.  Rows
  *            of queries that belong to no sequence are left as they were.
  *   scale    positive and finite

@@ -117,3 +117,34 @@ def test_weights_far_below_the_largest(q, n, score):
     off = np.abs(host(got) / want - 1).max()
     assert off <= max(2.0 ** -16, 2.0 ** -32 / weight if n * group > 768 else 0) + 2.0 ** -8 + 2 * 1032 * 2.0 ** -24 + 1e-6, off
     assert np.abs(host(lse) - (score + np.log(8) + np.log1p(127 * weight))).max() <= 1032 * 2.0 ** -24 + 17 * 2.0 ** -23
+
+
+LARGE = [  # queries, length, group, d: one query, a few rows, many rows
+    (1, 700, 4, 128), (6, 260, 3, 80), (40, 400, 4, 128), (9, 200, 2, 256), (40, 300, 2, 64), (230, 600, 4, 128),
+]
+
+
+@pytest.mark.parametrize("n,length,group,d", LARGE)
+@pytest.mark.parametrize("code", [253, 254])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_values_past_every_number(q, n, length, group, d, code, dt):
+    """Values with scale codes 253 and 254 stay with the rows that see their token: the other rows, and the other blocks of
+    these, are as if the blocks were NaN, which the oracle gives to the same rows."""
+    if dt == "f32" and n > 40:
+        pytest.skip("many rows are bf16")
+    say(f"case code {code} n={n} length={length} group={group} d={d} {dt}")
+    last = length - 1 if n == 1 else length - 2
+    where = {0: [(1, last, 0, 0), (1, length - n // 2 - 1, 1, (d - 1) // 32), (1, 2, 0, 1)], 1: [(1, last, 1, 1)], 2: [(1, 5, 0, 0)]}
+    rng, codes, scales, table, lengths, starts = poisoned(q, 79, [(n, length)] * 3, 2, d, 16, lambda b: where[b], code)
+    Q = torch.from_numpy(rng.standard_normal((3 * n, 2 * group, d)).astype(np.float32)).to(torch.bfloat16 if dt == "bf16" else torch.float32)
+    nan = scales.cpu().numpy()
+    nan[(nan == 253) | (nan == 254)] = 255
+    for window in (0, max(1, n // 3)):
+        got, lse = q.qamw_mxfp4_cache_attention(Q.to(DEV), codes, scales, *on_gpu(table, lengths, starts), n, window=window)
+        torch.cuda.synchronize()
+        with np.errstate(invalid="ignore"):
+            want = exact(Q, codes, nan, table, lengths, starts, window=window)
+            seen = torch.from_numpy(np.isnan(want[0]))
+            check(got.cpu().masked_fill(seen, float("nan")), lse, *want, dt, dt, d, length)
+            # a block's largest elements are infinite in fp32, in some of the rows that see them at least
+            assert not torch.isfinite(got.cpu()[seen]).all(), (code, window)

@@ -88,6 +88,10 @@ __device__ __forceinline__ void decode_16(uint32_t w, float s, uint32_t (&o)[4])
     o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
   }
 }
+// Scale codes of NaN blocks, and 253 and 254, which no write makes: they stand
+// for values that neither bf16 nor fp32 holds all of, and their infinities
+// would reach rows that must not see the token, by a weight of 0.
+__device__ __forceinline__ bool is_nan_code(uint32_t code) { return code > 252u; }
 // Scale codes whose blocks fp16 holds as normal numbers: 2^e / 2 to 6 2^e with e
 // in [-13, 13]; a code of 0 with the zeros that have it.
 __device__ __forceinline__ bool f16_holds(uint32_t code) { return code - 114u <= 26u || code == 0u; }
@@ -214,7 +218,7 @@ __device__ __forceinline__ i32x4 take_nan(uint32_t (&vc)[8], uint32_t (&vw)[8][R
   i32x4 bad = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (vc[e] == 255u) {
+    if (is_nan_code(vc[e])) {
       bad[e / 2] |= 0x3f80 << (16 * (e & 1));
       vc[e] = 0;
 #pragma unroll
@@ -226,7 +230,7 @@ __device__ __forceinline__ bool any_nan(const uint32_t (&vc)[8]) {
   uint32_t most = vc[0];
 #pragma unroll
   for (int e = 1; e < 8; ++e) most = max(most, vc[e]);
-  return __ballot(most == 255u) != 0;
+  return __ballot(is_nan_code(most)) != 0;
 }
 // The operands V^T, in fp16 or bf16: put(t, f) for the t-th element of every
 // lane.  Pairs of tokens are put together by byte permutes.
