@@ -461,9 +461,10 @@ int32_t qamw_mxfp4_matmul(const void* X, int32_t xdtype, int64_t T, int64_t d, i
  *            row is qamw_mxfp4_matmul's
  *   factors  [adapters] float32 or NULL (1)
  * A token's result depends on its own row and adapter alone, whatever the
- * others hold.  X A^T is summed in fp32 and multiplied with bf16 B as two bf16
- * numbers (16 bits) for a bf16 Y and three (24 bits) for fp32, in fp32 with fp32 B; all of Y is summed in fp32, in a
- * fixed order, and rounded once.
+ * others hold; infinities in its adapter or factor make it infinite or NaN.  X
+ * A^T is summed in fp32 and multiplied with bf16 B as two bf16 numbers (16
+ * bits) for a bf16 Y and three (24 bits) for fp32, in fp32 with fp32 B; all of
+ * Y is summed in fp32, in a fixed order, and rounded once.
  *   workspace >= qamw_mxfp4_adapter_matmul_workspace_bytes(T, N, d, rank,
  *             xdtype), 256-byte aligned
  */
@@ -520,7 +521,9 @@ int32_t qamw_mxfp4_adapter_matmul(const void* X, int32_t xdtype, int64_t T, int6
  * Each weight is rounded once before it multiplies a value: by up to 2^-16 of
  * itself, 2^-24 where Q or out is fp32, and for bf16 and many rows 2^-11 of
  * itself or 2^-32 of the row's largest.  out is rounded once.  Sums have a
- * fixed order for given sizes.  Scores beyond fp32's range are not supported.
+ * fixed order for given sizes.  Scores beyond fp32's range are not
+ * supported, nor values whose sum over the tokens, times 2^8, is; values below
+ * 2^-124 may count as 0.
  *   T q_heads / heads and table_cols page up to 2^30
  *   workspace >= qamw_mxfp4_cache_attention_workspace_bytes(..., table_cols
  *             page, ...), 256-byte aligned; may be NULL where that is 0

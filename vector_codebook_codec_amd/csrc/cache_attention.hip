@@ -93,7 +93,8 @@ __device__ __forceinline__ void decode_16(uint32_t w, float s, uint32_t (&o)[4])
 // would reach rows that must not see the token, by a weight of 0.
 __device__ __forceinline__ bool is_nan_code(uint32_t code) { return code > 252u; }
 // Scale codes whose blocks fp16 holds as normal numbers: 2^e / 2 to 6 2^e with e
-// in [-13, 13]; a code of 0 with the zeros that have it.
+// in [-13, 13]; a code of 0 for the zeros that have it (of values below 2^-124,
+// which have it too, fp16 makes zeros).
 __device__ __forceinline__ bool f16_holds(uint32_t code) { return code - 114u <= 26u || code == 0u; }
 // x as a sum of kTerms bf16 numbers: 8, 16 or 24 bits of it
 template <int kTerms>
@@ -340,9 +341,9 @@ __device__ __forceinline__ void store_elements(int32_t dt, void* row, int j, int
   }
 }
 
-// floats of a share's partial result: sums, then the reference exponent and the sum of weights of each row
 // wavefronts a SIMD that the registers are to allow
 template <int DB, int RT, int kTerms> constexpr int attn_waves() { return DB == 8 || RT == 2 || kTerms == 3 ? 2 : 3; }
+// floats of a share's partial result: sums, then the reference exponent and the sum of weights of each row
 template <int DB, int RT> constexpr int part_floats() { return 16 * RT * (32 * DB + 2); }
 
 // ---------------------------------------------------------------------------

@@ -456,14 +456,17 @@ static int matmul_quantised(const Mx4Plan& p, const Operand& W, const Operand& X
                             float* part, const Adapters& ad, hipStream_t st) {
   if (X.rows <= 16) return matmul_thin<1, MemBf16, Out, false, Ad>(W, X, nullptr, d, 0, kchunks, Y, ldy, ad, st);
   if (thin_pays(X.rows, W.rows)) return matmul_thin<2, MemBf16, Out, false, Ad>(W, X, nullptr, d, 0, kchunks, Y, ldy, ad, st);
-  if constexpr (Ad::kOn) {
-    if (adapters_in_delta(X.rows, W.rows, std::is_same<Ad, AdaptersF32>::value ? QAMW_F32 : QAMW_BF16, ad.rank)) {
-      const int rc = launch_adapter_expand(std::is_same<Ad, AdaptersF32>::value ? QAMW_F32 : QAMW_BF16, X.rows, W.rows, ad, st);
-      return rc ? rc : matmul_to<Out, AdapterDelta>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
-    }
+  auto by_matrix = [&](int32_t dt) {
+    const int rc = launch_adapter_expand(dt, X.rows, W.rows, ad, st);
+    return rc ? rc : matmul_to<Out, AdapterDelta>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
+  };
+  if constexpr (std::is_same<Ad, AdaptersF32>::value) {
+    return by_matrix(QAMW_F32);                    // adapters_in_delta is true of fp32 here
+  } else {
+    if constexpr (Ad::kOn)
+      if (adapters_in_delta(X.rows, W.rows, QAMW_BF16, ad.rank)) return by_matrix(QAMW_BF16);
+    return matmul_to<Out, Ad>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
   }
-  if constexpr (std::is_same<Ad, AdaptersF32>::value) return QAMW_EINVAL;       // always as a matrix
-  else return matmul_to<Out, Ad>(p.tiles, W, X, kchunks, Y, ldy, part, ad, st);
 }
 
 // Up to this many tokens of 16 bits the thin product quantises X itself: each
