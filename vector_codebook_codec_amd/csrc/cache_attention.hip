@@ -628,10 +628,12 @@ __global__ __launch_bounds__(kAttnThreads, (attn_waves<DB, RT, kTerms>())) void 
 //     results of a workgroup that met a value beyond fp16 (or a NaN block) are
 //     dropped, and a second launch does its work with values in bf16 and the
 //     weights as two bf16 numbers.
-// 4 chunks of 2048 queries behind up to 8192 tokens, 32/8 heads of 128: 648 us, 918
-// TFLOP/s.  The other vector instructions of 32 x 32 scores, 16 exponentials
-// and the decoding of the keys among them, take about as long as the 32 matrix
-// ones; two wavefronts a SIMD overlap them in part.
+// 4 chunks of 2048 queries behind up to 8192 tokens, 32/8 heads of 128: 648 us, 920
+// TFLOP/s; 1.47 ms where every workgroup meets a value that fp16 does not hold
+// (values times 2^-12).  Matrix instructions are 39 % busy; the other vector
+// instructions of 32 x 32 scores, 156 with 16 exponentials and the decoding of
+// the keys, take about as long as the 32 matrix ones, two wavefronts a SIMD
+// overlap them in part.
 // ---------------------------------------------------------------------------
 template <bool kF16>
 __global__ __launch_bounds__(kAttnThreads, 2) void cache_attention_chunk_kernel(AttentionArgs a, int row_tiles, int splits,

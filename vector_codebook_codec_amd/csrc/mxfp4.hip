@@ -402,9 +402,12 @@ size_t mx4_matmul_workspace_bytes(int64_t T, int64_t N, int64_t d) { return mx4_
 // tokens one after another: nothing where the tokens of a prompt share one,
 // but too much in a batch whose tokens have one each (48 of rank 16 beside 4096
 // x 4096: 31 us in the product's 64 workgroups).  Past 256 tokens the matrix in
-// fp32 costs more than that (4095 x 13824: 226 MB written and read).  Tiles
-// copy B by 16-byte chunks and hold U in bf16: fp32, and ranks of no whole
-// chunks unless launch_adapter_shrink fills them up, go by the matrix.
+// fp32 costs more than that where tokens share adapters (4095 x 13824: 226 MB
+// written and read; 256 and 257 tokens of one adapter, 4096 x 4096: 32 us and 26
+// us), and much less where they do not (of 64 adapters in turn: 48 us and 361
+// us), which the host does not know.  Tiles copy B by 16-byte chunks and hold U
+// in bf16: fp32, and ranks of no whole chunks unless launch_adapter_shrink fills
+// them up, go by the matrix.
 bool adapters_in_delta(int64_t T, int64_t N, int32_t dt, int64_t rank) {
   return !thin_pays(T, N) && (T <= 256 || dt == QAMW_F32 || rank % 8 != 0);
 }
