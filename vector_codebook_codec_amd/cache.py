@@ -152,8 +152,8 @@ def qamw_mxfp4_cache_attention(Q: torch.Tensor, codes: torch.Tensor, scales: tor
     table [sequences][columns] int32 names the pages of each sequence, lengths [sequences] int32 its cached tokens, those
     of the queries among them.  Without starts every sequence has one query; with starts [sequences + 1] int32 sequence b
     has the queries starts[b] to starts[b + 1] - 1, its latest tokens.  max_queries: as many as any sequence has, which
-    sizes the launch; of a sequence with more the first max_queries are computed.  T if not given (all of them in any
-    case, in a larger launch where there are several sequences).  causal: a query sees no token
+    sizes the launch; of a sequence with more the first max_queries are computed.  T if not given: all of them in any
+    case, in a launch and a workspace larger by the number of sequences.  causal: a query sees no token
     after its own; window > 0: only the latest `window` tokens up to its own.  scale: 1 / sqrt(d) if not given.
     out [T][q_heads][d] of out_dtype (that of Q if not given), lse [T][q_heads] fp32: 0 and -inf for a row that no token
     is left to; rows of queries that belong to no sequence stay as they were (in tensors made here: unset)."""

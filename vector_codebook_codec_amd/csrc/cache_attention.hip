@@ -969,10 +969,10 @@ static int dtype_terms(int32_t dt) { return dt == QAMW_F32 ? 3 : dt == QAMW_F16 
 // heads of 65 to 128 elements in bf16, from 1024 rows a key head on, where its
 // 128 rows a workgroup leave enough workgroups (8 sequences of up to 4096 tokens,
 // 32/8 heads of 128: 1024 rows 145 us against 168 us with 2 fragments, 512 rows
-// 104 us and 100 us; heads of 64 would fill half its
-// instructions).  2 fragments share the decoding (256 rows 52 us, with 1 fragment 60 us;
-// 64 rows 28 and 30 us, in one sequence of 8192 tokens 19 and 17 us); their
-// registers allow them for bf16 and heads of up to 128 elements.
+// 104 us and 100 us; heads of 64 would fill half its instructions).  2 fragments
+// share the decoding (256 rows 52 us, with 1 fragment 60 us; 64 rows 28 and 30
+// us, in one sequence of 8192 tokens 19 and 17 us); their registers allow them
+// for bf16 and heads of up to 128 elements.
 static int row_fragments(int64_t rows, int db, int terms) {
   if (terms > 1 || db == 8 || rows <= 128) return 1;
   return db == 4 && rows > 768 ? 8 : 2;

@@ -147,7 +147,7 @@ def qamw_mxfp4_adapter_matmul(X: torch.Tensor, codes: torch.Tensor, scales: torc
     product of qamw_mxfp4_matmul with every request's own low-rank adapter.
 
     X [T][d], A [adapters][rank][d] and B [adapters][N][rank] fp32 or bf16 alike, A and B contiguous; index [T] int32,
-    outside [0, adapters) for a token without one; factors [adapters] fp32 (1 if not given)."""
+    outside [0, adapters) for a token without one; factors [adapters] fp32 (1 if not given).  All lie on the current device."""
     T, d, ldx = _matrix(X, "X")
     xdt = _WDT.get(X.dtype)
     if xdt is None:
